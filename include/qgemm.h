@@ -215,6 +215,113 @@ int qgemm_w4a8_acc(int M, int K, int N, const int8_t* qa, const void* Bp, int32_
 /* Workspace bytes qgemm_w4a8_acc needs (0 for invalid sizes). */
 size_t qgemm_w4a8_acc_workspace_bytes(int M, int K);
 
+/* ---------------------------------------------------------------- 4-bit floating point */
+
+/* Microscaled 4-bit floating point, the operand formats that the tensor cores multiply as they are:
+ * both sides of the product below are 4 bits wide, with a scale per short block of K.
+ *   A code is an e2m1 value: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (bit 3 is the sign); byte j of
+ *   a row holds values 2j (low half) and 2j + 1. A row of K values is K/2 bytes.
+ *   QGEMM_FMT_MXFP4: one e8m0 scale byte s per 32 values, 2^(s - 127), 255 = NaN (OCP Microscaling
+ *     Formats v1.0). Quantization: 2^(floor(log2 max|x|) - 2), at least 2^-127.
+ *   QGEMM_FMT_NVFP4: one e4m3 scale byte per 16 values and one float32 scale g per row. Quantization:
+ *     g = 2^(floor(log2 max|row|) - 10) (exponent kept in [-116, 117]; 1 for a row of zeros), block
+ *     scale s = the e4m3 value nearest to (max|block| / g) / 6, the quotient in float32.
+ *   Codes are the e2m1 values nearest to x / scale, ties to the even code, saturating at 6 (zeros
+ *   where an NVFP4 block scale rounds to 0); zeros keep x's sign. Every decision is exact, so the codes
+ *   are bit-identical to any IEEE evaluation of these definitions. An infinity or NaN in a block
+ *   (MXFP4) or row (NVFP4) makes that block's scale, or g, NaN.
+ * Block scales have two layouts:
+ *   QGEMM_SCALES_ROWS (activations): row m's scales at m * pitch, pitch = K / block rounded up to 16
+ *     bytes, so that a row may sit anywhere in a ragged batch;
+ *   QGEMM_SCALES_TILED (weights): tiles of 128 rows x 4 scales, 512 bytes each, [ceil(rows / 128)][ceil(K /
+ *     block / 4)]; the four scales of row r of a tile lie at 16 (r % 32) + 4 (r / 32), the order in which
+ *     the tensor cores take them.
+ *   Bytes past the last row or scale are written as zeros. */
+#define QGEMM_FMT_F16 1   /* 16-bit operands of the grouped product (same numbers as the types) */
+#define QGEMM_FMT_BF16 2
+#define QGEMM_FMT_MXFP4 3
+#define QGEMM_FMT_NVFP4 4
+#define QGEMM_SCALES_ROWS 0
+#define QGEMM_SCALES_TILED 1
+
+/* Bytes of the codes and of the block scales of `rows` rows of K values (0 for invalid arguments;
+ * K must be a multiple of 64). Both are multiples of 16 per row (ROWS) or per weight (TILED), so the
+ * weights of several experts can follow one another. */
+size_t qgemm_fp4_codes_bytes(int rows, int K);
+size_t qgemm_fp4_scales_bytes(int rows, int K, int fmt, int layout);
+
+/* Quantize M rows of K values. X: [x_rows][ldx] in x_dtype, rows 16-byte aligned (ldx >= K values).
+ * rows: NULL (row m is X's row m; x_rows >= M), or int32 [M] with X's row for each output row, so that
+ * one call gathers and quantizes each expert's tokens; an entry outside [0, x_rows) gives a row of
+ * zeros. Writes codes [M][K/2], scales (qgemm_fp4_scales_bytes) and, for NVFP4, row_scale float32
+ * [M] (MXFP4: unused, may be NULL). */
+int qgemm_fp4_quant(int M, int K, const void* X, int x_dtype, long long ldx, int x_rows, const int32_t* rows, int fmt,
+                    int layout, void* codes, void* scales, float* row_scale, void* stream);
+
+/* The inverse: Y [M][K] in y_dtype = code * block scale * row scale (row_scale NULL: 1), rounded once. */
+int qgemm_fp4_dequant(int M, int K, int fmt, int layout, const void* codes, const void* scales, const float* row_scale,
+                      void* Y, int y_dtype, void* stream);
+
+/* Quantize and pack a float32 weight W [K][N] (as qgemm_pack takes it): codes Bp [N][K/2], scales Bs
+ * (TILED) and, for NVFP4, b_scale float32 [N] (MXFP4: unused, may be NULL); each channel is a row. */
+int qgemm_fp4_pack(const float* W, int K, int N, int fmt, void* Bp, void* Bs, float* b_scale, void* stream);
+
+/* SwiGLU, an activation of the two products below only: channels 2j and 2j + 1 are the gate and the
+ * up projection of output channel j, silu(gate) * up (each after its bias); C then has N / 2 columns. */
+#define QGEMM_ACT_SWIGLU 4
+
+/* The linear layer with both operands in 4 bits:
+ *   C[m][n] = act(a_scale[m] * b_scale[n] * sum_k A[m][k] B[n][k] + bias[n]) + residual[m][n]
+ * in float32, rounded once to c_dtype, where A and B are codes times block scales. fmt: MXFP4 or NVFP4.
+ *   A: codes [M][K/2], As: scales (ROWS), a_scale: float32 [M] or NULL for 1 (NVFP4: the row scales);
+ *   Bp: codes [N][K/2], Bs: scales (TILED), b_scale: float32 [N] or NULL for 1;
+ *   bias: float32 [N] or NULL; act: QGEMM_ACT_* (SwiGLU: N even); residual: C's shape and type, or NULL;
+ *   it may be C itself, but must not overlap C in any other way. K % 64 == 0; M and N are any.
+ * All pointers 16-byte aligned. No workspace: results depend on the shape and the inputs alone. */
+int qgemm_fp4_run(int M, int K, int N, int fmt, const void* A, const void* As, const float* a_scale, const void* Bp,
+                  const void* Bs, const float* b_scale, const float* bias, int act, const void* residual, void* C,
+                  int c_dtype, void* stream);
+
+/* ---------------------------------------------------------------- mixture of experts */
+
+#define QGEMM_MAX_EXPERTS 1024
+#define QGEMM_MAX_TOPK 32
+
+/* Routing: each of T tokens chooses the k experts of its k largest logits (ties: the lowest expert),
+ * and the chosen (token, choice) pairs are put in order of expert, then token, then choice.
+ *   logits: [T][ld] in dtype, ld >= E. A logit of -inf or NaN is never chosen.
+ *   expert int32 [T][k]: the chosen experts, largest logit first; -1 where fewer than k can be chosen.
+ *   weight float32 [T][k]: softmax over the E logits (renorm = 0) or over the chosen ones (renorm = 1);
+ *     0 beside expert -1. Infinite logits share the weight.
+ *   slot int32 [T][k]: the pair's position in expert order (-1 beside expert -1).
+ *   row int32 [T * k]: the token at each position (-1 past the last pair).
+ *   offsets int32 [E + 1]: expert e's pairs are positions offsets[e] .. offsets[e + 1] - 1.
+ * T may be 0 (offsets are then zeros). 1 <= k <= E, E <= QGEMM_MAX_EXPERTS, k <= QGEMM_MAX_TOPK. The order
+ * depends on the inputs alone. workspace: qgemm_moe_route_workspace_bytes (0 for a few tokens). */
+int qgemm_moe_route(int T, int E, int k, const void* logits, int dtype, long long ld, int renorm, int32_t* expert,
+                    float* weight, int32_t* slot, int32_t* row, int32_t* offsets, void* workspace, size_t workspace_bytes,
+                    void* stream);
+size_t qgemm_moe_route_workspace_bytes(int T, int E, int k);
+
+/* The experts' linear layers over ragged groups of rows: for row m of expert e (offsets[e] <= m <
+ * offsets[e + 1]), C[m][n] = act(a_scale[m] * b_scale[e][n] * sum_k A[m][k] B[e][n][k] + bias[e][n]).
+ *   fmt: QGEMM_FMT_F16 / BF16 (A [T][K] and Bp [E][N][K] in that type; As and Bs unused), or MXFP4 / NVFP4 (A
+ *     and Bp codes, As ROWS scales, Bs the experts' TILED scales one after another, each of
+ *     qgemm_fp4_scales_bytes(N, K, fmt, QGEMM_SCALES_TILED) bytes).
+ *   offsets: int32 [E + 1] on the device, nondecreasing (qgemm_moe_route's); a group may be empty, and rows
+ *     outside [offsets[0], offsets[E]) are neither read nor written in C. Entries are held to [0, T].
+ *   a_scale [T], b_scale [E][N], bias [E][N]: float32 or NULL. act, C, c_dtype, K, N: as qgemm_fp4_run.
+ * T is the rows that A and C hold; the host never reads the offsets. E <= QGEMM_MAX_EXPERTS. */
+int qgemm_grouped_run(int T, int E, int K, int N, int fmt, const int32_t* offsets, const void* A, const void* As,
+                      const float* a_scale, const void* Bp, const void* Bs, const float* b_scale, const float* bias, int act,
+                      void* C, int c_dtype, void* stream);
+
+/* Each token's weighted sum of its experts' rows: out[t] = sum_j weight[t][j] * Y[slot[t][j]] + residual[t], in
+ * float32 in the order of j, rounded once to out_dtype. Y: [R][N] in y_dtype; a slot outside [0, R) adds
+ * nothing. residual: [T][N] in out_dtype or NULL; it may be out itself. */
+int qgemm_moe_combine(int T, int k, int N, int R, const void* Y, int y_dtype, const int32_t* slot, const float* weight,
+                      const void* residual, void* out, int out_dtype, void* stream);
+
 /* ---------------------------------------------------------------- no-allocation variant */
 
 /* Size of the library's own scratch buffer used by qgemm_run_noalloc (4 MiB). */
@@ -314,8 +421,8 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
 
 /* QGEMM_OPT_FAULT_INJECT (default 0, or the value of the environment variable QGEMM_FAULT_INJECT
  * when the library loads). Host-side fault injection: when n > 0, the n-th compute call from now
- * (qgemm_pack, qgemm_run, qgemm_run_fused, qgemm_run_noalloc, qgemm_act_quant, qgemm_w4a8_acc)
- * passes its argument checks and then returns QGEMM_ERR_CUDA with the detail "simulated launch
+ * (qgemm_pack, qgemm_run, qgemm_run_fused, qgemm_run_noalloc, qgemm_act_quant, qgemm_w4a8_acc, the
+ * qgemm_fp4_*, qgemm_grouped_run and qgemm_moe_* calls) passes its argument checks and then returns QGEMM_ERR_CUDA with the detail "simulated launch
  * failure" instead of launching, as a failed launch would; the count then stays 0. No GPU fault is
  * involved. For testing callers' error handling. Process-wide. */
 #define QGEMM_OPT_FAULT_INJECT 6

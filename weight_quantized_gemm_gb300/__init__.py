@@ -17,6 +17,9 @@ __all__ = [
     "qgemm_run", "qgemm_act_quant", "qgemm_w4a8_acc", "qgemm_w4a8_acc_workspace_bytes", "qgemm_status", "qgemm_error_string", "qgemm_last_error",
     "qgemm_set_option", "qgemm_get_option", "OPT_LAUNCH_OVERLAP", "OPT_DECODE_MAX_M", "OPT_SPLIT_K", "OPT_WAIT_LIMIT_US", "OPT_DEBUG_STALL", "OPT_FAULT_INJECT", "qgemm_run_fused", "qgemm_save", "qgemm_load_info", "qgemm_load", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU_TANH", "qgemm_run_noalloc", "NOALLOC_SCRATCH_BYTES", "qgemm_run_fused_quant",
     "qgemm_fused_quant_workspace_bytes", "qgemm_run_w4a8_codes", "qgemm_w4a8_codes_workspace_bytes",
+    "qgemm_fp4_codes_bytes", "qgemm_fp4_scales_bytes", "qgemm_fp4_quant", "qgemm_fp4_dequant", "qgemm_fp4_pack", "qgemm_fp4_run",
+    "qgemm_moe_route", "qgemm_moe_route_workspace_bytes", "qgemm_grouped_run", "qgemm_moe_combine",
+    "FMT_F16", "FMT_BF16", "FMT_MXFP4", "FMT_NVFP4", "SCALES_ROWS", "SCALES_TILED", "ACT_SWIGLU", "MAX_EXPERTS", "MAX_TOPK",
     "MODE_FLOAT", "MODE_INT4", "MODE_INT8", "MODE_W4A8", "F32", "F16", "BF16", "LIB_PATH",
 ]
 
@@ -30,6 +33,10 @@ OPT_FAULT_INJECT = 6
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU_TANH = 0, 1, 2, 3
 NOALLOC_SCRATCH_BYTES = 4 << 20
 F32, F16, BF16 = 0, 1, 2
+FMT_F16, FMT_BF16, FMT_MXFP4, FMT_NVFP4 = 1, 2, 3, 4
+SCALES_ROWS, SCALES_TILED = 0, 1
+ACT_SWIGLU = 4
+MAX_EXPERTS, MAX_TOPK = 1024, 32
 OK = 0
 ERRORS = {-1: "QGEMM_ERR_ARG", -2: "QGEMM_ERR_UNSUPPORTED", -3: "QGEMM_ERR_ALIGN", -4: "QGEMM_ERR_WORKSPACE",
           -5: "QGEMM_ERR_CUDA", -6: "QGEMM_ERR_TIMEOUT", -7: "QGEMM_ERR_IO"}
@@ -38,7 +45,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 _lib = None
 
 # exported symbol -> (argtypes, restype)
-_P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _SZ, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
 SIGNATURES = {
     "qgemm_packed_bytes": ([_I, _I, _I, _I], _SZ),
     "qgemm_table_bytes": ([_I, _I, _I, _I], _SZ),
@@ -58,6 +65,16 @@ SIGNATURES = {
     "qgemm_save": ([ctypes.c_char_p, _I, _I, _I, _I, _I, _P, _P, _I, _P], _I),
     "qgemm_load_info": ([ctypes.c_char_p] + [ctypes.POINTER(ctypes.c_int)] * 5, _I),
     "qgemm_load": ([ctypes.c_char_p, _P, _SZ, _P, _SZ, _I, _P], _I),
+    "qgemm_fp4_codes_bytes": ([_I, _I], _SZ),
+    "qgemm_fp4_scales_bytes": ([_I, _I, _I, _I], _SZ),
+    "qgemm_fp4_quant": ([_I, _I, _P, _I, _LL, _I, _P, _I, _I, _P, _P, _P, _P], _I),
+    "qgemm_fp4_dequant": ([_I, _I, _I, _I, _P, _P, _P, _P, _I, _P], _I),
+    "qgemm_fp4_pack": ([_P, _I, _I, _I, _P, _P, _P, _P], _I),
+    "qgemm_fp4_run": ([_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _P], _I),
+    "qgemm_moe_route": ([_I, _I, _I, _P, _I, _LL, _I, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "qgemm_moe_route_workspace_bytes": ([_I, _I, _I], _SZ),
+    "qgemm_grouped_run": ([_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _P], _I),
+    "qgemm_moe_combine": ([_I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _I, _P], _I),
     "qgemm_set_option": ([_I, _I], _I),
     "qgemm_get_option": ([_I], _I),
     "qgemm_error_string": ([_I], ctypes.c_char_p),
@@ -232,6 +249,70 @@ def qgemm_w4a8_acc(M: int, K: int, N: int, qa, Bp, acc, workspace=None, workspac
         workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().qgemm_w4a8_acc(M, K, N, _ptr(qa), _ptr(Bp), _ptr(acc), _ptr(workspace), workspace_bytes,
                                  _stream(stream)), "qgemm_w4a8_acc")
+
+
+# ---------------------------------------------------------------- 4-bit floating point
+def qgemm_fp4_codes_bytes(rows: int, K: int) -> int:
+    return load().qgemm_fp4_codes_bytes(rows, K)
+
+
+def qgemm_fp4_scales_bytes(rows: int, K: int, fmt: int, layout: int) -> int:
+    return load().qgemm_fp4_scales_bytes(rows, K, fmt, layout)
+
+
+def qgemm_fp4_quant(M: int, K: int, X, x_dtype: int, ldx: int, x_rows: int, rows, fmt: int, layout: int, codes, scales,
+                    row_scale=None, stream=None) -> None:
+    """Quantizes M rows of X (row m, or X's row rows[m]) to 4-bit codes and block scales (see qgemm.h)."""
+    _check(load().qgemm_fp4_quant(M, K, _ptr(X), x_dtype, ldx, x_rows, _ptr(rows), fmt, layout, _ptr(codes),
+                                  _ptr(scales), _ptr(row_scale), _stream(stream)), "qgemm_fp4_quant")
+
+
+def qgemm_fp4_dequant(M: int, K: int, fmt: int, layout: int, codes, scales, row_scale, Y, y_dtype: int,
+                      stream=None) -> None:
+    _check(load().qgemm_fp4_dequant(M, K, fmt, layout, _ptr(codes), _ptr(scales), _ptr(row_scale), _ptr(Y), y_dtype,
+                                    _stream(stream)), "qgemm_fp4_dequant")
+
+
+def qgemm_fp4_pack(W, K: int, N: int, fmt: int, Bp, Bs, b_scale=None, stream=None) -> None:
+    _check(load().qgemm_fp4_pack(_ptr(W), K, N, fmt, _ptr(Bp), _ptr(Bs), _ptr(b_scale), _stream(stream)),
+           "qgemm_fp4_pack")
+
+
+def qgemm_fp4_run(M: int, K: int, N: int, fmt: int, A, As, a_scale, Bp, Bs, b_scale, bias, act: int, residual, C,
+                  c_dtype: int, stream=None) -> None:
+    """C = act(a_scale * b_scale * (A x B^T) + bias) + residual, both operands in 4 bits (see qgemm.h)."""
+    _check(load().qgemm_fp4_run(M, K, N, fmt, _ptr(A), _ptr(As), _ptr(a_scale), _ptr(Bp), _ptr(Bs), _ptr(b_scale),
+                                _ptr(bias), act, _ptr(residual), _ptr(C), c_dtype, _stream(stream)), "qgemm_fp4_run")
+
+
+# ---------------------------------------------------------------- mixture of experts
+def qgemm_moe_route_workspace_bytes(T: int, E: int, k: int) -> int:
+    return load().qgemm_moe_route_workspace_bytes(T, E, k)
+
+
+def qgemm_moe_route(T: int, E: int, k: int, logits, dtype: int, ld: int, renorm: int, expert, weight, slot, row,
+                    offsets, workspace=None, workspace_bytes: int | None = None, stream=None) -> None:
+    """Top-k experts and weights of each token, and the expert-sorted order of the pairs (see qgemm.h)."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().qgemm_moe_route(T, E, k, _ptr(logits), dtype, ld, renorm, _ptr(expert), _ptr(weight), _ptr(slot),
+                                  _ptr(row), _ptr(offsets), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "qgemm_moe_route")
+
+
+def qgemm_grouped_run(T: int, E: int, K: int, N: int, fmt: int, offsets, A, As, a_scale, Bp, Bs, b_scale, bias,
+                      act: int, C, c_dtype: int, stream=None) -> None:
+    """The experts' layers over the row groups given by offsets, a device tensor (see qgemm.h)."""
+    _check(load().qgemm_grouped_run(T, E, K, N, fmt, _ptr(offsets), _ptr(A), _ptr(As), _ptr(a_scale), _ptr(Bp),
+                                    _ptr(Bs), _ptr(b_scale), _ptr(bias), act, _ptr(C), c_dtype, _stream(stream)),
+           "qgemm_grouped_run")
+
+
+def qgemm_moe_combine(T: int, k: int, N: int, R: int, Y, y_dtype: int, slot, weight, residual, out, out_dtype: int,
+                      stream=None) -> None:
+    """out[t] = sum_j weight[t][j] * Y[slot[t][j]] + residual[t] (see qgemm.h)."""
+    _check(load().qgemm_moe_combine(T, k, N, R, _ptr(Y), y_dtype, _ptr(slot), _ptr(weight), _ptr(residual), _ptr(out),
+                                    out_dtype, _stream(stream)), "qgemm_moe_combine")
 
 
 def qgemm_status(stream=None) -> int:

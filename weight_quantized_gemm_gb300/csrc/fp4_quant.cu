@@ -1,0 +1,389 @@
+// Microscaled 4-bit quantization (activation rows and [K][N] weights) and its inverse.
+//
+// Formulas and formats: fp4.cuh and include/qgemm.h. All three kernels move each input and output
+// byte once, so HBM bounds them; a thread takes 16 consecutive values of a row (one NVFP4 block, half
+// an MXFP4 block, whose two halves are neighbouring lanes), which makes 8 bytes of codes.
+#include "fp4.cuh"
+
+namespace qg {
+namespace {
+
+using namespace fp4;
+
+constexpr int kUnit = 16;   // values per thread
+
+// The 16 values of unit u of a row, as stored.
+template <int DT>
+struct Raw {
+    static constexpr int kVecs = DT == DT_F32 ? 4 : 2;
+    uint4 v[kVecs];
+    __device__ __forceinline__ void load(const void* row, int u) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (size_t)u * kUnit * (DT == DT_F32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = __ldg(p + i);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void to_float(float (&x)[kUnit]) const {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+        if constexpr (DT == DT_F32) {
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) x[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kUnit / 2; ++i) {
+                if constexpr (DT == DT_F16) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(w + i));
+                    x[2 * i] = f.x;
+                    x[2 * i + 1] = f.y;
+                } else {
+                    x[2 * i] = __uint_as_float(w[i] << 16);
+                    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                }
+            }
+        }
+    }
+    // bits of the largest |x| as float32 (an infinity or NaN is larger than any number)
+    __device__ __forceinline__ uint32_t top() const {
+        float x[kUnit];
+        to_float(x);
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) t = max(t, abs_bits(x[i]));
+        return t;
+    }
+};
+
+// Codes of one NVFP4 block of row-scaled values y: the e2m1 value nearest to y / s. The quotient
+// must land on a tie exactly where y does: for float32 input that is the correctly rounded
+// quotient. 16-bit input (at most 11 significant bits) is either on a tie or at least 2^-13 away
+// from it (ties are 0.25 and more), so y * (1 / s), wrong by a few 2^-23, is rounded to a multiple
+// of 2^-16 by adding and subtracting 192, which puts it back on the tie or keeps it off.
+template <int DT>
+__device__ __forceinline__ uint2 nv_codes(float (&y)[kUnit], float s) {
+    const float r = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+        float q;
+        if constexpr (DT == DT_F32) q = s > 0.f ? __fdiv_rn(y[i], s) : 0.f;
+        else q = __fsub_rn(__fmaf_rn(y[i], r, 192.f), 192.f);
+        y[i] = copysignf(q, y[i]);
+    }
+    return make_uint2(pack8(y), pack8(y + 8));
+}
+
+struct QuantArgs {
+    int M, K;
+    const void* X;
+    long long ldx_bytes;
+    int x_rows;
+    const int32_t* rows;      // source row of each output row, or none
+    int layout, pitch, ktiles;
+    int rows_out, units_out;  // rows and units that have scale bytes (padding included)
+    uint8_t* codes;
+    uint8_t* scales;
+    float* row_scale;
+};
+
+__device__ __forceinline__ size_t scale_index(const QuantArgs& a, int m, int j) {
+    return a.layout == SC_ROWS ? (size_t)m * a.pitch + j : tiled_index(m, j, a.ktiles);
+}
+// Row m's values (null: a row of zeros: past the end, or gathered from outside X).
+__device__ __forceinline__ const uint8_t* source_row(const QuantArgs& a, int m) {
+    if (m >= a.M) return nullptr;
+    const int r = a.rows ? __ldg(a.rows + m) : m;
+    return r >= 0 && r < a.x_rows ? static_cast<const uint8_t*>(a.X) + (long long)r * a.ldx_bytes : nullptr;
+}
+
+// MXFP4: every block is by itself. Block: 32 units (512 values) x 8 rows.
+template <int DT>
+__global__ void __launch_bounds__(256) mx_quant_kernel(const QuantArgs a) {
+    const int u = blockIdx.y * 32 + threadIdx.x, m = blockIdx.x * 8 + threadIdx.y;
+    if (m >= a.rows_out) return;               // whole warps: a warp is 32 units of one row
+    const bool in = m < a.M && u < a.K / kUnit;
+    const uint8_t* row = in ? source_row(a, m) : nullptr;
+    Raw<DT> raw;
+    if (row) raw.load(row, u);
+    else raw.zero();
+    uint32_t top = raw.top();
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    float mul;
+    const uint32_t byte = mx_scale(top, &mul);
+    if (in) {
+        float x[kUnit];
+        raw.to_float(x);
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) x[i] = mul != 0.f ? x[i] * mul : 0.f;
+        reinterpret_cast<uint2*>(a.codes)[(size_t)m * (a.K / kUnit) + u] = make_uint2(pack8(x), pack8(x + 8));
+    }
+    if ((u & 1) == 0 && u < a.units_out) a.scales[scale_index(a, m, u >> 1)] = in ? (uint8_t)byte : (uint8_t)0;
+}
+
+// NVFP4: one thread block per row, which it reads once while up to kKeep units a thread stay in
+// registers (rows of up to 16384 values; longer ones are read again for the codes).
+constexpr int kNvThreads = 256;
+template <int DT>
+__global__ void __launch_bounds__(kNvThreads) nv_quant_kernel(const QuantArgs a) {
+    constexpr int kKeep = DT == DT_F32 ? 2 : 4;
+    __shared__ uint32_t s_top[kNvThreads / 32];
+    const int m = blockIdx.x, units = a.K / kUnit, step = blockDim.x;
+    const uint8_t* row = source_row(a, m);
+    Raw<DT> keep[kKeep];
+    uint32_t top = 0;
+    if (row) {
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) {
+            const int u = threadIdx.x + i * step;
+            if (u < units) {
+                keep[i].load(row, u);
+                top = max(top, keep[i].top());
+            }
+        }
+        for (int u = threadIdx.x + kKeep * step; u < units; u += step) {
+            Raw<DT> raw;
+            raw.load(row, u);
+            top = max(top, raw.top());
+        }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+    for (int w = 0; w < step / 32; ++w) top = max(top, s_top[w]);
+    float mul;
+    const float g = nv_row_scale(top, &mul);
+    if (threadIdx.x == 0 && m < a.M) a.row_scale[m] = g;
+    auto emit = [&](const Raw<DT>& raw, int u) {
+        float y[kUnit];
+        raw.to_float(y);
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+            y[i] = mul != 0.f ? y[i] * mul : 0.f;
+            t = max(t, abs_bits(y[i]));
+        }
+        float s;
+        a.scales[scale_index(a, m, u)] = (uint8_t)nv_scale(t, &s);
+        reinterpret_cast<uint2*>(a.codes)[(size_t)m * units + u] = nv_codes<DT>(y, s);
+    };
+    if (m < a.M) {
+        if (row) {
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                const int u = threadIdx.x + i * step;
+                if (u < units) emit(keep[i], u);
+            }
+            for (int u = threadIdx.x + kKeep * step; u < units; u += step) {
+                Raw<DT> raw;
+                raw.load(row, u);
+                emit(raw, u);
+            }
+        } else {
+            for (int u = threadIdx.x; u < units; u += step) {
+                a.scales[scale_index(a, m, u)] = 0;
+                reinterpret_cast<uint2*>(a.codes)[(size_t)m * units + u] = make_uint2(0, 0);
+            }
+        }
+    }
+    for (int u = threadIdx.x + (m < a.M ? units : 0); u < a.units_out; u += step) a.scales[scale_index(a, m, u)] = 0;
+}
+
+// The inverse: y = code * block scale * row scale, rounded once to y's type.
+struct DequantArgs {
+    int M, K;
+    int layout, pitch, ktiles;
+    const uint8_t* codes;
+    const uint8_t* scales;
+    const float* row_scale;
+    void* Y;
+};
+template <int FMT, int DT>
+__global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantArgs a) {
+    const int units = a.K / kUnit;
+    const int u = blockIdx.y * 32 + threadIdx.x, m = blockIdx.x * 8 + threadIdx.y;
+    if (m >= a.M || u >= units) return;
+    const uint2 c = __ldg(reinterpret_cast<const uint2*>(a.codes) + (size_t)m * units + u);
+    const int j = FMT == GF_MXFP4 ? u >> 1 : u;
+    const uint32_t byte = __ldg(a.scales + (a.layout == SC_ROWS ? (size_t)m * a.pitch + j : tiled_index(m, j, a.ktiles)));
+    const float s = FMT == GF_MXFP4 ? mx_scale_value(byte) : nv_scale_value(byte);
+    const float g = a.row_scale ? __ldg(a.row_scale + m) : 1.f;
+    float y[kUnit];
+    unpack8(c.x, y);
+    unpack8(c.y, y + 8);
+    uint32_t w[DT == DT_F32 ? 16 : 8];
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) y[i] = y[i] * s * g;
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) w[i] = __float_as_uint(y[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kUnit / 2; ++i) {
+            if constexpr (DT == DT_F16) {
+                const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    }
+    constexpr int kVecs = Raw<DT>::kVecs;
+    uint4* out = static_cast<uint4*>(a.Y) + ((size_t)m * units + u) * kVecs;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// A float32 weight [K][N] to codes [N][K/2] with TILED scales: 32 channels x 64 of K at a time
+// through shared memory (reads along N, writes along K); 128 threads, four units a channel. One
+// thread block per 32 channels runs through K; NVFP4 runs through it twice, first for the channels'
+// largest |w|. Offline work, so it is kept simple.
+struct PackArgs {
+    const float* W;
+    int K, N, ktiles;
+    uint8_t* codes;
+    uint8_t* scales;
+    float* row_scale;
+};
+template <int FMT>
+__global__ void __launch_bounds__(128) fp4_pack_kernel(const PackArgs a) {
+    __shared__ float s_w[64][33];
+    const int n0 = blockIdx.x * 32, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int n = n0 + (int)(threadIdx.x >> 2), g = threadIdx.x & 3;   // this thread's channel and unit
+    const int units = a.K / kUnit;
+    auto fill = [&](int k0) {
+        __syncthreads();
+        for (int k = ty; k < 64; k += 4) s_w[k][tx] = n0 + tx < a.N ? a.W[(size_t)(k0 + k) * a.N + n0 + tx] : 0.f;
+        __syncthreads();
+    };
+    float x[kUnit], mul = 1.f;
+    auto take = [&]() {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+            x[i] = s_w[g * kUnit + i][threadIdx.x >> 2];
+            t = max(t, abs_bits(x[i]));
+        }
+        return t;
+    };
+    if constexpr (FMT == GF_NVFP4) {
+        uint32_t top = 0;
+        for (int k0 = 0; k0 < a.K; k0 += 64) {
+            fill(k0);
+            top = max(top, take());
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float gs = nv_row_scale(top, &mul);
+        if (g == 0 && n < a.N) a.row_scale[n] = gs;
+    }
+    for (int k0 = 0; k0 < a.K; k0 += 64) {
+        fill(k0);
+        uint32_t top = take();
+        const int u = k0 / kUnit + g;
+        uint2 c;
+        uint32_t byte;
+        int j;
+        if constexpr (FMT == GF_MXFP4) {
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            byte = mx_scale(top, &mul);
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) x[i] = mul != 0.f ? x[i] * mul : 0.f;
+            c = make_uint2(pack8(x), pack8(x + 8));
+            j = u >> 1;
+        } else {
+            uint32_t t = 0;
+            float s;
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) {
+                x[i] = mul != 0.f ? x[i] * mul : 0.f;
+                t = max(t, abs_bits(x[i]));
+            }
+            byte = nv_scale(t, &s);
+            c = nv_codes<DT_F32>(x, s);
+            j = u;
+        }
+        if (n < a.N) reinterpret_cast<uint2*>(a.codes)[(size_t)n * units + u] = c;
+        if (FMT == GF_NVFP4 || (g & 1) == 0) a.scales[tiled_index(n, j, a.ktiles)] = n < a.N ? (uint8_t)byte : (uint8_t)0;
+    }
+    // scales past K in the last tile
+    for (int j = a.K / Format<FMT>::kBlock + g; j < a.ktiles * 4; j += 4) a.scales[tiled_index(n, j, a.ktiles)] = 0;
+    // the last group of 32 channels also clears the rest of its 128-row tile
+    if (n0 + 32 >= a.N)
+        for (int r = n0 + 32 + (int)(threadIdx.x >> 2); r < (n0 + 128) / 128 * 128; r += 32)
+            for (int j = g; j < a.ktiles * 4; j += 4) a.scales[tiled_index(r, j, a.ktiles)] = 0;
+}
+
+template <int DT>
+cudaError_t quant_dt(const QuantArgs& a, int fmt, cudaStream_t s) {
+    if (fmt == GF_MXFP4) {
+        const dim3 grid((a.rows_out + 7) / 8, (a.units_out + 31) / 32);
+        mx_quant_kernel<DT><<<grid, dim3(32, 8), 0, s>>>(a);
+    } else {
+        const int units = a.K / kUnit;
+        const int threads = units >= kNvThreads ? kNvThreads : (units + 31) / 32 * 32;
+        nv_quant_kernel<DT><<<a.rows_out, threads, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t dequant_fmt(const DequantArgs& a, int dt, cudaStream_t s) {
+    const dim3 grid((a.M + 7) / 8, (a.K / kUnit + 31) / 32), block(32, 8);
+    switch (dt) {
+        case DT_F32: fp4_dequant_kernel<FMT, DT_F32><<<grid, block, 0, s>>>(a); break;
+        case DT_F16: fp4_dequant_kernel<FMT, DT_F16><<<grid, block, 0, s>>>(a); break;
+        default: fp4_dequant_kernel<FMT, DT_BF16><<<grid, block, 0, s>>>(a); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t fp4_scales_bytes(int rows, int K, int fmt, int layout) {
+    const int block = fmt == GF_MXFP4 ? 32 : 16;
+    if (layout == SC_ROWS) return (size_t)rows * fp4::scale_pitch(K, block);
+    return (size_t)((rows + 127) / 128) * fp4::scale_ktiles(K, block) * 512;
+}
+
+cudaError_t launch_fp4_quant(int M, int K, const void* X, int x_dtype, long long ldx, int x_rows, const int32_t* rows,
+                             int fmt, int layout, void* codes, void* scales, float* row_scale, cudaStream_t s) {
+    const int block = fmt == GF_MXFP4 ? 32 : 16;
+    QuantArgs a{};
+    a.M = M; a.K = K;
+    a.X = X; a.ldx_bytes = ldx * (long long)dt_size(x_dtype);
+    a.x_rows = x_rows; a.rows = rows;
+    a.layout = layout;
+    a.pitch = fp4::scale_pitch(K, block);
+    a.ktiles = fp4::scale_ktiles(K, block);
+    a.rows_out = layout == SC_ROWS ? M : (M + 127) / 128 * 128;
+    a.units_out = (layout == SC_ROWS ? a.pitch : a.ktiles * 4) * (block / kUnit);
+    a.codes = static_cast<uint8_t*>(codes);
+    a.scales = static_cast<uint8_t*>(scales);
+    a.row_scale = row_scale;
+    switch (x_dtype) {
+        case DT_F32: return quant_dt<DT_F32>(a, fmt, s);
+        case DT_F16: return quant_dt<DT_F16>(a, fmt, s);
+        default: return quant_dt<DT_BF16>(a, fmt, s);
+    }
+}
+
+cudaError_t launch_fp4_dequant(int M, int K, int fmt, int layout, const void* codes, const void* scales,
+                               const float* row_scale, void* Y, int y_dtype, cudaStream_t s) {
+    const int block = fmt == GF_MXFP4 ? 32 : 16;
+    DequantArgs a{M, K, layout, fp4::scale_pitch(K, block), fp4::scale_ktiles(K, block), static_cast<const uint8_t*>(codes),
+                  static_cast<const uint8_t*>(scales), row_scale, Y};
+    return fmt == GF_MXFP4 ? dequant_fmt<GF_MXFP4>(a, y_dtype, s) : dequant_fmt<GF_NVFP4>(a, y_dtype, s);
+}
+
+cudaError_t launch_fp4_pack(const float* W, int K, int N, int fmt, void* codes, void* scales, float* row_scale, cudaStream_t s) {
+    PackArgs a{W, K, N, fp4::scale_ktiles(K, fmt == GF_MXFP4 ? 32 : 16), static_cast<uint8_t*>(codes),
+               static_cast<uint8_t*>(scales), row_scale};
+    const int grid = (N + 31) / 32;
+    if (fmt == GF_MXFP4) fp4_pack_kernel<GF_MXFP4><<<grid, 128, 0, s>>>(a);
+    else fp4_pack_kernel<GF_NVFP4><<<grid, 128, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace qg

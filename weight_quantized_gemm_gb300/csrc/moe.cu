@@ -1,0 +1,413 @@
+// The two ends of a mixture-of-experts layer: the router's choice of k experts for each token with
+// the expert-sorted order of the chosen (token, expert) pairs, and the weighted sum of each token's
+// expert output rows. Formulas and conventions: include/qgemm.h.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+
+namespace qg {
+namespace {
+
+// ---------------------------------------------------------------- routing
+// One warp per token: lane i holds the logits of experts i, i + 32, ... as order-preserving integer
+// keys, and each of the k rounds takes the largest key by a warp reduction, ties to the lowest expert
+// (a second reduction over the experts that hold it). A stable counting sort of the pairs by expert
+// follows: histograms, exclusive prefix sums, then each pair's rank among the pairs before it by
+// warp matches, so the order depends on nothing but the input. A few tokens run in one thread
+// block and one launch; more run in two, where the second launch's blocks each sum the first's
+// histograms themselves (at most kRouteBlocks x E counts, from L2) instead of waiting for a third
+// launch that scans them.
+constexpr int kSortWarps = 8;         // warps that rank a block's pairs
+constexpr int kSmallThreads = 1024;
+constexpr int kBigThreads = 512;
+
+struct RouteArgs {
+    int T, E, k, renorm;
+    const void* logits;
+    long long ld;
+    int32_t* expert;
+    float* weight;
+    int32_t* slot;
+    int32_t* row;
+    int32_t* offsets;
+    int32_t* hist;      // [blocks][E]
+    int per_block;      // tokens per block
+};
+
+template <int DT>
+__device__ __forceinline__ float load_as_float(const void* p, size_t i) {
+    if constexpr (DT == DT_F32) return __ldg(static_cast<const float*>(p) + i);
+    else if constexpr (DT == DT_F16) return __half2float(__ldg(static_cast<const __half*>(p) + i));
+    else return __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p) + i));
+}
+// Keys grow with the value; 0 stands for an expert that cannot be chosen (-inf or NaN logit).
+__device__ __forceinline__ uint32_t to_key(float x) {
+    if (!(x > __uint_as_float(0xFF800000u))) return 0u;
+    const uint32_t b = __float_as_uint(x + 0.f);   // -0 and 0 are one value
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_key(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// exp(x - top), where equal infinities count as equal values
+__device__ __forceinline__ float rel_exp(float x, float top) { return x == top ? 1.f : expf(x - top); }
+
+// Token t's choice by the calling warp: lane j < k ends with its j-th expert (-1: none left) and weight.
+template <int DT, int EL>
+__device__ __forceinline__ void choose(const RouteArgs& a, int t, int lane, int* expert, float* weight) {
+    uint32_t key[EL];
+#pragma unroll
+    for (int j = 0; j < EL; ++j) {
+        const int e = lane + 32 * j;
+        key[j] = e < a.E ? to_key(load_as_float<DT>(a.logits, (size_t)((long long)t * a.ld) + e)) : 0u;
+    }
+    uint32_t best = 0, chosen_key = 0, first = 0;
+    int best_j = 0, chosen = -1;
+#pragma unroll
+    for (int j = 0; j < EL; ++j)
+        if (key[j] > best) { best = key[j]; best_j = j; }
+    float all = 0.f;
+    for (int r = 0; r < a.k; ++r) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (r == 0) {
+            first = top;
+            if (!a.renorm && top) {
+                const float m = from_key(top);
+#pragma unroll
+                for (int j = 0; j < EL; ++j)
+                    if (key[j]) all += rel_exp(from_key(key[j]), m);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+            }
+        }
+        if (!top) break;
+        const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(lane + 32 * best_j) : 0xffffffffu);
+        if (lane == r) {
+            chosen = (int)e;
+            chosen_key = top;
+        }
+        if ((int)(e & 31u) == lane) {   // its holder takes it out
+            best = 0;
+#pragma unroll
+            for (int j = 0; j < EL; ++j) {
+                if (lane + 32 * j == (int)e) key[j] = 0u;
+                if (key[j] > best) { best = key[j]; best_j = j; }
+            }
+        }
+    }
+    const float w = chosen >= 0 ? rel_exp(from_key(chosen_key), from_key(first)) : 0.f;
+    if (a.renorm) {
+        all = w;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    *expert = chosen;
+    *weight = chosen >= 0 ? w / all : 0.f;
+}
+
+// The choice of tokens [t0, t1) by all warps of the block; counts[e] gets the block's pairs per
+// expert (shared memory, cleared here; integer sums, so their order does not matter).
+template <int DT, int EL>
+__device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int t1, int32_t* counts) {
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) counts[e] = 0;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    for (int t = t0 + (int)(threadIdx.x >> 5); t < t1; t += blockDim.x >> 5) {
+        int e;
+        float w;
+        choose<DT, EL>(a, t, lane, &e, &w);
+        if (lane < a.k) {
+            a.expert[(size_t)t * a.k + lane] = e;
+            a.weight[(size_t)t * a.k + lane] = w;
+            if (e >= 0) atomicAdd(counts + e, 1);
+        }
+    }
+    __syncthreads();
+}
+
+// Stable placement of pairs [p0, p1): base[e] = position of the block's first pair of expert e.
+// start: [kSortWarps][E] shared memory. Every warp of the block calls it.
+__device__ __forceinline__ void place_block(const RouteArgs& a, int p0, int p1, const int32_t* base, int32_t* start) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kSortWarps * a.E; i += blockDim.x) start[i] = 0;
+    __syncthreads();
+    const int seg = ((p1 - p0 + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int b = min(p0 + warp * seg, p1), e1 = min(b + seg, p1);
+    if (warp < kSortWarps) {
+        for (int p = b + lane; p < b + (e1 - b + 31) / 32 * 32; p += 32) {
+            const int e = p < e1 ? a.expert[p] : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            if (e >= 0 && lane == __ffs(same) - 1) start[warp * a.E + e] += __popc(same);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        int at = base[e];
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = start[w * a.E + e];
+            start[w * a.E + e] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    if (warp < kSortWarps) {
+        for (int p = b + lane; p < b + (e1 - b + 31) / 32 * 32; p += 32) {
+            const int e = p < e1 ? a.expert[p] : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            int at = -1;
+            if (e >= 0) {
+                at = start[warp * a.E + e] + __popc(same & ((1u << lane) - 1u));
+                a.row[at] = p / a.k;
+            }
+            if (p < e1) a.slot[p] = at;
+            __syncwarp();
+            if (e >= 0 && lane == __ffs(same) - 1) start[warp * a.E + e] += __popc(same);
+            __syncwarp();
+        }
+    }
+}
+
+// Exclusive prefix sum of v[0 .. E) into out[0 .. E], by the block's first warp.
+__device__ __forceinline__ void prefix(const int32_t* v, int32_t* out, int E) {
+    if (threadIdx.x < 32) {
+        int carry = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + threadIdx.x, x = e < E ? v[e] : 0;
+            int s = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, s, o);
+                if ((int)threadIdx.x >= o) s += y;
+            }
+            if (e < E) out[e] = carry + s - x;
+            carry += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (threadIdx.x == 0) out[E] = carry;
+    }
+    __syncthreads();
+}
+
+template <int DT, int EL>
+__global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteArgs a) {
+    extern __shared__ int32_t sm[];
+    int32_t *counts = sm, *first = sm + a.E, *start = first + a.E + 1;
+    choose_block<DT, EL>(a, 0, a.T, counts);     // (its last barrier orders the experts it wrote, too)
+    prefix(counts, first, a.E);
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.offsets[e] = first[e];
+    for (int p = first[a.E] + threadIdx.x; p < a.T * a.k; p += blockDim.x) a.row[p] = -1;
+    place_block(a, 0, a.T * a.k, first, start);
+}
+
+template <int DT, int EL>
+__global__ void __launch_bounds__(kBigThreads) route_choose_kernel(const RouteArgs a) {
+    extern __shared__ int32_t sm[];
+    const int t0 = min(blockIdx.x * a.per_block, a.T), t1 = min(t0 + a.per_block, a.T);
+    choose_block<DT, EL>(a, t0, t1, sm);
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(size_t)blockIdx.x * a.E + e] = sm[e];
+}
+
+__global__ void __launch_bounds__(kBigThreads) route_place_kernel(const RouteArgs a) {
+    extern __shared__ int32_t sm[];
+    int32_t *total = sm, *before = sm + a.E, *first = before + a.E, *start = first + a.E + 1;
+    for (int e = threadIdx.x; e < 2 * a.E; e += blockDim.x) sm[e] = 0;
+    __syncthreads();
+    // the pairs per expert in all blocks, and in the blocks before this one: 16 histograms at a time
+    // to a group of threads
+    const int groups = max((int)blockDim.x / a.E, 1);
+    for (int i = threadIdx.x; i < groups * a.E; i += blockDim.x) {
+        const int g = i / a.E, e = i - g * a.E;
+        int all = 0, mine = 0;
+#pragma unroll 8
+        for (int b = g; b < (int)gridDim.x; b += groups) {
+            const int c = __ldg(a.hist + (size_t)b * a.E + e);
+            all += c;
+            mine += b < (int)blockIdx.x ? c : 0;
+        }
+        atomicAdd(total + e, all);
+        atomicAdd(before + e, mine);
+    }
+    __syncthreads();
+    prefix(total, first, a.E);
+    if (blockIdx.x == 0) {
+        for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.offsets[e] = first[e];
+        for (int p = first[a.E] + threadIdx.x; p < a.T * a.k; p += blockDim.x) a.row[p] = -1;
+    }
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) before[e] += first[e];
+    __syncthreads();
+    const int t0 = min(blockIdx.x * a.per_block, a.T), t1 = min(t0 + a.per_block, a.T);
+    place_block(a, t0 * a.k, t1 * a.k, before, start);
+}
+
+template <int DT, int EL>
+cudaError_t route_el(RouteArgs a, cudaStream_t s) {
+    const size_t sort = (size_t)kSortWarps * a.E * sizeof(int32_t);
+    if (!route_needs_workspace(a.T)) {
+        route_small_kernel<DT, EL><<<1, kSmallThreads, (2 * a.E + 1) * sizeof(int32_t) + sort, s>>>(a);
+        return cudaGetLastError();
+    }
+    const int want = (a.T + 15) / 16;
+    const int blocks = want < kRouteBlocks ? want : kRouteBlocks;
+    a.per_block = (a.T + blocks - 1) / blocks;
+    route_choose_kernel<DT, EL><<<blocks, kBigThreads, a.E * sizeof(int32_t), s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    route_place_kernel<<<blocks, kBigThreads, (3 * a.E + 1) * sizeof(int32_t) + sort, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int DT>
+cudaError_t route_dt(const RouteArgs& a, cudaStream_t s) {
+    if (a.E <= 32) return route_el<DT, 1>(a, s);
+    if (a.E <= 64) return route_el<DT, 2>(a, s);
+    if (a.E <= 128) return route_el<DT, 4>(a, s);
+    if (a.E <= 256) return route_el<DT, 8>(a, s);
+    if (a.E <= 512) return route_el<DT, 16>(a, s);
+    return route_el<DT, 32>(a, s);
+}
+
+// ---------------------------------------------------------------- combining
+// out[t] = sum_j weight[t][j] * Y[slot[t][j]] + residual[t], in float32, in the order of j, rounded
+// once. HBM bounds it (k rows in, one out, each byte once); a thread takes 8 columns of one token and
+// has up to four rows' loads in flight.
+struct CombineArgs {
+    int T, k, N, R;
+    const void* Y;
+    const int32_t* slot;
+    const float* weight;
+    const void* residual;
+    void* out;
+};
+
+template <int DT, int V>
+struct Vec {   // V consecutive values (V = 8: 16-byte loads; V = 1: any N)
+    float x[V];
+    __device__ __forceinline__ void load(const void* p, size_t i) {
+        if constexpr (V == 1) {
+            x[0] = load_as_float<DT>(p, i);
+        } else {
+            constexpr int kVecs = DT == DT_F32 ? 2 : 1;
+            uint32_t w[4 * kVecs];
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * (DT == DT_F32 ? 4 : 2));
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                const uint4 r = __ldg(q + v);
+                w[4 * v] = r.x; w[4 * v + 1] = r.y; w[4 * v + 2] = r.z; w[4 * v + 3] = r.w;
+            }
+#pragma unroll
+            for (int c = 0; c < V; ++c) {
+                if constexpr (DT == DT_F32) x[c] = __uint_as_float(w[c]);
+                else if constexpr (DT == DT_F16) x[c] = __half2float(__ushort_as_half((unsigned short)(w[c >> 1] >> (16 * (c & 1)))));
+                else x[c] = __uint_as_float((c & 1) ? w[c >> 1] & 0xFFFF0000u : w[c >> 1] << 16);
+            }
+        }
+    }
+};
+
+template <int DT, int V>
+__device__ __forceinline__ void store_vec(void* p, size_t i, const float* x) {
+    if constexpr (V == 1) {
+        if constexpr (DT == DT_F32) static_cast<float*>(p)[i] = x[0];
+        else if constexpr (DT == DT_F16) static_cast<__half*>(p)[i] = __float2half_rn(x[0]);
+        else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x[0]);
+    } else if constexpr (DT == DT_F32) {
+        float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        q[0] = make_float4(x[0], x[1], x[2], x[3]);
+        q[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if constexpr (DT == DT_F16) {
+                const __half2 h = __floats2half2_rn(x[2 * c], x[2 * c + 1]);
+                w[c] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * c], x[2 * c + 1]);
+                w[c] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p) + i * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// block (64, 4): 64 runs of V columns of 4 tokens
+template <int DT, int ODT, int V>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
+    const int t = blockIdx.x * 4 + threadIdx.y;
+    const int n = (blockIdx.y * 64 + threadIdx.x) * V;
+    if (t >= a.T || n >= a.N) return;
+    float acc[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] = 0.f;
+    for (int j0 = 0; j0 < a.k; j0 += 4) {
+        Vec<DT, V> y[4];
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int s = j0 + j < a.k ? __ldg(a.slot + (size_t)t * a.k + j0 + j) : -1;
+            const bool in = s >= 0 && s < a.R;    // a pair that was not placed adds nothing
+            w[j] = in ? __ldg(a.weight + (size_t)t * a.k + j0 + j) : 0.f;
+            if (in) y[j].load(a.Y, (size_t)s * a.N + n);
+            else
+#pragma unroll
+                for (int c = 0; c < V; ++c) y[j].x[c] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < V; ++c) acc[c] = fmaf(w[j], y[j].x[c], acc[c]);
+    }
+    if (a.residual) {
+        Vec<ODT, V> r;
+        r.load(a.residual, (size_t)t * a.N + n);
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] += r.x[c];
+    }
+    store_vec<ODT, V>(a.out, (size_t)t * a.N + n, acc);
+}
+
+template <int DT, int ODT>
+cudaError_t combine_v(const CombineArgs& a, cudaStream_t s) {
+    if (a.N % 8 == 0) {
+        const dim3 grid((a.T + 3) / 4, (a.N / 8 + 63) / 64);
+        combine_kernel<DT, ODT, 8><<<grid, dim3(64, 4), 0, s>>>(a);
+    } else {
+        const dim3 grid((a.T + 3) / 4, (a.N + 63) / 64);
+        combine_kernel<DT, ODT, 1><<<grid, dim3(64, 4), 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+template <int DT>
+cudaError_t combine_dt(const CombineArgs& a, int out_dtype, cudaStream_t s) {
+    switch (out_dtype) {
+        case DT_F32: return combine_v<DT, DT_F32>(a, s);
+        case DT_F16: return combine_v<DT, DT_F16>(a, s);
+        default: return combine_v<DT, DT_BF16>(a, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(int T, int E, int k, const void* logits, int dtype, long long ld, int renorm, int32_t* expert,
+                             float* weight, int32_t* slot, int32_t* row, int32_t* offsets, void* workspace, cudaStream_t s) {
+    RouteArgs a{T, E, k, renorm, logits, ld, expert, weight, slot, row, offsets, static_cast<int32_t*>(workspace), 0};
+    switch (dtype) {
+        case DT_F32: return route_dt<DT_F32>(a, s);
+        case DT_F16: return route_dt<DT_F16>(a, s);
+        default: return route_dt<DT_BF16>(a, s);
+    }
+}
+
+cudaError_t launch_moe_combine(int T, int k, int N, int R, const void* Y, int y_dtype, const int32_t* slot,
+                               const float* weight, const void* residual, void* out, int out_dtype, cudaStream_t s) {
+    const CombineArgs a{T, k, N, R, Y, slot, weight, residual, out};
+    switch (y_dtype) {
+        case DT_F32: return combine_dt<DT_F32>(a, out_dtype, s);
+        case DT_F16: return combine_dt<DT_F16>(a, out_dtype, s);
+        default: return combine_dt<DT_BF16>(a, out_dtype, s);
+    }
+}
+
+}  // namespace qg

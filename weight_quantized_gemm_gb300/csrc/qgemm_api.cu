@@ -260,6 +260,7 @@ long long qg::option_wait_ns() { return 1000LL * g_opt_wait_us.load(std::memory_
 int qg::option_stall() { return g_opt_stall.load(std::memory_order_relaxed); }
 
 int qg::api_fail(int code, const char* detail) { return fail(code, "%s", detail); }
+bool qg::api_inject_fault() { return inject_fault(); }
 size_t qg::api_packed_bytes(int K, int N, int mode, int block, int w_dtype, size_t* table_bytes) {
     *table_bytes = 0;
     if (check_shape(K, N, mode, &block) != QGEMM_OK) return 0;
