@@ -165,7 +165,13 @@ struct GroupGemmArgs {
     void* C;
     int c_dtype;
 };
-cudaError_t launch_group_gemm(const GroupGemmArgs& a, int fmt, cudaStream_t s);
+cudaError_t launch_group_gemm_half(const GroupGemmArgs& a, int fmt, cudaStream_t s);
+cudaError_t launch_group_gemm_mxfp4(const GroupGemmArgs& a, int fmt, cudaStream_t s);
+cudaError_t launch_group_gemm_nvfp4(const GroupGemmArgs& a, int fmt, cudaStream_t s);
+inline cudaError_t launch_group_gemm(const GroupGemmArgs& a, int fmt, cudaStream_t s) {
+    return fmt == GF_MXFP4 ? launch_group_gemm_mxfp4(a, fmt, s)
+                           : (fmt == GF_NVFP4 ? launch_group_gemm_nvfp4(a, fmt, s) : launch_group_gemm_half(a, fmt, s));
+}
 // The router's launches: up to kRouteSmallTokens tokens in one thread block, else kRouteBlocks blocks
 // at most, with a histogram of E counts each in the workspace.
 constexpr int kRouteSmallTokens = 128;
