@@ -14,7 +14,7 @@
 //               weight rows and activation rows (128-byte swizzle), and the weight's scale tiles, which
 //               are stored in the order the tensor cores take them;
 //   warps 2, 3  the activations' scales, stored row by row because a group may start at any row, brought
-//               into that same order by 4-byte asynchronous copies, several stages ahead;
+//               into that same order through registers;
 //   warp 1      one lane copies a stage's scales to tensor memory (tcgen05.cp; copies and MMAs of one
 //               thread run in issue order) and issues its MMAs, accumulating in tensor memory;
 //   warps 4-11  read the accumulator, apply the epilogue and store. The next tile's MMAs run meanwhile
@@ -31,6 +31,8 @@
 // and a cluster's blocks leave together.
 #pragma once
 
+#include <type_traits>
+
 #include "epilogue.cuh"
 #include "fp4.cuh"
 #include "ptx.cuh"
@@ -40,7 +42,7 @@ namespace gg {
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
-constexpr int kScaleWarp = 2, kScaleThreads = 64;
+constexpr int kScaleWarp = 2;
 constexpr int kRowBytes = 128;                     // K bytes of a row per stage
 constexpr int kCh = 128;                           // channels per tile
 constexpr int kMaxSplit = 8;
@@ -61,9 +63,6 @@ struct Plan {
     static constexpr int kTables = 2 * (1024 + 1) * 4;                     // group starts and tile counts
     static constexpr int kRoom = (int)kSmemMax - kTail - kTables - kRed;
     static constexpr int kStages = kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
-    // stages whose scale copies are in flight: half the ring, so that a stage's scales are reported in
-    // place while the MMAs are still half a ring away from it
-    static constexpr int kLag = kStages / 2;
     static constexpr size_t kSmem = (size_t)kStages * kStage + kRed + kTail + kTables;
     static constexpr int kBoxRows = BN == 32 ? 16 : BN / 2;                // rows of one activation box
     static constexpr bool kOverlap = F != HALF && BN == 256;
@@ -190,8 +189,13 @@ __device__ __forceinline__ bool cluster_bar_wait(uint32_t bar, uint32_t parity, 
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
     return true;
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// True in one lane of the (converged) warp. The instructions that a single thread issues (TMA,
+// tcgen05.mma, tcgen05.cp) take their operands from warp-wide registers; under this predicate the
+// compiler knows that one lane is active and moves them there directly, under `lane == 0` it loops.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
 }
 
 struct Tile {
@@ -206,6 +210,83 @@ __device__ __forceinline__ void pair_up(const float (&v)[16], float (&first)[8],
         const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 8], 1);
         first[i] = odd ? got : v[i];
         second[i] = odd ? v[i + 8] : got;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void act16(float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = act_fixed<ACT>(v[i]);
+}
+
+// The rest of the epilogue for 16 rows m .. m + 15 (the first `live` of them) of channel n: activation,
+// residual, rounding, stores. One choice of activation and type per chunk, none per value. 16-bit
+// outputs leave as pairs of channels (64 contiguous bytes a row), of rows 0-7 from the even lanes
+// and 8-15 from the odd ones; SwiGLU pairs become one channel the same way.
+template <int CDT>
+__device__ __forceinline__ void store_chunk(const Params& p, float (&v)[16], int n, int m, int live, bool odd) {
+    constexpr size_t kEsz = CDT == DT_F32 ? 4 : 2;
+    switch (p.act) {
+        case ACT_RELU: act16<ACT_RELU>(v); break;
+        case ACT_SILU: act16<ACT_SILU>(v); break;
+        case ACT_GELU_TANH: act16<ACT_GELU_TANH>(v); break;
+        default: break;
+    }
+    const bool glu = p.act == ACT_SWIGLU;
+    const size_t step = (size_t)p.cols * kEsz;
+    // `count` values of one channel in consecutive rows
+    auto column = [&](float* y, int row, int col, int rows, auto count) {
+        constexpr int kCount = decltype(count)::value;
+        const size_t at = (size_t)row * p.cols + col;
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < kCount; ++i)
+                if (i < rows) y[i] += load_c<CDT>(p.residual, at + (size_t)i * p.cols);
+        }
+        uint8_t* out = static_cast<uint8_t*>(p.C) + at * kEsz;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i)
+            if (i < rows) store_out_rt(out + i * step, 0, y[i], CDT);
+    };
+    if (glu || (CDT != DT_F32 && (p.N & 1) == 0)) {
+        float a[8], b[8];
+        pair_up(v, a, b, odd);
+        const int row = m + (odd ? 8 : 0), rows = live - (odd ? 8 : 0);
+        if (n >= p.N) return;              // (N is even here: both lanes of a pair)
+        if (glu) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = act_fixed<ACT_SILU>(a[i]) * b[i];
+            column(a, row, n >> 1, rows, std::integral_constant<int, 8>());
+        } else if constexpr (CDT != DT_F32) {
+            const size_t at = ((size_t)row * p.cols + (n & ~1)) * kEsz;
+            if (p.residual) {
+                uint32_t r[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    r[i] = i < rows ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.residual) + at + i * step)) : 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (CDT == DT_F16) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+                        a[i] += f.x;
+                        b[i] += f.y;
+                    } else {
+                        a[i] += __uint_as_float(r[i] << 16);
+                        b[i] += __uint_as_float(r[i] & 0xFFFF0000u);
+                    }
+                }
+            }
+            uint8_t* out = static_cast<uint8_t*>(p.C) + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t w;
+                if constexpr (CDT == DT_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b[i]), "f"(a[i]));
+                else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b[i]), "f"(a[i]));
+                if (i < rows) *reinterpret_cast<uint32_t*>(out + i * step) = w;
+            }
+        }
+    } else if (n < p.N) {
+        column(v, m, n, live, std::integral_constant<int, 16>());
     }
 }
 
@@ -240,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             ptx::mbar_init(full(s), 1);
-            ptx::mbar_init(full_sc(s), kScaleThreads / 32);
+            ptx::mbar_init(full_sc(s), BN == 256 ? 2 : 1);   // one warp, or one a half
             ptx::mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -315,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
 
     if (warp == 0) {
         // ---------------- TMA
-        if (lane == 0) {
+        if (elect_one()) {
             int g = 0, s = 0;
             uint32_t ph = 0;
             bool stop = false;
@@ -350,56 +431,71 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
         }
     } else if (warp == kScaleWarp || warp == kScaleWarp + 1) {
         // ---------------- the activations' scales
+        // A lane takes the 16-byte pieces (two stages' scales in MXFP4, one's in NVFP4) of the four rows
+        // r, r + 32, r + 64, r + 96 of a half of the tile, the next pieces while it writes these, and writes
+        // each scale tile's four words of its rows, which lie side by side there, as 16 bytes. (Bringing
+        // the words in one by one with 4-byte asynchronous copies took as long as the stage's MMAs:
+        // each touches another line of the cache.) The warps take a half each, or turns.
         if constexpr (F != HALF) {
-            const int tid = threadIdx.x - kScaleWarp * 32;
-            int g = 0, s = 0;
+            constexpr bool kTurns = BN < 256;
+            constexpr int kStep = kTurns ? 2 : 1;
+            const int w = warp - kScaleWarp, half = kTurns ? 0 : w;
+            int s = 0, g = 0;
             uint32_t ph = 0;
             bool stop = false;
-            auto landed = [&](int i) {        // stage i's copies are complete: visible to the tensor core's copies
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(full_sc(i % S));
-            };
             for (int t = worker; t < total && !stop; t += workers) {
                 const Tile x = tile_of(t);
-                constexpr int kRows = BN / kScaleThreads > 0 ? BN / kScaleThreads : 1;
-                const uint8_t* src[kRows];
+                uint4 now[4], next[4];
+                const uint8_t* src = p.As + (size_t)(x.m0 + 128 * half + lane) * p.pitch;
+                auto fetch = [&](int piece, uint4 (&v)[4]) {
 #pragma unroll
-                for (int j = 0; j < kRows; ++j)
-                    src[j] = p.As + (size_t)(x.m0 + min(tid + j * kScaleThreads, x.rows - 1)) * p.pitch;
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = 128 * half + 32 * j + lane < x.rows
+                                   ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)(32 * j) * p.pitch) + piece)
+                                   : make_uint4(0, 0, 0, 0);
+                };
+                const int last = (ks0 + nks - 1) / (F == MX ? 2 : 1);
+                int have = -1;
                 for (int i = 0; i < nks; ++i) {
-                    const bool go = !*abort_flag && (g < S || wait(empty(s), ph ^ 1u));
-                    if (!__all_sync(0xffffffffu, go)) {
-                        stop = true;
-                        break;
-                    }
-                    const uint32_t dst = ring + (uint32_t)s * P::kStage + P::kA + P::kB + P::kSA;
+                    const int k = ks0 + i, piece = F == MX ? k >> 1 : k;
+                    if (!kTurns || (piece & 1) == w) {
+                        if (piece != have) {
+                            if (have < 0) fetch(piece, now);
+                            else
 #pragma unroll
-                    for (int j = 0; j < kRows; ++j) {
-                        const int r = tid + j * kScaleThreads;
-                        if (r < x.rows) {
-#pragma unroll
-                            for (int c = 0; c < P::kChunks; ++c)
-                                cp_async4(dst + (c * P::kHalves + (r >> 7)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4,
-                                          src[j] + ((ks0 + i) * P::kChunks + c) * 4);
+                                for (int j = 0; j < 4; ++j) now[j] = next[j];
+                            have = piece;
+                            if (piece + kStep <= last) fetch(piece + kStep, next);
                         }
-                    }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (g >= P::kLag) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(P::kLag) : "memory");
-                        landed(g - P::kLag);
+                        const bool go = !*abort_flag && (g < S || wait(empty(s), ph ^ 1u));
+                        if (!__all_sync(0xffffffffu, go)) {
+                            stop = true;
+                            break;
+                        }
+                        const uint32_t dst = ring + (uint32_t)s * P::kStage + P::kA + P::kB + P::kSA + lane * 16;
+                        const bool second = F == MX && (k & 1);
+#pragma unroll
+                        for (int c = 0; c < P::kChunks; ++c) {
+                            auto word = [&](const uint4& v) {
+                                if (F == MX) return c == 0 ? (second ? v.z : v.x) : (second ? v.w : v.y);
+                                return c == 0 ? v.x : (c == 1 ? v.y : (c == 2 ? v.z : v.w));
+                            };
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c * P::kHalves + half) * 512),
+                                         "r"(word(now[0])), "r"(word(now[1])), "r"(word(now[2])), "r"(word(now[3]))
+                                         : "memory");
+                        }
+                        ptx::fence_proxy_async_smem();       // visible to the tensor core's copies
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(full_sc(s));
                     }
                     ++g;
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
-            ptx::cp_async_wait_all();
-            if (!stop)
-                for (int i = max(0, g - P::kLag); i < g; ++i) landed(i);
         }
     } else if (warp == 1) {
         // ---------------- MMA
-        if (lane == 0) {
+        if (elect_one()) {
             int s = 0, tj = 0;
             uint32_t ph = 0;
             bool stop = false, issued = false;
@@ -462,8 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     } else {
         // ---------------- epilogue
         const int q = warp & 3, h = (warp - kEpiWarp) >> 2;
-        const bool odd = lane & 1, glu = p.act == ACT_SWIGLU, half_out = p.c_dtype != DT_F32;
-        const bool pairs = half_out && !glu && (p.N & 1) == 0;
+        const bool odd = lane & 1, glu = p.act == ACT_SWIGLU;
         float* const part = reinterpret_cast<float*>(smem + S * P::kStage);
         auto cluster_wait = [&](uint32_t b, uint32_t parity) {
             return cluster_bar_wait(b, parity, abort_flag, p.status, p.wait_ns);
@@ -473,25 +568,6 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                 y += p.c_dtype == DT_F32 ? load_c<DT_F32>(p.residual, at)
                                          : (p.c_dtype == DT_F16 ? load_c<DT_F16>(p.residual, at) : load_c<DT_BF16>(p.residual, at));
             store_out_rt(p.C, at, y, p.c_dtype);
-        };
-        auto store_two = [&](size_t at, float y0, float y1) {     // 16-bit, at even
-            uint32_t w;
-            if (p.c_dtype == DT_F16) {
-                if (p.residual) {
-                    const float2 r = __half22float2(__ldg(reinterpret_cast<const __half2*>(static_cast<const __half*>(p.residual) + at)));
-                    y0 += r.x;
-                    y1 += r.y;
-                }
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y1), "f"(y0));
-            } else {
-                if (p.residual) {
-                    const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.residual) + at));
-                    y0 += __uint_as_float(r << 16);
-                    y1 += __uint_as_float(r & 0xFFFF0000u);
-                }
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y1), "f"(y0));
-            }
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.C) + at) = w;
         };
         int tj = 0;
         for (int t = worker; t < total; t += workers, ++tj) {
@@ -572,29 +648,9 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], ws, bias);
-                    if (glu || pairs) {
-                        float a[8], b[8];
-                        if (!glu) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] = act_apply(p.act, v[i]);
-                        }
-                        pair_up(v, a, b, odd);
-                        const int r0 = odd ? 8 : 0, ne = n & ~1;
-                        if (n < p.N) {              // (N is even here: both lanes of a pair)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                if (r0 + i >= live) break;
-                                if (glu) store_one((size_t)(m + r0 + i) * p.cols + (ne >> 1), act_fixed<ACT_SILU>(a[i]) * b[i]);
-                                else store_two((size_t)(m + r0 + i) * p.cols + ne, a[i], b[i]);
-                            }
-                        }
-                    } else if (n < p.N) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (i >= live) break;
-                            store_one((size_t)(m + i) * p.cols + n, act_apply(p.act, v[i]));
-                        }
-                    }
+                    if (p.c_dtype == DT_BF16) store_chunk<DT_BF16>(p, v, n, m, live, odd);
+                    else if (p.c_dtype == DT_F16) store_chunk<DT_F16>(p, v, n, m, live, odd);
+                    else store_chunk<DT_F32>(p, v, n, m, live, odd);
                 }
                 __syncwarp();
             }
