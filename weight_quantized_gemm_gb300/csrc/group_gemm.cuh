@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             bool stop = false, issued = false;
             if (p.stall) wait(stall_bar, 0u);      // diagnostic: runs out
             const int kbytes = F == HALF ? 2 * p.K : p.K / 2;
+            const uint64_t wdesc = sw128_desc(ring), adesc = sw128_desc(ring + P::kA), sdesc = scale_desc(ring + P::kA + P::kB);
             for (int t = worker; t < total && !stop; t += workers, ++tj) {
                 const Tile x = tile_of(t);
                 const uint32_t idesc = inst_desc<F>((x.rows + 15) / 16 * 16, p.bf16);
@@ -510,38 +511,35 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                 if (P::kOverlap ? (tj >= 1 && !wait(acc_empty(0), (uint32_t)(tj - 1) & 1u))
                                 : (tj >= 2 && !wait(acc_empty(tj & 1), (uint32_t)((tj >> 1) - 1) & 1u)))
                     break;
-                const int halves = (x.rows + 127) / 128;
                 for (int i = 0; i < nks; ++i) {
-                    if (*abort_flag || !wait(full(s), ph) || (F != HALF && !wait(full_sc(s), ph))) {
+                    if (!wait(full(s), ph) || (F != HALF && !wait(full_sc(s), ph))) {
                         stop = true;
                         break;
                     }
                     tc_fence_after();
                     issued = true;
-                    const uint32_t st = ring + (uint32_t)s * P::kStage;
-                    const uint64_t wdesc = sw128_desc(st), adesc = sw128_desc(st + P::kA);
+                    const uint64_t at = (uint64_t)(s * (P::kStage >> 4));     // the stage, in descriptor units
                     const int steps = min(4, (kbytes - (ks0 + i) * kRowBytes) / 32);     // 32 bytes of K per MMA
-                    if constexpr (F != HALF) {
-                        const uint32_t sa = st + P::kA + P::kB, sb = sa + P::kSA;
-#pragma unroll
-                        for (int c = 0; c < P::kChunks; ++c) {
-                            if (c * (4 / P::kChunks) >= steps) break;
-                            copy_scales(tmem + P::kSaCol + 4 * c, scale_desc(sa + c * 512));
-                            for (int h = 0; h < halves; ++h)
-                                copy_scales(tmem + P::kSbCol + 4 * (c * P::kHalves + h), scale_desc(sb + (c * P::kHalves + h) * 512));
-                        }
-                    }
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk >= steps) break;
                         const uint32_t add = (i | kk) != 0;
                         if constexpr (F == HALF) {
-                            mma_half(acc, wdesc + 2 * kk, adesc + 2 * kk, idesc, add);
+                            mma_half(acc, wdesc + at + 2 * kk, adesc + at + 2 * kk, idesc, add);
                         } else {
+                            // a scale tile serves two MMAs (MXFP4) or one; rows and halves past the tile's
+                            // are copied too, whatever they hold: their columns are not read
                             const int c = F == MX ? kk >> 1 : kk;
+                            if (F == NV || (kk & 1) == 0) {
+                                copy_scales(tmem + P::kSaCol + 4 * c, sdesc + at + c * 32);
+#pragma unroll
+                                for (int h = 0; h < P::kHalves; ++h)
+                                    copy_scales(tmem + P::kSbCol + 4 * (c * P::kHalves + h),
+                                                sdesc + at + (P::kChunks + c * P::kHalves + h) * 32);
+                            }
                             const uint32_t sf = F == MX ? 2u * (kk & 1) : 0u;
-                            mma_fp4<F>(acc, wdesc + 2 * kk, adesc + 2 * kk, idesc | sf << 29 | sf << 4, tmem + P::kSaCol + 4 * c,
-                                       tmem + P::kSbCol + 4 * c * P::kHalves, add);
+                            mma_fp4<F>(acc, wdesc + at + 2 * kk, adesc + at + 2 * kk, idesc | sf << 29 | sf << 4,
+                                       tmem + P::kSaCol + 4 * c, tmem + P::kSbCol + 4 * c * P::kHalves, add);
                         }
                     }
                     mma_commit(empty(s));
