@@ -19,7 +19,7 @@
 //               thread run in issue order) and issues its MMAs, accumulating in tensor memory;
 //   warps 4-11  read the accumulator, apply the epilogue and store. The next tile's MMAs run meanwhile
 //               in a second accumulator. Two of 256 columns do not fit beside the scales: they overlap in
-//               48 columns, which the epilogue reads first.
+//               32 (MXFP4) or 48 columns, which the epilogue reads first.
 // Groups are found in the kernel from the offsets (the host never reads them): each block sums the
 // groups' tile counts once, and finds a tile's group by binary search.
 //
@@ -47,43 +47,50 @@ constexpr int kRowBytes = 128;                     // K bytes of a row per stage
 constexpr int kCh = 128;                           // channels per tile
 constexpr int kMaxSplit = 8;
 constexpr int kMaxStages = 10;
+constexpr long long kDrainNs = 20000000;           // limit of a wait for copies in flight after an abort (PAIR)
 constexpr size_t kSmemMax = 232448;
 constexpr int kTail = 1024;                        // barriers
 
 // Operand forms: 16-bit, or 4-bit with 2 (MXFP4) or 4 (NVFP4) scale tiles per stage.
 enum Form { HALF = 0, MX = 1, NV = 2 };
-template <int F, int BN, bool SPLIT>
+// Blocks and tiles: one block a tile; a cluster that shares a tile's K; two blocks a tile of 256 channels.
+enum Mode { SOLO = 0, SPLIT = 1, PAIR = 2 };
+template <int F, int BN, int MODE>
 struct Plan {
     static constexpr int kChunks = F == HALF ? 0 : (F == MX ? 2 : 4);      // scale tiles (128 rows x 4) per stage
     static constexpr int kHalves = (BN + 127) / 128;                       // ... of the activations, per 128 rows
-    static constexpr int kA = kCh * kRowBytes, kB = BN * kRowBytes;
+    static constexpr int kTileCh = MODE == PAIR ? 2 * kCh : kCh;            // channels of a tile
+    static constexpr int kBRows = MODE == PAIR ? BN / 2 : BN;              // activation rows in this block's stage
+    static constexpr int kA = kCh * kRowBytes, kB = kBRows * kRowBytes;
     static constexpr int kSA = kChunks * 512, kSB = kChunks * kHalves * 512;
     static constexpr int kStage = kA + kB + kSA + kSB;
-    static constexpr int kRed = SPLIT ? BN * kCh * 4 : 0;                  // this block's partial sums
+    static constexpr int kRed = MODE == SPLIT ? BN * kCh * 4 : 0;                  // this block's partial sums
     static constexpr int kTables = 2 * (1024 + 1) * 4;                     // group starts and tile counts
     static constexpr int kRoom = (int)kSmemMax - kTail - kTables - kRed;
     static constexpr int kStages = kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
     static constexpr size_t kSmem = (size_t)kStages * kStage + kRed + kTail + kTables;
-    static constexpr int kBoxRows = BN == 32 ? 16 : BN / 2;                // rows of one activation box
-    static constexpr bool kOverlap = F != HALF && BN == 256;
-    static constexpr int kAcc1 = kOverlap ? 208 : BN;                      // second accumulator's column
-    static constexpr int kSaCol = kOverlap ? 464 : 2 * BN;                 // scale columns
-    static constexpr int kSbCol = kSaCol + 16;
+    static constexpr int kBoxRows = BN == 32 ? 16 : 64;                 // rows of one activation box
+    // tensor-memory columns: two accumulators, then the scales of a stage
+    static constexpr int kScaleCols = kChunks * (1 + kHalves) * 4;
+    static constexpr bool kOverlap = 2 * BN + kScaleCols > 512;
+    static constexpr int kAcc1 = kOverlap ? (512 - kScaleCols - BN) / 16 * 16 : BN;
+    static constexpr int kSaCol = kAcc1 + BN, kSbCol = kSaCol + 4 * kChunks;
+    static constexpr int kShared = kOverlap ? (BN - kAcc1 + 15) / 16 : 0;  // chunks of 16 columns with shared ones
     static_assert(kStage % 1024 == 0, "stages keep the 128-byte swizzle's alignment");
     static_assert(kStages >= 4, "ring");
-    static_assert(F == HALF ? 2 * BN <= 512 : kSbCol + kChunks * kHalves * 4 <= 512, "tensor memory");
+    static_assert(kAcc1 + BN + kScaleCols <= 512 && kShared <= 4, "tensor memory");
 };
 
 struct Params {
     int M, E, K, N, cols;      // cols: C's columns (N, or N / 2 for SwiGLU)
     int n_tiles, stages;       // channel tiles; stages of K
+    int ch_tiles;              // 128-channel tiles of the weight's scales
     int bf16;                  // HALF: bf16 (else f16)
-    int split;                 // blocks of a cluster that share a tile
+    int split;                 // blocks of a cluster (1, 2 for PAIR)
     const int32_t* offsets;
     const uint8_t* As;
     int pitch;                 // bytes of a row of As
-    const uint8_t* Bs;
-    int ktiles;                // scale tiles along K of one channel tile of Bs
+    int ktiles;                // the weight's scale tiles along K
     const float* a_scale;
     const float* b_scale;
     const float* bias;
@@ -97,6 +104,7 @@ struct Params {
 struct Maps {
     CUtensorMap a;             // activations [M][row bytes]
     CUtensorMap b;             // weights [E][N][row bytes]
+    CUtensorMap sb;            // the weights' scale tiles [E x channel tiles x K tiles][512 bytes]
 };
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -111,42 +119,84 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
 __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
 }
-// Scale tile (512 bytes) to four tensor-memory columns, in all four lane quarters.
+// Scale tile (512 bytes) to four tensor-memory columns, in all four lane quarters (PAIR: each block's
+// own tile to its own columns).
+template <int MODE>
 __device__ __forceinline__ void copy_scales(uint32_t tcol, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tcol), "l"(desc) : "memory");
+    if constexpr (MODE == PAIR)
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tcol),
+                     "l"(desc)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tcol),
+                     "l"(desc)
+                     : "memory");
 }
-// Instruction descriptors for n columns (a multiple of 16) and 128 rows. 16-bit: float32 D, A and B
+// Instruction descriptors for m rows (128, PAIR: 256) and n columns. 16-bit: float32 D, A and B
 // both f16 (0) or bf16 (1). 4-bit: A and B e2m1, scales e4m3 (0) or e8m0 (1 at bit 23), and which of a
 // column's four scale bytes come first (sf: A's at bit 29, B's at bit 4).
 template <int F>
-__device__ __forceinline__ uint32_t inst_desc(int n, int bf16) {
+__device__ __forceinline__ uint32_t inst_desc(int m, int n, int bf16) {
     if constexpr (F == HALF)
-        return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kCh >> 4) << 24);
-    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((F == MX ? 1u : 0u) << 23) | ((uint32_t)(kCh >> 7) << 27);
+        return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((F == MX ? 1u : 0u) << 23) | ((uint32_t)(m >> 7) << 27);
 }
-__device__ __forceinline__ void mma_half(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
-        "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+// One MMA over 32 bytes of K, issued by one elected lane of the warp: D (+)= A x B, both from shared
+// memory (PAIR: each block holds its 128 rows of A and D and half of B's columns).
+#define QG_MMA(GROUP, KIND, ...)                                                                           \
+    asm volatile(                                                                                           \
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"                     \
+        "@e tcgen05.mma.cta_group::" GROUP "." KIND ", p;\n\t}" ::"r"(d),                                      \
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), ##__VA_ARGS__                                                  \
+        : "memory")
+template <int F, int MODE>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc) {
+    if constexpr (F == HALF) {
+        if constexpr (MODE == PAIR) QG_MMA("2", "kind::f16 [%0], %1, %2, %3");
+        else QG_MMA("1", "kind::f16 [%0], %1, %2, %3");
+    } else if constexpr (F == MX) {
+        if constexpr (MODE == PAIR) QG_MMA("2", "kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6]", "r"(sa), "r"(sb));
+        else QG_MMA("1", "kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6]", "r"(sa), "r"(sb));
+    } else {
+        if constexpr (MODE == PAIR) QG_MMA("2", "kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6]", "r"(sa), "r"(sb));
+        else QG_MMA("1", "kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6]", "r"(sa), "r"(sb));
+    }
 }
-template <int F>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc) {
-    if constexpr (F == MX)
+#undef QG_MMA
+// One arrival on `bar` (PAIR: in both blocks) once the copies and MMAs issued so far are done.
+template <int MODE>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    if constexpr (MODE == PAIR)
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+                     "h"((uint16_t)3)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+                     : "memory");
+}
+// Tiled TMA loads into this block's shared memory; with PAIR, `bar` may be the other block's.
+template <int MODE>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    if constexpr (MODE == PAIR)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d), "l"(a), "l"(b),
-            "r"(idesc), "r"(acc), "r"(sa), "r"(sb)
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
             : "memory");
     else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d), "l"(a),
-            "l"(b), "r"(idesc), "r"(acc), "r"(sa), "r"(sb)
-            : "memory");
+        ptx::tma_load_2d(dst, map, x, y, bar);
 }
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+template <int MODE>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    if constexpr (MODE == PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        ptx::tma_load_3d(dst, map, x, y, z, bar);
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
@@ -177,21 +227,45 @@ __device__ __forceinline__ uint32_t peer(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same without ordering other memory between the blocks: for shared memory that this block wrote
+// and its own tensor core reads, and tensor memory that it has read (a release at cluster scope
+// waits for every load of the thread in flight, a few thousand cycles beside the scales' prefetches).
+__device__ __forceinline__ void peer_signal(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ float peer_load(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
-// mbar_wait (ptx.cuh) for a barrier that other blocks of the cluster arrive on.
+// ptx.cuh's waits for barriers that other blocks of the cluster arrive on.
+__device__ __forceinline__ bool cluster_bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool cluster_bar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned int* status,
                                                  long long limit_ns) {
-    if (!ptx::mbar_wait(bar, parity, abort_flag, status, limit_ns)) return false;
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    return true;
+    if (cluster_bar_try(bar, parity)) return true;
+    return ptx::mbar_wait(bar, parity, abort_flag, status, limit_ns) && cluster_bar_try(bar, parity);
+}
+// A look that never suspends the warp.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 // True in one lane of the (converged) warp. The instructions that a single thread issues (TMA,
-// tcgen05.mma, tcgen05.cp) take their operands from warp-wide registers; under this predicate the
-// compiler knows that one lane is active and moves them there directly, under `lane == 0` it loops.
+// tcgen05.mma, tcgen05.cp) take their operands from warp-wide registers; elect.sync tells the
+// compiler that one lane is active (under `lane == 0` each of them measured 88 cycles).
 __device__ __forceinline__ bool elect_one() {
     uint32_t yes;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
@@ -199,7 +273,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 struct Tile {
-    int e, n0, m0, rows;       // expert, first channel, first row, rows (0: none)
+    int e, n0, m0, rows;       // expert, first channel (of this block), first row, rows
 };
 
 // Two neighbouring channels' values of the chunk's 16 rows, exchanged between the lanes of a pair: the
@@ -290,10 +364,11 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[16], int
     }
 }
 
-template <int F, int BN, bool SPLIT>
+template <int F, int BN, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-    using P = Plan<F, BN, SPLIT>;
+    using P = Plan<F, BN, MODE>;
     constexpr int S = P::kStages;
+    constexpr bool kPair = MODE == PAIR, kCluster = MODE != SOLO;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * P::kStage + P::kRed);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxStages + 10);
@@ -309,37 +384,49 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     auto acc_empty = [&](int b) { return bar(3 * kMaxStages + 2 + b); };   // the epilogue has read what the next MMAs overwrite
     const uint32_t drain = bar(3 * kMaxStages + 4), stall_bar = bar(3 * kMaxStages + 5);
     const uint32_t parts_ready = bar(3 * kMaxStages + 6), parts_taken = bar(3 * kMaxStages + 7);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto wait = [&](uint32_t b, uint32_t parity) { return ptx::mbar_wait(b, parity, abort_flag, p.status, p.wait_ns); };
-    const uint32_t rank = SPLIT ? cluster_rank() : 0u;
-    const int worker = SPLIT ? (int)blockIdx.x / p.split : (int)blockIdx.x;
-    const int workers = SPLIT ? (int)gridDim.x / p.split : (int)gridDim.x;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known to be uniform
+    auto wait = [&](uint32_t b, uint32_t parity) {
+        return kPair ? cluster_bar_wait(b, parity, abort_flag, p.status, p.wait_ns)
+                     : ptx::mbar_wait(b, parity, abort_flag, p.status, p.wait_ns);
+    };
+    const uint32_t rank = kCluster ? cluster_rank() : 0u;
+    const int worker = kCluster ? (int)blockIdx.x / p.split : (int)blockIdx.x;
+    const int workers = kCluster ? (int)gridDim.x / p.split : (int)gridDim.x;
     // this block's stages of every tile
-    const int ks0 = SPLIT ? (int)((long long)p.stages * rank / p.split) : 0;
-    const int nks = SPLIT ? (int)((long long)p.stages * (rank + 1) / p.split) - ks0 : p.stages;
+    const int ks0 = MODE == SPLIT ? (int)((long long)p.stages * rank / p.split) : 0;
+    const int nks = MODE == SPLIT ? (int)((long long)p.stages * (rank + 1) / p.split) - ks0 : p.stages;
+    // PAIR: block 0's barriers gather both blocks' copies, scales and epilogues for the MMAs it issues
+    auto lead = [&](uint32_t b) { return kPair ? peer(b, 0) : b; };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             ptx::mbar_init(full(s), 1);
-            ptx::mbar_init(full_sc(s), BN == 256 ? 2 : 1);   // one warp, or one a half
+            ptx::mbar_init(full_sc(s), kPair ? 4 : 1);   // one warp (PAIR: one a half, in both blocks)
             ptx::mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(acc_full(b), 1);
-            ptx::mbar_init(acc_empty(b), kEpiWarps);
+            ptx::mbar_init(acc_empty(b), kPair ? 2 * kEpiWarps : kEpiWarps);
         }
         ptx::mbar_init(drain, 1);
         ptx::mbar_init(stall_bar, 1);
-        ptx::mbar_init(parts_ready, SPLIT ? kEpiWarps * p.split : 1);
-        ptx::mbar_init(parts_taken, SPLIT ? kEpiWarps * p.split : 1);
+        ptx::mbar_init(parts_ready, kEpiWarps * p.split);
+        ptx::mbar_init(parts_taken, kEpiWarps * p.split);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ptx::prefetch_tmap(&maps.a);
         ptx::prefetch_tmap(&maps.b);
+        if (F != HALF) ptx::prefetch_tmap(&maps.sb);
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(tmem_slot)), "r"(512) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        // (one block fits an SM, so the columns are free; PAIR: both blocks take part)
+        if constexpr (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(tmem_slot)), "r"(512) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(tmem_slot)), "r"(512) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     if (p.offsets && warp == 2) {
         // group starts and the tiles before each group
@@ -363,11 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
         }
     }
     tc_fence_before();
-    if constexpr (SPLIT) cluster_sync();   // the peers' barriers are initialized before anyone arrives on them
+    if constexpr (kCluster) cluster_sync();   // the peers' barriers are initialized before anyone arrives on them
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const int dense_m = (p.M + BN - 1) / BN;
+    // the MMA's columns for a tile of `rows` rows
+    auto columns = [](int rows) { return kPair ? (rows + 31) / 32 * 32 : (rows + 15) / 16 * 16; };
     const int total = p.offsets ? before[p.E] : dense_m * p.n_tiles;
     // Tile t: groups in order, in a group the row tiles of a channel tile side by side (they share its
     // weights).
@@ -388,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             hi = max(start[a + 1], lo);
             mt = (hi - lo + BN - 1) / BN;
         }
-        x.n0 = t / mt * kCh;
+        x.n0 = t / mt * P::kTileCh + (kPair ? (int)rank * kCh : 0);      // this block's channels
         x.m0 = lo + t % mt * BN;
         x.rows = min(BN, hi - x.m0);
         return x;
@@ -402,154 +491,207 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             bool stop = false;
             for (int t = worker; t < total && !stop; t += workers) {
                 const Tile x = tile_of(t);
-                const int boxes = (x.rows + P::kBoxRows - 1) / P::kBoxRows;
-                const uint8_t* bs = F == HALF ? nullptr : p.Bs + ((size_t)x.e * p.n_tiles + x.n0 / kCh) * p.ktiles * 512;
+                // PAIR: each block brings the rows of its half of the MMA's columns
+                const int mine = kPair ? columns(x.rows) / 2 : x.rows, first = x.m0 + (kPair ? (int)rank * mine : 0);
+                const int boxes = (mine + P::kBoxRows - 1) / P::kBoxRows;
+                const uint32_t bytes = (uint32_t)(P::kA + boxes * P::kBoxRows * kRowBytes + P::kSA) * (kPair ? 2u : 1u);
+                const int tiles0 = (x.e * p.ch_tiles + x.n0 / kCh) * p.ktiles;      // the channels' first scale tile
                 for (int i = 0; i < nks; ++i) {
                     if (*abort_flag || (g >= S && !wait(empty(s), ph ^ 1u))) {
                         stop = true;
                         break;
                     }
-                    const int k = ks0 + i;
-                    const uint32_t st = ring + (uint32_t)s * P::kStage;
-                    const int chunks = min(P::kChunks, p.ktiles - k * P::kChunks);     // (16-bit: none)
-                    const uint32_t sbytes = F == HALF ? 0u : (uint32_t)chunks * 512u;
-                    ptx::mbar_expect_tx(full(s), (uint32_t)P::kA + (uint32_t)(boxes * P::kBoxRows * kRowBytes) + sbytes);
-                    const int kx = k * (F == HALF ? 64 : kRowBytes);
-                    ptx::tma_load_3d(st, &maps.b, kx, x.n0, x.e, full(s));
+                    const int k = ks0 + i, kx = k * (F == HALF ? 64 : kRowBytes);
+                    const uint32_t st = ring + (uint32_t)s * P::kStage, done = lead(full(s));
+                    if (rank == 0 || !kPair) ptx::mbar_expect_tx(full(s), bytes);
+                    load_3d<MODE>(st, &maps.b, kx, x.n0, x.e, done);
                     for (int b = 0; b < boxes; ++b)
-                        ptx::tma_load_2d(st + P::kA + b * (P::kBoxRows * kRowBytes), &maps.a, kx, x.m0 + b * P::kBoxRows, full(s));
-                    if (F != HALF) ptx::bulk_load(st + P::kA + P::kB, bs + (size_t)k * P::kSA, sbytes, full(s));
+                        load_2d<MODE>(st + P::kA + b * (P::kBoxRows * kRowBytes), &maps.a, kx, first + b * P::kBoxRows, done);
+                    // (a stage past the channels' last scale tile brings tiles that no MMA uses)
+                    if (F != HALF) load_2d<MODE>(st + P::kA + P::kB, &maps.sb, 0, tiles0 + k * P::kChunks, done);
                     ++g;
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
-            if (*abort_flag)   // the copies issued land before the block exits
-                for (int i = max(0, g - S); i < g; ++i) {
+            // PAIR: the last reports of finished stages have arrived here before the block leaves
+            if (kPair && !stop)
+                for (int i = max(0, g - S); i < g; ++i) wait(empty(i % S), (uint32_t)(i / S) & 1u);
+            if (*abort_flag && (rank == 0 || !kPair))
+                // the copies issued land before the block (PAIR: the cluster, whose copies report here; the
+                // other block may have issued fewer or more, so the wait is short and for every slot) exits
+                for (int i = max(0, g - S); i < (kPair ? max(0, g - S) + S : g); ++i) {
                     volatile int never = 0;
-                    ptx::mbar_wait(full(i % S), (uint32_t)(i / S) & 1u, &never, p.status);
+                    ptx::mbar_wait(full(i % S), (uint32_t)(i / S) & 1u, &never, p.status, kPair ? kDrainNs : ptx::kWaitNs);
                 }
         }
     } else if (warp == kScaleWarp || warp == kScaleWarp + 1) {
         // ---------------- the activations' scales
         // A lane takes the 16-byte pieces (two stages' scales in MXFP4, one's in NVFP4) of the four rows
-        // r, r + 32, r + 64, r + 96 of a half of the tile, the next pieces while it writes these, and writes
-        // each scale tile's four words of its rows, which lie side by side there, as 16 bytes. (Bringing
-        // the words in one by one with 4-byte asynchronous copies took as long as the stage's MMAs:
-        // each touches another line of the cache.) The warps take a half each, or turns.
+        // r, r + 32, r + 64, r + 96 of a half of the tile and writes each scale tile's four words of its
+        // rows, which lie side by side there, as 16 bytes. (Bringing the words in one by one with 4-byte
+        // asynchronous copies took as long as the stage's MMAs: each touches another line of the cache.)
+        // The loads run as far ahead as the ring's, behind whose copies they queue, across tiles, in sets
+        // of registers taken in turn (passing them on from set to set would wait for them). The warps
+        // take a half each (PAIR), or every other piece.
         if constexpr (F != HALF) {
-            constexpr bool kTurns = BN < 256;
-            constexpr int kStep = kTurns ? 2 : 1;
+            constexpr bool kTurns = !kPair;
+            constexpr int kStep = kTurns ? 2 : 1, kPer = F == MX ? 2 : 1;      // pieces, stages per piece
             const int w = warp - kScaleWarp, half = kTurns ? 0 : w;
-            int s = 0, g = 0;
-            uint32_t ph = 0;
-            bool stop = false;
-            for (int t = worker; t < total && !stop; t += workers) {
-                const Tile x = tile_of(t);
-                uint4 now[4], next[4];
-                const uint8_t* src = p.As + (size_t)(x.m0 + 128 * half + lane) * p.pitch;
-                auto fetch = [&](int piece, uint4 (&v)[4]) {
+            int first = ks0 / kPer;
+            const int last = (ks0 + nks - 1) / kPer;
+            if (kTurns && (first & 1) != w) ++first;
+            // the next loads: piece qf of tile tf
+            int tf = first <= last ? worker : total, qf = first, rows = 0;
+            const uint8_t* src = nullptr;
+            auto open_tile = [&]() {
+                if (tf >= total) return;
+                const Tile x = tile_of(tf);
+                rows = x.rows - 128 * half - lane;           // row 32 j of this lane is the tile's while 32 j < rows
+                src = p.As + (size_t)(x.m0 + 128 * half + lane) * p.pitch;
+            };
+            auto fetch = [&](uint4 (&v)[4]) {
+                if (tf >= total) return;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[j] = 128 * half + 32 * j + lane < x.rows
-                                   ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)(32 * j) * p.pitch) + piece)
-                                   : make_uint4(0, 0, 0, 0);
-                };
-                const int last = (ks0 + nks - 1) / (F == MX ? 2 : 1);
-                int have = -1;
-                for (int i = 0; i < nks; ++i) {
-                    const int k = ks0 + i, piece = F == MX ? k >> 1 : k;
-                    if (!kTurns || (piece & 1) == w) {
-                        if (piece != have) {
-                            if (have < 0) fetch(piece, now);
-                            else
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) now[j] = next[j];
-                            have = piece;
-                            if (piece + kStep <= last) fetch(piece + kStep, next);
-                        }
-                        const bool go = !*abort_flag && (g < S || wait(empty(s), ph ^ 1u));
-                        if (!__all_sync(0xffffffffu, go)) {
-                            stop = true;
-                            break;
-                        }
-                        const uint32_t dst = ring + (uint32_t)s * P::kStage + P::kA + P::kB + P::kSA + lane * 16;
-                        const bool second = F == MX && (k & 1);
-#pragma unroll
-                        for (int c = 0; c < P::kChunks; ++c) {
-                            auto word = [&](const uint4& v) {
-                                if (F == MX) return c == 0 ? (second ? v.z : v.x) : (second ? v.w : v.y);
-                                return c == 0 ? v.x : (c == 1 ? v.y : (c == 2 ? v.z : v.w));
-                            };
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c * P::kHalves + half) * 512),
-                                         "r"(word(now[0])), "r"(word(now[1])), "r"(word(now[2])), "r"(word(now[3]))
-                                         : "memory");
-                        }
-                        ptx::fence_proxy_async_smem();       // visible to the tensor core's copies
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(full_sc(s));
-                    }
-                    ++g;
-                    if (++s == S) { s = 0; ph ^= 1u; }
+                for (int j = 0; j < 4; ++j)
+                    v[j] = 32 * j < rows ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)(32 * j) * p.pitch) + qf) : make_uint4(0, 0, 0, 0);
+                qf += kStep;
+                if (qf > last) {
+                    qf = first;
+                    tf += workers;
+                    open_tile();
                 }
+            };
+            // the next pieces written: q of tile tu, whose first stage is the block's gb-th
+            int tu = tf, q = first, gb = 0;
+            auto write = [&](uint4 (&v)[4]) {
+                if (tu >= total) return false;
+#pragma unroll
+                for (int d = 0; d < kPer; ++d) {
+                    const int i = q * kPer + d - ks0;
+                    if (i < 0 || i >= nks) continue;
+                    const int g = gb + i, s = g % S;
+                    const bool go = !*abort_flag && (g < S || wait(empty(s), (uint32_t)(g / S - 1) & 1u));
+                    if (!__all_sync(0xffffffffu, go)) return false;
+                    const uint32_t dst = ring + (uint32_t)s * P::kStage + P::kA + P::kB + P::kSA + half * 512 + lane * 16;
+#pragma unroll
+                    for (int c = 0; c < P::kChunks; ++c) {
+                        constexpr int kWords = P::kChunks;       // words of a row per stage
+                        auto word = [&](const uint4& x) {
+                            const int i4 = d * kWords + c;
+                            return i4 == 0 ? x.x : (i4 == 1 ? x.y : (i4 == 2 ? x.z : x.w));
+                        };
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + c * P::kHalves * 512), "r"(word(v[0])),
+                                     "r"(word(v[1])), "r"(word(v[2])), "r"(word(v[3]))
+                                     : "memory");
+                    }
+                    ptx::fence_proxy_async_smem();       // visible to the tensor core's copies
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kPair) peer_signal(lead(full_sc(s)));
+                        else ptx::mbar_arrive(full_sc(s));
+                    }
+                }
+                fetch(v);
+                q += kStep;
+                if (q > last) {
+                    q = first;
+                    tu += workers;
+                    gb += nks;
+                }
+                return true;
+            };
+            constexpr int kSets = F == MX ? 4 : 6;
+            uint4 sets[kSets][4];
+            open_tile();
+#pragma unroll
+            for (int i = 0; i < kSets; ++i) fetch(sets[i]);
+            for (bool more = true; more;) {
+#pragma unroll
+                for (int i = 0; i < kSets; ++i) more = more && write(sets[i]);
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMA
-        if (elect_one()) {
+        // ---------------- MMA. The whole warp runs through this, so that the operands stay in warp-wide
+        // registers; each instruction elects its lane.
+        if (rank == 0 || !kPair) {
+            auto wait_all = [&](uint32_t b, uint32_t parity) {       // one answer for the warp
+                return __all_sync(0xffffffffu, wait(b, parity));
+            };
             int s = 0, tj = 0;
             uint32_t ph = 0;
             bool stop = false, issued = false;
-            if (p.stall) wait(stall_bar, 0u);      // diagnostic: runs out
-            const int kbytes = F == HALF ? 2 * p.K : p.K / 2;
+            // A stage's MMAs run in groups that share a scale tile: two MMAs in MXFP4, one in NVFP4 (16-bit:
+            // the whole stage). Copies and MMAs execute in the order of issue, and a copy issued just
+            // before the MMA that needs it leaves the tensor cores idle meanwhile, so each group's copies
+            // are issued ahead of the previous group's MMAs. Rows and halves past the tile's are copied
+            // too, whatever they hold: their columns are not read.
+            constexpr int kGroups = F == HALF ? 1 : P::kChunks;
             const uint64_t wdesc = sw128_desc(ring), adesc = sw128_desc(ring + P::kA), sdesc = scale_desc(ring + P::kA + P::kB);
+            auto copy_group = [&](int slot, int c) {
+                if constexpr (F != HALF) {
+                    const uint64_t at = sdesc + (uint64_t)(slot * (P::kStage >> 4));
+                    copy_scales<MODE>(tmem + P::kSaCol + 4 * c, at + c * 32);
+#pragma unroll
+                    for (int h = 0; h < P::kHalves; ++h)
+                        copy_scales<MODE>(tmem + P::kSbCol + 4 * (c * P::kHalves + h), at + (P::kChunks + c * P::kHalves + h) * 32);
+                }
+            };
+            if (p.stall) wait_all(stall_bar, 0u);      // diagnostic: runs out
+            const int kbytes = F == HALF ? 2 * p.K : p.K / 2;
             for (int t = worker; t < total && !stop; t += workers, ++tj) {
-                const Tile x = tile_of(t);
-                const uint32_t idesc = inst_desc<F>((x.rows + 15) / 16 * 16, p.bf16);
+                const int rows = __shfl_sync(0xffffffffu, tile_of(t).rows, 0);
+                const uint32_t idesc = inst_desc<F>(P::kTileCh, columns(rows), p.bf16);
                 const uint32_t acc = tmem + ((tj & 1) ? (uint32_t)P::kAcc1 : 0u);
                 // overlapping accumulators: the last tile's shared columns have been read; else: the
                 // accumulator's tile before the last has been read
-                if (P::kOverlap ? (tj >= 1 && !wait(acc_empty(0), (uint32_t)(tj - 1) & 1u))
-                                : (tj >= 2 && !wait(acc_empty(tj & 1), (uint32_t)((tj >> 1) - 1) & 1u)))
+                if (P::kOverlap ? (tj >= 1 && !wait_all(acc_empty(0), (uint32_t)(tj - 1) & 1u))
+                                : (tj >= 2 && !wait_all(acc_empty(tj & 1), (uint32_t)((tj >> 1) - 1) & 1u)))
                     break;
+                bool copied = false;       // the stage is in place and its first scales are on their way
                 for (int i = 0; i < nks; ++i) {
-                    if (!wait(full(s), ph) || (F != HALF && !wait(full_sc(s), ph))) {
-                        stop = true;
-                        break;
+                    if (!copied) {
+                        if (!wait_all(full(s), ph) || (F != HALF && !wait_all(full_sc(s), ph))) {
+                            stop = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        issued = true;
+                        copy_group(s, 0);
                     }
-                    tc_fence_after();
-                    issued = true;
                     const uint64_t at = (uint64_t)(s * (P::kStage >> 4));     // the stage, in descriptor units
                     const int steps = min(4, (kbytes - (ks0 + i) * kRowBytes) / 32);     // 32 bytes of K per MMA
+                    const int s1 = s + 1 == S ? 0 : s + 1;
+                    const uint32_t ph1 = s + 1 == S ? ph ^ 1u : ph;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (kk >= steps) break;
-                        const uint32_t add = (i | kk) != 0;
-                        if constexpr (F == HALF) {
-                            mma_half(acc, wdesc + at + 2 * kk, adesc + at + 2 * kk, idesc, add);
-                        } else {
-                            // a scale tile serves two MMAs (MXFP4) or one; rows and halves past the tile's
-                            // are copied too, whatever they hold: their columns are not read
-                            const int c = F == MX ? kk >> 1 : kk;
-                            if (F == NV || (kk & 1) == 0) {
-                                copy_scales(tmem + P::kSaCol + 4 * c, sdesc + at + c * 32);
-#pragma unroll
-                                for (int h = 0; h < P::kHalves; ++h)
-                                    copy_scales(tmem + P::kSbCol + 4 * (c * P::kHalves + h),
-                                                sdesc + at + (P::kChunks + c * P::kHalves + h) * 32);
+                    for (int gr = 0; gr < kGroups; ++gr) {
+                        // the next group's scales before this group's MMAs
+                        if (gr + 1 < kGroups) {
+                            copy_group(s, gr + 1);
+                        } else if (F != HALF) {
+                            copied = i + 1 < nks && __all_sync(0xffffffffu, bar_test(full(s1), ph1) && bar_test(full_sc(s1), ph1));
+                            if (copied) {
+                                tc_fence_after();
+                                copy_group(s1, 0);
                             }
+                        }
+#pragma unroll
+                        for (int kk = gr * (4 / kGroups); kk < (gr + 1) * (4 / kGroups); ++kk) {
+                            if (kk >= steps) break;
+                            const uint32_t add = (i | kk) != 0;
                             const uint32_t sf = F == MX ? 2u * (kk & 1) : 0u;
-                            mma_fp4<F>(acc, wdesc + at + 2 * kk, adesc + at + 2 * kk, idesc | sf << 29 | sf << 4,
-                                       tmem + P::kSaCol + 4 * c, tmem + P::kSbCol + 4 * c * P::kHalves, add);
+                            mma<F, MODE>(acc, wdesc + at + 2 * kk, adesc + at + 2 * kk, idesc | sf << 29 | sf << 4,
+                                         tmem + P::kSaCol + 4 * gr, tmem + P::kSbCol + 4 * gr * P::kHalves, add);
                         }
                     }
-                    mma_commit(empty(s));
-                    if (++s == S) { s = 0; ph ^= 1u; }
+                    mma_commit<MODE>(empty(s));
+                    s = s1;
+                    ph = ph1;
                 }
-                if (!stop) mma_commit(acc_full(tj & 1));
+                if (!stop) mma_commit<MODE>(acc_full(tj & 1));
             }
-            if (*abort_flag && issued) {   // the MMAs issued finish before their tensor memory is released
+            if (__any_sync(0xffffffffu, *abort_flag) && issued) {   // the MMAs issued finish before their tensor memory is released
                 volatile int never = 0;
-                mma_commit(drain);
+                mma_commit<MODE>(drain);
                 ptx::mbar_wait(drain, 0u, &never, p.status);
             }
         }
@@ -574,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + ((tj & 1) ? (uint32_t)P::kAcc1 : 0u);
             constexpr int kParts = BN / 32;      // chunks of 16 columns of each column half
-            if constexpr (SPLIT) {
+            if constexpr (MODE == SPLIT) {
                 // this block's partial sums [row][channel], once the peers have read the last tile's
                 if (tj > 0 && !__all_sync(0xffffffffu, cluster_wait(parts_taken, (uint32_t)(tj - 1) & 1u))) break;
                 for (int j = 0; j < kParts; ++j) {
@@ -627,16 +769,21 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                 const float bias = p.bias ? __ldg(p.bias + en) : 0.f;
 #pragma unroll 1
                 for (int j = 0; j < kParts; ++j) {
-                    // the shared columns of overlapping accumulators first: half 0 upwards, half 1 downwards
-                    const int c0 = 16 * (h == 0 ? j : 2 * kParts - 1 - j);
+                    // chunks alternate between the halves; overlapping accumulators share the first one's
+                    // last columns and the second one's first: those go first
+                    const int i2 = 2 * j + h, c0 = 16 * (P::kOverlap && !(tj & 1) ? 2 * kParts - 1 - i2 : i2);
                     const int live = min(16, x.rows - c0);       // rows of this chunk (none: <= 0)
                     float v[16];
                     __syncwarp();
                     if (live > 0) tmem_ld16(acc + (uint32_t)c0, v);
-                    if (P::kOverlap ? j == 2 : j == kParts - 1) {
+                    if (j == (P::kOverlap ? (P::kShared + 1) / 2 - 1 : kParts - 1)) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(acc_empty(P::kOverlap ? 0 : tj & 1));
+                        if (lane == 0) {
+                            const uint32_t b = acc_empty(P::kOverlap ? 0 : tj & 1);
+                            if constexpr (kPair) peer_signal(lead(b));
+                            else ptx::mbar_arrive(b);
+                        }
                     }
                     if (live <= 0) continue;
                     const int m = x.m0 + c0;
@@ -656,11 +803,12 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     }
     tc_fence_before();
     __syncthreads();
-    if constexpr (SPLIT) cluster_sync();   // no block leaves while a peer may still read its partial sums
+    if constexpr (kCluster) cluster_sync();   // no block leaves while a peer may still reach its memory
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
@@ -683,29 +831,44 @@ inline cudaError_t make_map(CUtensorMap* map, const void* base, int form, int bf
                : cudaErrorInvalidValue;
 }
 
+// The weights' scale tiles as a 2-D tensor of 512-byte rows; boxes of a stage's tiles.
+inline cudaError_t make_scale_map(CUtensorMap* map, const void* base, size_t tiles, int chunks) {
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {128, (cuuint64_t)tiles};
+    const cuuint64_t strides[1] = {512};
+    const cuuint32_t box[2] = {128, (cuuint32_t)chunks};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 // The launch for a tile height and cluster size; tiles: at least as many as the call has.
-template <int F, int BN, bool SPLIT>
+template <int F, int BN, int MODE>
 cudaError_t launch(const GroupGemmArgs& a, int fmt, int split, long long tiles, cudaStream_t s) {
-    using P = Plan<F, BN, SPLIT>;
+    using P = Plan<F, BN, MODE>;
     const int bf16 = fmt == GF_BF16, block = F == MX ? 32 : 16;
     Maps maps;
     cudaError_t e = make_map(&maps.a, a.A, F, bf16, a.K, a.M, 0, P::kBoxRows);
     if (e == cudaSuccess) e = make_map(&maps.b, a.B, F, bf16, a.K, a.N, a.E, kCh);
+    const int ch_tiles = (a.N + kCh - 1) / kCh, ktiles = F == HALF ? 0 : fp4::scale_ktiles(a.K, block);
+    if (F == HALF) maps.sb = maps.b;   // unused
+    else if (e == cudaSuccess) e = make_scale_map(&maps.sb, a.Bs, (size_t)a.E * ch_tiles * ktiles, P::kChunks);
     if (e != cudaSuccess) return e;
     Params p{};
     p.M = a.M; p.E = a.E; p.K = a.K; p.N = a.N;
     p.cols = a.act == ACT_SWIGLU ? a.N / 2 : a.N;
-    p.n_tiles = (a.N + kCh - 1) / kCh;
+    p.n_tiles = (a.N + P::kTileCh - 1) / P::kTileCh;
+    p.ch_tiles = ch_tiles;
     p.stages = F == HALF ? a.K / 64 : (a.K + 255) / 256;
     p.bf16 = bf16;
     p.split = split;
     p.offsets = a.offsets;
     p.As = static_cast<const uint8_t*>(a.As);
-    p.Bs = static_cast<const uint8_t*>(a.Bs);
-    if (F != HALF) {
-        p.pitch = fp4::scale_pitch(a.K, block);
-        p.ktiles = fp4::scale_ktiles(a.K, block);
-    }
+    p.pitch = F == HALF ? 0 : fp4::scale_pitch(a.K, block);
+    p.ktiles = ktiles;
     p.a_scale = a.a_scale; p.b_scale = a.b_scale; p.bias = a.bias;
     p.residual = a.residual;
     p.C = a.C;
@@ -714,7 +877,7 @@ cudaError_t launch(const GroupGemmArgs& a, int fmt, int split, long long tiles, 
     if (!p.status) return cudaErrorUnknown;
     p.wait_ns = option_wait_ns();
     p.stall = option_stall();
-    auto kern = group_gemm_kernel<F, BN, SPLIT>;
+    auto kern = group_gemm_kernel<F, BN, MODE>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kSmem);
     if (e != cudaSuccess) return e;
     const long long most = kTargetSms / split;
@@ -728,7 +891,7 @@ cudaError_t launch(const GroupGemmArgs& a, int fmt, int split, long long tiles, 
     attr[0].val.clusterDim.x = (unsigned)split;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = SPLIT ? 1 : 0;
+    cfg.numAttrs = MODE == SOLO ? 0 : 1;
     return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
@@ -739,22 +902,21 @@ inline int group_rows(const GroupGemmArgs& a) {
     const int used = a.M < a.E ? a.M : a.E;
     return (a.M + used - 1) / used;
 }
-inline long long most_tiles(const GroupGemmArgs& a, int bn) {
-    const long long groups = a.offsets ? (a.M < a.E ? a.M : a.E) : 1;
-    return (a.M / bn + groups) * ((a.N + kCh - 1) / kCh);
-}
-
 template <int F>
 cudaError_t launch_form(const GroupGemmArgs& a, int fmt, cudaStream_t s) {
     const int rows = group_rows(a), stages = F == HALF ? a.K / 64 : (a.K + 255) / 256;
     const int bn = rows <= 32 ? 32 : (rows <= 128 ? 128 : 256);
-    const long long tiles = a.offsets ? most_tiles(a, bn) : (long long)((a.M + bn - 1) / bn) * ((a.N + kCh - 1) / kCh);
-    if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // output tiles: exact for the dense product, else at least as many as there are
+    const int channels = bn == 256 ? 2 * kCh : kCh;
+    const long long groups = a.offsets ? (a.M < a.E ? a.M : a.E) : 1;
+    const long long m_tiles = a.offsets ? a.M / bn + groups : (a.M + bn - 1) / bn;
+    const long long tiles = m_tiles * ((a.N + channels - 1) / channels);
+    if (tiles > 0x7fffffffLL || (long long)a.E * ((a.N + kCh - 1) / kCh) * ((a.K + 63) / 64) > 0x7fffffffLL) return cudaErrorInvalidValue;
     int split = 1;
     while (bn < 256 && split < kMaxSplit && tiles * split * 2 <= kTargetSms && stages / (split * 2) >= 2) split *= 2;
-    if (bn == 32) return split > 1 ? launch<F, 32, true>(a, fmt, split, tiles, s) : launch<F, 32, false>(a, fmt, 1, tiles, s);
-    if (bn == 128) return split > 1 ? launch<F, 128, true>(a, fmt, split, tiles, s) : launch<F, 128, false>(a, fmt, 1, tiles, s);
-    return launch<F, 256, false>(a, fmt, 1, tiles, s);
+    if (bn == 32) return split > 1 ? launch<F, 32, SPLIT>(a, fmt, split, tiles, s) : launch<F, 32, SOLO>(a, fmt, 1, tiles, s);
+    if (bn == 128) return split > 1 ? launch<F, 128, SPLIT>(a, fmt, split, tiles, s) : launch<F, 128, SOLO>(a, fmt, 1, tiles, s);
+    return launch<F, 256, PAIR>(a, fmt, 2, tiles, s);
 }
 
 }  // namespace gg
