@@ -788,8 +788,9 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                     if (live <= 0) continue;
                     const int m = x.m0 + c0;
                     if (p.a_scale) {
+                        const float as = __ldg(p.a_scale + m + min(lane & 15, live - 1));
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] *= __ldg(p.a_scale + m + min(i, live - 1));
+                        for (int i = 0; i < 16; ++i) v[i] *= __shfl_sync(0xffffffffu, as, i);
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], ws, bias);
