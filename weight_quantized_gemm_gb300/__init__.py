@@ -108,11 +108,10 @@ def _ptr(x):
     """Device (or host) address of a tensor, an int address, or None."""
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
-    return x.ctypes.data      # a numpy array (host memory)
+    except AttributeError:
+        return x if isinstance(x, int) else x.ctypes.data      # a numpy array (host memory)
 
 
 def _on_device(*xs) -> int:
@@ -124,10 +123,20 @@ def _on_device(*xs) -> int:
     return int(where.pop()) if where else 0
 
 
+def _current_stream():
+    """torch's current stream as a cudaStream_t. The raw handle is asked for, since a Stream object
+    for every call takes longer (3 us) than the call itself."""
+    global _current_stream
+    import torch
+    torch.cuda.current_stream()      # brings CUDA up
+    handle, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _current_stream = lambda: handle(device())
+    return _current_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -24,8 +24,9 @@
 // groups' tile counts once, and finds a tile's group by binary search.
 //
 // SPLIT: with too few tiles to fill the GPU, the blocks of a cluster share a tile, each taking a part
-// of K; partial sums meet in distributed shared memory, where every block adds its part of the
-// channels over the blocks in rank order. No workspace, no atomics, one launch.
+// of K. Each block is sent its share of the channels' partial sums by all of them (asynchronous stores
+// to distributed shared memory that a barrier counts: no fence between blocks) and adds them in rank
+// order. No workspace, no atomics, one launch. A cluster has one tile at most.
 //
 // Every wait is bounded (see ptx.cuh); after an abort the copies and MMAs in flight are waited for,
 // and a cluster's blocks leave together.
@@ -64,7 +65,8 @@ struct Plan {
     static constexpr int kA = kCh * kRowBytes, kB = kBRows * kRowBytes;
     static constexpr int kSA = kChunks * 512, kSB = kChunks * kHalves * 512;
     static constexpr int kStage = kA + kB + kSA + kSB;
-    static constexpr int kRed = MODE == SPLIT ? BN * kCh * 4 : 0;                  // this block's partial sums
+    static constexpr int kRedRow = BN + 4;                                 // SPLIT: a channel's partial sums (padded)
+    static constexpr int kRed = MODE == SPLIT ? kCh * kRedRow * 4 : 0;     // [block][channel of the share][row]
     static constexpr int kTables = 2 * (1024 + 1) * 4;                     // group starts and tile counts
     static constexpr int kRoom = (int)kSmemMax - kTail - kTables - kRed;
     static constexpr int kStages = kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
@@ -215,28 +217,26 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // Address of this block's shared-memory location in the cluster's block `rank`.
 __device__ __forceinline__ uint32_t peer(uint32_t saddr, uint32_t rank) {
     uint32_t r;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void peer_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// The same without ordering other memory between the blocks: for shared memory that this block wrote
-// and its own tensor core reads, and tensor memory that it has read (a release at cluster scope
-// waits for every load of the thread in flight, a few thousand cycles beside the scales' prefetches).
+// An arrival on a barrier of the cluster, without ordering other memory between the blocks: for shared
+// memory that this block wrote and its own tensor core reads, and tensor memory that it has read (a
+// release at cluster scope waits for every load of the thread in flight, a few thousand cycles
+// beside the scales' prefetches).
 __device__ __forceinline__ void peer_signal(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ float peer_load(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+// Four values to another block's shared memory, counted in bytes by a barrier of that block.
+__device__ __forceinline__ void peer_store4(uint32_t addr, float a, float b, float c, float d, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr), "f"(a), "f"(b),
+                 "f"(c), "f"(d), "r"(bar)
+                 : "memory");
 }
 // ptx.cuh's waits for barriers that other blocks of the cluster arrive on.
 __device__ __forceinline__ bool cluster_bar_try(uint32_t bar, uint32_t parity) {
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     auto acc_full = [&](int b) { return bar(3 * kMaxStages + b); };   // the accumulator's MMAs are done
     auto acc_empty = [&](int b) { return bar(3 * kMaxStages + 2 + b); };   // the epilogue has read what the next MMAs overwrite
     const uint32_t drain = bar(3 * kMaxStages + 4), stall_bar = bar(3 * kMaxStages + 5);
-    const uint32_t parts_ready = bar(3 * kMaxStages + 6), parts_taken = bar(3 * kMaxStages + 7);
+    const uint32_t parts = bar(3 * kMaxStages + 6);       // SPLIT: the partial sums of this block's channels arrived
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known to be uniform
     auto wait = [&](uint32_t b, uint32_t parity) {
         return kPair ? cluster_bar_wait(b, parity, abort_flag, p.status, p.wait_ns)
@@ -398,7 +398,57 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     // PAIR: block 0's barriers gather both blocks' copies, scales and epilogues for the MMAs it issues
     auto lead = [&](uint32_t b) { return kPair ? peer(b, 0) : b; };
 
-    if (threadIdx.x == 0) {
+    const int dense_m = (p.M + BN - 1) / BN;
+    // the MMA's columns for a tile of `rows` rows
+    auto columns = [](int rows) { return kPair ? (rows + 31) / 32 * 32 : (rows + 15) / 16 * 16; };
+    // Tile t: groups in order, in a group the row tiles of a channel tile side by side (they share its
+    // weights).
+    auto tile_of = [&](int t) {
+        Tile x;
+        int lo = 0, hi = p.M, mt = dense_m;
+        x.e = 0;
+        if (p.offsets) {
+            int a = 0, b = p.E;            // before[a] <= t < before[b]
+            while (b - a > 1) {
+                const int c = (a + b) >> 1;
+                if (before[c] <= t) a = c;
+                else b = c;
+            }
+            x.e = a;
+            t -= before[a];
+            lo = start[a];
+            hi = max(start[a + 1], lo);
+            mt = (hi - lo + BN - 1) / BN;
+        }
+        x.n0 = t / mt * P::kTileCh + (kPair ? (int)rank * kCh : 0);      // this block's channels
+        x.m0 = lo + t % mt * BN;
+        x.rows = min(BN, hi - x.m0);
+        return x;
+    };
+
+    // Stage i of this block's part of tile x into slot s.
+    auto issue = [&](const Tile& x, int i, int s) {
+        // PAIR: each block brings the rows of its half of the MMA's columns
+        const int mine = kPair ? columns(x.rows) / 2 : x.rows, first = x.m0 + (kPair ? (int)rank * mine : 0);
+        const int boxes = (mine + P::kBoxRows - 1) / P::kBoxRows;
+        const int k = ks0 + i, kx = k * (F == HALF ? 64 : kRowBytes);
+        const uint32_t st = ring + (uint32_t)s * P::kStage, done = lead(full(s));
+        if (rank == 0 || !kPair)
+            ptx::mbar_expect_tx(full(s), (uint32_t)(P::kA + boxes * P::kBoxRows * kRowBytes + P::kSA) * (kPair ? 2u : 1u));
+        load_3d<MODE>(st, &maps.b, kx, x.n0, x.e, done);
+        for (int b = 0; b < boxes; ++b)
+            load_2d<MODE>(st + P::kA + b * (P::kBoxRows * kRowBytes), &maps.a, kx, first + b * P::kBoxRows, done);
+        // (a stage past the channels' last scale tile brings tiles that no MMA uses)
+        if (F != HALF)
+            load_2d<MODE>(st + P::kA + P::kB, &maps.sb, 0, (x.e * p.ch_tiles + x.n0 / kCh) * p.ktiles + k * P::kChunks, done);
+    };
+
+    bool sent = false;   // SPLIT: this thread has waited for the peers' barriers
+    // Stages of the first tile that are loaded before the block barrier: where neither the tile table
+    // nor another block is needed. (The same in every lane, or the compiler takes each TMA instruction's
+    // operands for the lane's own.)
+    const int ahead = !kPair && !p.offsets && worker < dense_m * p.n_tiles ? min(S, nks) : 0;
+    if (warp == 0 && elect_one()) {
         for (int s = 0; s < S; ++s) {
             ptx::mbar_init(full(s), 1);
             ptx::mbar_init(full_sc(s), kPair ? 4 : 1);   // one warp (PAIR: one a half, in both blocks)
@@ -410,13 +460,16 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
         }
         ptx::mbar_init(drain, 1);
         ptx::mbar_init(stall_bar, 1);
-        ptx::mbar_init(parts_ready, kEpiWarps * p.split);
-        ptx::mbar_init(parts_taken, kEpiWarps * p.split);
+        ptx::mbar_init(parts, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         ptx::prefetch_tmap(&maps.a);
         ptx::prefetch_tmap(&maps.b);
         if (F != HALF) ptx::prefetch_tmap(&maps.sb);
+        if (ahead > 0) {
+            const Tile x = tile_of(worker);
+            for (int i = 0; i < ahead; ++i) issue(x, i, i);
+        }
     }
     if (warp == 1) {
         // (one block fits an SM, so the columns are free; PAIR: both blocks take part)
@@ -450,65 +503,27 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
         }
     }
     tc_fence_before();
-    if constexpr (kCluster) cluster_sync();   // the peers' barriers are initialized before anyone arrives on them
+    // the peers' barriers are initialized before anyone arrives on them (SPLIT: the wait comes later)
+    if constexpr (kCluster) cluster_arrive();
+    if constexpr (kPair) cluster_wait();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const int dense_m = (p.M + BN - 1) / BN;
-    // the MMA's columns for a tile of `rows` rows
-    auto columns = [](int rows) { return kPair ? (rows + 31) / 32 * 32 : (rows + 15) / 16 * 16; };
     const int total = p.offsets ? before[p.E] : dense_m * p.n_tiles;
-    // Tile t: groups in order, in a group the row tiles of a channel tile side by side (they share its
-    // weights).
-    auto tile_of = [&](int t) {
-        Tile x;
-        int lo = 0, hi = p.M, mt = dense_m;
-        x.e = 0;
-        if (p.offsets) {
-            int a = 0, b = p.E;            // before[a] <= t < before[b]
-            while (b - a > 1) {
-                const int c = (a + b) >> 1;
-                if (before[c] <= t) a = c;
-                else b = c;
-            }
-            x.e = a;
-            t -= before[a];
-            lo = start[a];
-            hi = max(start[a + 1], lo);
-            mt = (hi - lo + BN - 1) / BN;
-        }
-        x.n0 = t / mt * P::kTileCh + (kPair ? (int)rank * kCh : 0);      // this block's channels
-        x.m0 = lo + t % mt * BN;
-        x.rows = min(BN, hi - x.m0);
-        return x;
-    };
-
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     if (warp == 0) {
         // ---------------- TMA
         if (elect_one()) {
-            int g = 0, s = 0;
-            uint32_t ph = 0;
+            int g = ahead, s = ahead % S;
+            uint32_t ph = (uint32_t)(ahead / S) & 1u;
             bool stop = false;
             for (int t = worker; t < total && !stop; t += workers) {
                 const Tile x = tile_of(t);
-                // PAIR: each block brings the rows of its half of the MMA's columns
-                const int mine = kPair ? columns(x.rows) / 2 : x.rows, first = x.m0 + (kPair ? (int)rank * mine : 0);
-                const int boxes = (mine + P::kBoxRows - 1) / P::kBoxRows;
-                const uint32_t bytes = (uint32_t)(P::kA + boxes * P::kBoxRows * kRowBytes + P::kSA) * (kPair ? 2u : 1u);
-                const int tiles0 = (x.e * p.ch_tiles + x.n0 / kCh) * p.ktiles;      // the channels' first scale tile
-                for (int i = 0; i < nks; ++i) {
+                for (int i = t == worker ? ahead : 0; i < nks; ++i) {
                     if (*abort_flag || (g >= S && !wait(empty(s), ph ^ 1u))) {
                         stop = true;
                         break;
                     }
-                    const int k = ks0 + i, kx = k * (F == HALF ? 64 : kRowBytes);
-                    const uint32_t st = ring + (uint32_t)s * P::kStage, done = lead(full(s));
-                    if (rank == 0 || !kPair) ptx::mbar_expect_tx(full(s), bytes);
-                    load_3d<MODE>(st, &maps.b, kx, x.n0, x.e, done);
-                    for (int b = 0; b < boxes; ++b)
-                        load_2d<MODE>(st + P::kA + b * (P::kBoxRows * kRowBytes), &maps.a, kx, first + b * P::kBoxRows, done);
-                    // (a stage past the channels' last scale tile brings tiles that no MMA uses)
-                    if (F != HALF) load_2d<MODE>(st + P::kA + P::kB, &maps.sb, 0, tiles0 + k * P::kChunks, done);
+                    issue(x, i, s);
                     ++g;
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
@@ -699,10 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
         // ---------------- epilogue
         const int q = warp & 3, h = (warp - kEpiWarp) >> 2;
         const bool odd = lane & 1, glu = p.act == ACT_SWIGLU;
-        float* const part = reinterpret_cast<float*>(smem + S * P::kStage);
-        auto cluster_wait = [&](uint32_t b, uint32_t parity) {
-            return cluster_bar_wait(b, parity, abort_flag, p.status, p.wait_ns);
-        };
+        const float* const part = reinterpret_cast<const float*>(smem + S * P::kStage);
         auto store_one = [&](size_t at, float y) {
             if (p.residual)
                 y += p.c_dtype == DT_F32 ? load_c<DT_F32>(p.residual, at)
@@ -717,31 +729,31 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + ((tj & 1) ? (uint32_t)P::kAcc1 : 0u);
             constexpr int kParts = BN / 32;      // chunks of 16 columns of each column half
             if constexpr (MODE == SPLIT) {
-                // this block's partial sums [row][channel], once the peers have read the last tile's
-                if (tj > 0 && !__all_sync(0xffffffffu, cluster_wait(parts_taken, (uint32_t)(tj - 1) & 1u))) break;
+                const int share = kCh / p.split, ch = 32 * q + lane;      // channels of a block's share; this lane's
+                if (threadIdx.x == kEpiWarp * 32) ptx::mbar_expect_tx(parts, (uint32_t)(kCh * ((x.rows + 3) / 4 * 4) * 4));
+                cluster_wait();
+                sent = true;
+                const uint32_t to = peer(red + (uint32_t)(((int)rank * share + ch % share) * P::kRedRow) * 4, ch / share);
+                const uint32_t to_bar = peer(parts, ch / share);
                 for (int j = 0; j < kParts; ++j) {
                     const int c0 = 16 * (kParts * h + j);
                     if (c0 >= x.rows) break;
                     float v[16];
                     tmem_ld16(acc + (uint32_t)c0, v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) part[(c0 + i) * kCh + 32 * q + lane] = v[i];
+                    for (int i = 0; i < 16; i += 4)
+                        if (c0 + i < x.rows) peer_store4(to + (uint32_t)(c0 + i) * 4, v[i], v[i + 1], v[i + 2], v[i + 3], to_bar);
+                    __syncwarp();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    ptx::mbar_arrive(acc_empty(tj & 1));
-                    for (int r = 0; r < p.split; ++r) peer_arrive(peer(parts_ready, r));
-                }
-                if (!__all_sync(0xffffffffu, cluster_wait(parts_ready, (uint32_t)tj & 1u))) break;
+                if (!__all_sync(0xffffffffu, cluster_bar_wait(parts, 0u, abort_flag, p.status, p.wait_ns))) break;
                 // this block's share of the channels (a multiple of 16), all rows
-                const int share = kCh / p.split, count = x.rows * share;
+                const int count = x.rows * share;
                 for (int i0 = threadIdx.x - kEpiWarp * 32; i0 < (count + 31) / 32 * 32; i0 += kEpiThreads) {
-                    const int i = min(i0, count - 1), c = (int)rank * share + i % share, m = x.m0 + i / share, n = x.n0 + c;
+                    const int i = min(i0, count - 1), cl = i % share, m = x.m0 + i / share, n = x.n0 + (int)rank * share + cl;
                     float v[kMaxSplit];
 #pragma unroll
                     for (int r = 0; r < kMaxSplit; ++r)
-                        v[r] = r < p.split ? peer_load(peer(red + (uint32_t)((i / share) * kCh + c) * 4, r)) : 0.f;
+                        v[r] = r < p.split ? part[(r * share + cl) * P::kRedRow + i / share] : 0.f;
 #pragma unroll
                     for (int r = 1; r < kMaxSplit; ++r) v[0] += v[r];
                     const size_t en = (size_t)x.e * p.N + min(n, p.N - 1);
@@ -758,9 +770,6 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                         if (i0 < count && n < p.N) store_one((size_t)m * p.cols + n, y);
                     }
                 }
-                __syncwarp();          // (the loads above are complete: their values were used)
-                if (lane == 0)
-                    for (int r = 0; r < p.split; ++r) peer_arrive(peer(parts_taken, r));
             } else {
                 // (x is in registers of every lane; its chunk's rows are x.m0 + c0 + i)
                 const int n = x.n0 + 32 * q + lane;
@@ -804,7 +813,15 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     }
     tc_fence_before();
     __syncthreads();
-    if constexpr (kCluster) cluster_sync();   // no block leaves while a peer may still reach its memory
+    // No block leaves while a peer may still reach its memory. SPLIT: a block that has its sums has heard
+    // the last of its peers; one that gave up waits until they have left or given up too.
+    if (kPair || (MODE == SPLIT && *abort_flag)) {
+        if constexpr (MODE == SPLIT) {
+            if (warp < kEpiWarp || !sent) cluster_wait();       // the first phase, where it was not waited for
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
