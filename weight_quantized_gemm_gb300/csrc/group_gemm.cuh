@@ -48,7 +48,7 @@ constexpr int kRowBytes = 128;                     // K bytes of a row per stage
 constexpr int kCh = 128;                           // channels per tile
 constexpr int kMaxSplit = 8;
 constexpr int kMaxStages = 10;
-constexpr long long kDrainNs = 20000000;           // limit of a wait for copies in flight after an abort (PAIR)
+constexpr long long kDrainNs = 20000000;           // limit of a wait for copies in flight after an abort
 constexpr size_t kSmemMax = 232448;
 constexpr int kTail = 1024;                        // barriers
 
@@ -371,19 +371,18 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     constexpr bool kPair = MODE == PAIR, kCluster = MODE != SOLO;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * P::kStage + P::kRed);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kMaxStages + 10);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 10);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int32_t* start = reinterpret_cast<int32_t*>(smem + S * P::kStage + P::kRed + kTail);   // group starts, held to [0, M]
     int32_t* before = start + p.E + 1;                                                      // tiles before each group
     const uint32_t ring = ptx::smem_u32(smem), red = ring + S * P::kStage;
     auto bar = [&](int i) { return ptx::smem_u32(bars + i); };
-    auto full = [&](int s) { return bar(s); };                        // the stage's TMA copies landed
-    auto full_sc = [&](int s) { return bar(kMaxStages + s); };        // the activations' scales are in place
-    auto empty = [&](int s) { return bar(2 * kMaxStages + s); };      // the stage's MMAs are done
-    auto acc_full = [&](int b) { return bar(3 * kMaxStages + b); };   // the accumulator's MMAs are done
-    auto acc_empty = [&](int b) { return bar(3 * kMaxStages + 2 + b); };   // the epilogue has read what the next MMAs overwrite
-    const uint32_t drain = bar(3 * kMaxStages + 4), stall_bar = bar(3 * kMaxStages + 5);
-    const uint32_t parts = bar(3 * kMaxStages + 6);       // SPLIT: the partial sums of this block's channels arrived
+    auto full = [&](int s) { return bar(s); };                        // the stage's copies landed, the scales are in place
+    auto empty = [&](int s) { return bar(kMaxStages + s); };          // the stage's MMAs are done
+    auto acc_full = [&](int b) { return bar(2 * kMaxStages + b); };   // the accumulator's MMAs are done
+    auto acc_empty = [&](int b) { return bar(2 * kMaxStages + 2 + b); };   // the epilogue has read what the next MMAs overwrite
+    const uint32_t drain = bar(2 * kMaxStages + 4), stall_bar = bar(2 * kMaxStages + 5);
+    const uint32_t parts = bar(2 * kMaxStages + 6);       // SPLIT: the partial sums of this block's channels arrived
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known to be uniform
     auto wait = [&](uint32_t b, uint32_t parity) {
         return kPair ? cluster_bar_wait(b, parity, abort_flag, p.status, p.wait_ns)
@@ -450,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     const int ahead = !kPair && !p.offsets && worker < dense_m * p.n_tiles ? min(S, nks) : 0;
     if (warp == 0 && elect_one()) {
         for (int s = 0; s < S; ++s) {
-            ptx::mbar_init(full(s), 1);
-            ptx::mbar_init(full_sc(s), kPair ? 4 : 1);   // one warp (PAIR: one a half, in both blocks)
+            // the TMA warp, and one scale warp (PAIR: one a half in both blocks)
+            ptx::mbar_init(full(s), F == HALF ? 1 : (kPair ? 5 : 2));
             ptx::mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -532,11 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             if (kPair && !stop)
                 for (int i = max(0, g - S); i < g; ++i) wait(empty(i % S), (uint32_t)(i / S) & 1u);
             if (*abort_flag && (rank == 0 || !kPair))
-                // the copies issued land before the block (PAIR: the cluster, whose copies report here; the
-                // other block may have issued fewer or more, so the wait is short and for every slot) exits
+                // the copies issued land before the block (PAIR: the cluster, whose copies report here) exits;
+                // the scale warps, or the other block, may have left some of these phases open, so the
+                // wait is short
                 for (int i = max(0, g - S); i < (kPair ? max(0, g - S) + S : g); ++i) {
                     volatile int never = 0;
-                    ptx::mbar_wait(full(i % S), (uint32_t)(i / S) & 1u, &never, p.status, kPair ? kDrainNs : ptx::kWaitNs);
+                    ptx::mbar_wait(full(i % S), (uint32_t)(i / S) & 1u, &never, p.status, kDrainNs);
                 }
         }
     } else if (warp == kScaleWarp || warp == kScaleWarp + 1) {
@@ -602,8 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                     ptx::fence_proxy_async_smem();       // visible to the tensor core's copies
                     __syncwarp();
                     if (lane == 0) {
-                        if constexpr (kPair) peer_signal(lead(full_sc(s)));
-                        else ptx::mbar_arrive(full_sc(s));
+                        if constexpr (kPair) peer_signal(lead(full(s)));
+                        else ptx::mbar_arrive(full(s));
                     }
                 }
                 fetch(v);
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                 bool copied = false;       // the stage is in place and its first scales are on their way
                 for (int i = 0; i < nks; ++i) {
                     if (!copied) {
-                        if (!wait_all(full(s), ph) || (F != HALF && !wait_all(full_sc(s), ph))) {
+                        if (!wait_all(full(s), ph)) {
                             stop = true;
                             break;
                         }
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                         if (gr + 1 < kGroups) {
                             copy_group(s, gr + 1);
                         } else if (F != HALF) {
-                            copied = i + 1 < nks && __all_sync(0xffffffffu, bar_test(full(s1), ph1) && bar_test(full_sc(s1), ph1));
+                            copied = i + 1 < nks && __all_sync(0xffffffffu, bar_test(full(s1), ph1));
                             if (copied) {
                                 tc_fence_after();
                                 copy_group(s1, 0);
