@@ -112,26 +112,24 @@ struct Maps {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Shared-memory matrix descriptors: K-major rows of 128 bytes with the 128-byte swizzle (8-row atoms
-// 1024 bytes apart), and a 32 x 16-byte scale tile without swizzle (8-row groups 128 bytes apart).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
+// Shared-memory matrix descriptors, the high words: K-major rows of 128 bytes with the 128-byte
+// swizzle (8-row atoms 1024 bytes apart), and a 32 x 16-byte scale tile without swizzle (8-row groups 128
+// bytes apart). The low word is the address in units of 16 bytes (14 bits, so that adding offsets
+// inside shared memory never carries) and, for the rows, a leading offset of 1.
+constexpr uint32_t kRowsHi = (1024u >> 4) | (1u << 14) | (2u << 29), kScaleHi = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t rows_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t scale_lo(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4; }
 // Scale tile (512 bytes) to four tensor-memory columns, in all four lane quarters (PAIR: each block's
 // own tile to its own columns).
 template <int MODE>
-__device__ __forceinline__ void copy_scales(uint32_t tcol, uint64_t desc) {
+__device__ __forceinline__ void copy_scales(uint32_t tcol, uint32_t lo) {
     if constexpr (MODE == PAIR)
-        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tcol),
-                     "l"(desc)
+        asm volatile("{\n\t.reg .pred e;\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], x;\n\t}" ::"r"(tcol), "r"(lo), "n"(kScaleHi)
                      : "memory");
     else
-        asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tcol),
-                     "l"(desc)
+        asm volatile("{\n\t.reg .pred e;\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\telect.sync _|e, 0xffffffff;\n\t"
+                     "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], x;\n\t}" ::"r"(tcol), "r"(lo), "n"(kScaleHi)
                      : "memory");
 }
 // Instruction descriptors for m rows (128, PAIR: 256) and n columns. 16-bit: float32 D, A and B
@@ -144,24 +142,24 @@ __device__ __forceinline__ uint32_t inst_desc(int m, int n, int bf16) {
     return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((F == MX ? 1u : 0u) << 23) | ((uint32_t)(m >> 7) << 27);
 }
 // One MMA over 32 bytes of K, issued by one elected lane of the warp: D (+)= A x B, both from shared
-// memory (PAIR: each block holds its 128 rows of A and D and half of B's columns).
-#define QG_MMA(GROUP, KIND, ...)                                                                           \
-    asm volatile(                                                                                           \
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"                     \
-        "@e tcgen05.mma.cta_group::" GROUP "." KIND ", p;\n\t}" ::"r"(d),                                      \
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), ##__VA_ARGS__                                                  \
+// memory (PAIR: each block holds its 128 rows of A and D and half of B's columns). a, b: low words.
+#define QG_MMA(GROUP, KIND, ...)                                                                               \
+    asm volatile(                                                                                               \
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"               \
+        "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t@e tcgen05.mma.cta_group::" GROUP "." KIND ", p;\n\t}" ::"r"(d), \
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kRowsHi), ##__VA_ARGS__                                        \
         : "memory")
 template <int F, int MODE>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t acc) {
     if constexpr (F == HALF) {
-        if constexpr (MODE == PAIR) QG_MMA("2", "kind::f16 [%0], %1, %2, %3");
-        else QG_MMA("1", "kind::f16 [%0], %1, %2, %3");
+        if constexpr (MODE == PAIR) QG_MMA("2", "kind::f16 [%0], x, y, %3");
+        else QG_MMA("1", "kind::f16 [%0], x, y, %3");
     } else if constexpr (F == MX) {
-        if constexpr (MODE == PAIR) QG_MMA("2", "kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6]", "r"(sa), "r"(sb));
-        else QG_MMA("1", "kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6]", "r"(sa), "r"(sb));
+        if constexpr (MODE == PAIR) QG_MMA("2", "kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %3, [%6], [%7]", "r"(sa), "r"(sb));
+        else QG_MMA("1", "kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %3, [%6], [%7]", "r"(sa), "r"(sb));
     } else {
-        if constexpr (MODE == PAIR) QG_MMA("2", "kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6]", "r"(sa), "r"(sb));
-        else QG_MMA("1", "kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6]", "r"(sa), "r"(sb));
+        if constexpr (MODE == PAIR) QG_MMA("2", "kind::mxf4nvf4.block_scale.scale_vec::4X [%0], x, y, %3, [%6], [%7]", "r"(sa), "r"(sb));
+        else QG_MMA("1", "kind::mxf4nvf4.block_scale.scale_vec::4X [%0], x, y, %3, [%6], [%7]", "r"(sa), "r"(sb));
     }
 }
 #undef QG_MMA
@@ -641,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             // are issued ahead of the previous group's MMAs. Rows and halves past the tile's are copied
             // too, whatever they hold: their columns are not read.
             constexpr int kGroups = F == HALF ? 1 : P::kChunks;
-            const uint64_t wdesc = sw128_desc(ring), adesc = sw128_desc(ring + P::kA), sdesc = scale_desc(ring + P::kA + P::kB);
+            const uint32_t wdesc = rows_lo(ring), adesc = rows_lo(ring + P::kA), sdesc = scale_lo(ring + P::kA + P::kB);
             auto copy_group = [&](int slot, int c) {
                 if constexpr (F != HALF) {
-                    const uint64_t at = sdesc + (uint64_t)(slot * (P::kStage >> 4));
+                    const uint32_t at = sdesc + (uint32_t)(slot * (P::kStage >> 4));
                     copy_scales<MODE>(tmem + P::kSaCol + 4 * c, at + c * 32);
 #pragma unroll
                     for (int h = 0; h < P::kHalves; ++h)
@@ -673,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                         issued = true;
                         copy_group(s, 0);
                     }
-                    const uint64_t at = (uint64_t)(s * (P::kStage >> 4));     // the stage, in descriptor units
+                    const uint32_t at = (uint32_t)(s * (P::kStage >> 4));     // the stage, in descriptor units
                     const int steps = min(4, (kbytes - (ks0 + i) * kRowBytes) / 32);     // 32 bytes of K per MMA
                     const int s1 = s + 1 == S ? 0 : s + 1;
                     const uint32_t ph1 = s + 1 == S ? ph ^ 1u : ph;
