@@ -24,9 +24,9 @@
 // groups' tile counts once, and finds a tile's group by binary search.
 //
 // SPLIT: with too few tiles to fill the GPU, the blocks of a cluster share a tile, each taking a part
-// of K. Each block is sent its share of the channels' partial sums by all of them (asynchronous stores
-// to distributed shared memory that a barrier counts: no fence between blocks) and adds them in rank
-// order. No workspace, no atomics, one launch. A cluster has one tile at most.
+// of K. Each block is sent its share of the channels' partial sums by all of them (one bulk copy to
+// distributed shared memory each, counted by a barrier: no fence between blocks) and adds them in
+// rank order. No workspace, no atomics, one launch. A cluster has one tile at most.
 //
 // Every wait is bounded (see ptx.cuh); after an abort the copies and MMAs in flight are waited for,
 // and a cluster's blocks leave together.
@@ -65,8 +65,7 @@ struct Plan {
     static constexpr int kA = kCh * kRowBytes, kB = kBRows * kRowBytes;
     static constexpr int kSA = kChunks * 512, kSB = kChunks * kHalves * 512;
     static constexpr int kStage = kA + kB + kSA + kSB;
-    static constexpr int kRedRow = BN + 4;                                 // SPLIT: a channel's partial sums (padded)
-    static constexpr int kRed = MODE == SPLIT ? kCh * kRedRow * 4 : 0;     // [block][channel of the share][row]
+    static constexpr int kRed = MODE == SPLIT ? kCh * BN * 4 : 0;          // partial sums received, [block][row][channel of the share]
     static constexpr int kTables = 2 * (1024 + 1) * 4;                     // group starts and tile counts
     static constexpr int kRoom = (int)kSmemMax - kTail - kTables - kRed;
     static constexpr int kStages = kRoom / kStage < kMaxStages ? kRoom / kStage : kMaxStages;
@@ -230,10 +229,10 @@ __device__ __forceinline__ uint32_t peer(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void peer_signal(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Four values to another block's shared memory, counted in bytes by a barrier of that block.
-__device__ __forceinline__ void peer_store4(uint32_t addr, float a, float b, float c, float d, uint32_t bar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr), "f"(a), "f"(b),
-                 "f"(c), "f"(d), "r"(bar)
+// Bulk copy of this block's shared memory into another's, counted in bytes by a barrier of that block.
+__device__ __forceinline__ void peer_copy(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "r"(src),
+                 "r"(bytes), "r"(bar)
                  : "memory");
 }
 // ptx.cuh's waits for barriers that other blocks of the cluster arrive on.
@@ -359,6 +358,54 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[16], int
         }
     } else if (n < p.N) {
         column(v, m, n, live, std::integral_constant<int, 16>());
+    }
+}
+
+__device__ __forceinline__ float element(const void* p, size_t i, int dt) {
+    return dt == DT_F32 ? load_c<DT_F32>(p, i) : (dt == DT_F16 ? load_c<DT_F16>(p, i) : load_c<DT_BF16>(p, i));
+}
+// Scales, bias and the rest of the epilogue for channels n .. n + 3 of expert e in C's row m (SPLIT).
+__device__ __forceinline__ void finish4(const Params& p, float (&y)[4], int e, size_t m, int n) {
+    const size_t en = (size_t)e * p.N + n;
+    const int live = min(4, p.N - n);
+    const float as = p.a_scale ? __ldg(p.a_scale + m) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float ws = p.b_scale && i < live ? __ldg(p.b_scale + en + i) : 1.f;
+        const float bias = p.bias && i < live ? __ldg(p.bias + en + i) : 0.f;
+        y[i] = fmaf(y[i] * as, ws, bias);
+    }
+    const bool glu = p.act == ACT_SWIGLU;
+    if (glu) {
+        y[0] = act_fixed<ACT_SILU>(y[0]) * y[1];
+        y[1] = act_fixed<ACT_SILU>(y[2]) * y[3];
+    } else if (p.act != ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = act_apply(p.act, y[i]);
+    }
+    const int count = glu ? live >> 1 : live;
+    const size_t at = m * p.cols + (glu ? n >> 1 : n);
+    if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) y[i] += element(p.residual, at + i, p.c_dtype);
+    }
+    if (count == 4 && (p.cols & 3) == 0) {
+        if (p.c_dtype == DT_F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.C) + at) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (p.c_dtype == DT_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(y[2 * i + 1]), "f"(y[2 * i]));
+                else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(y[2 * i + 1]), "f"(y[2 * i]));
+            }
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.C) + at) = make_uint2(w[0], w[1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) store_out_rt(p.C, at + i, y[i], p.c_dtype);
     }
 }
 
@@ -711,14 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     } else {
         // ---------------- epilogue
         const int q = warp & 3, h = (warp - kEpiWarp) >> 2;
-        const bool odd = lane & 1, glu = p.act == ACT_SWIGLU;
+        const bool odd = lane & 1;
         const float* const part = reinterpret_cast<const float*>(smem + S * P::kStage);
-        auto store_one = [&](size_t at, float y) {
-            if (p.residual)
-                y += p.c_dtype == DT_F32 ? load_c<DT_F32>(p.residual, at)
-                                         : (p.c_dtype == DT_F16 ? load_c<DT_F16>(p.residual, at) : load_c<DT_BF16>(p.residual, at));
-            store_out_rt(p.C, at, y, p.c_dtype);
-        };
         int tj = 0;
         for (int t = worker; t < total; t += workers, ++tj) {
             const Tile x = tile_of(t);
@@ -727,46 +768,50 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + ((tj & 1) ? (uint32_t)P::kAcc1 : 0u);
             constexpr int kParts = BN / 32;      // chunks of 16 columns of each column half
             if constexpr (MODE == SPLIT) {
-                const int share = kCh / p.split, ch = 32 * q + lane;      // channels of a block's share; this lane's
-                if (threadIdx.x == kEpiWarp * 32) ptx::mbar_expect_tx(parts, (uint32_t)(kCh * ((x.rows + 3) / 4 * 4) * 4));
-                cluster_wait();
-                sent = true;
-                const uint32_t to = peer(red + (uint32_t)(((int)rank * share + ch % share) * P::kRedRow) * 4, ch / share);
-                const uint32_t to_bar = peer(parts, ch / share);
+                // the partial sums as [block][row][channel of its share] where the ring was (its MMAs are
+                // done), then one copy to each block
+                const int share = kCh / p.split, ch = 32 * q + lane, held = x.rows * share * 4;
+                float* const own = reinterpret_cast<float*>(smem) + (size_t)(ch / share) * x.rows * share + ch % share;
                 for (int j = 0; j < kParts; ++j) {
                     const int c0 = 16 * (kParts * h + j);
                     if (c0 >= x.rows) break;
                     float v[16];
                     tmem_ld16(acc + (uint32_t)c0, v);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        if (c0 + i < x.rows) peer_store4(to + (uint32_t)(c0 + i) * 4, v[i], v[i + 1], v[i + 2], v[i + 3], to_bar);
+                    for (int i = 0; i < 16; ++i)
+                        if (c0 + i < x.rows) own[(c0 + i) * share] = v[i];
                     __syncwarp();
                 }
+                ptx::fence_proxy_async_smem();
+                asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+                cluster_wait();
+                sent = true;
+                if (threadIdx.x == kEpiWarp * 32) {
+                    ptx::mbar_expect_tx(parts, (uint32_t)(p.split * held));
+                    for (int r = 0; r < p.split; ++r)
+                        peer_copy(peer(red + rank * held, r), ring + r * held, (uint32_t)held, peer(parts, r));
+                }
                 if (!__all_sync(0xffffffffu, cluster_bar_wait(parts, 0u, abort_flag, p.status, p.wait_ns))) break;
-                // this block's share of the channels (a multiple of 16), all rows
-                const int count = x.rows * share;
-                for (int i0 = threadIdx.x - kEpiWarp * 32; i0 < (count + 31) / 32 * 32; i0 += kEpiThreads) {
-                    const int i = min(i0, count - 1), cl = i % share, m = x.m0 + i / share, n = x.n0 + (int)rank * share + cl;
-                    float v[kMaxSplit];
+                // this block's share of the channels (a power of two from 16 up), all rows, four channels a thread
+                const int lg = 31 - __clz(share >> 2), step = x.rows * share;
+#pragma unroll 1
+                for (int i = threadIdx.x - kEpiWarp * 32; i < step / 4; i += kEpiThreads) {
+                    const int row = i >> lg, n = x.n0 + (int)rank * share + 4 * (i - (row << lg));
+                    if (n >= p.N) continue;
+                    float4 v[kMaxSplit];
 #pragma unroll
                     for (int r = 0; r < kMaxSplit; ++r)
-                        v[r] = r < p.split ? part[(r * share + cl) * P::kRedRow + i / share] : 0.f;
+                        if (r < p.split) v[r] = *reinterpret_cast<const float4*>(part + r * step + 4 * i);
+                    float y[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-                    for (int r = 1; r < kMaxSplit; ++r) v[0] += v[r];
-                    const size_t en = (size_t)x.e * p.N + min(n, p.N - 1);
-                    float y = v[0];
-                    if (p.a_scale) y *= __ldg(p.a_scale + m);
-                    if (p.b_scale) y *= __ldg(p.b_scale + en);
-                    if (p.bias) y += __ldg(p.bias + en);
-                    if (glu) {
-                        const float up = __shfl_xor_sync(0xffffffffu, y, 1);
-                        y = act_fixed<ACT_SILU>(y) * up;
-                        if (i0 < count && n < p.N && !odd) store_one((size_t)m * p.cols + (n >> 1), y);
-                    } else {
-                        y = act_apply(p.act, y);
-                        if (i0 < count && n < p.N) store_one((size_t)m * p.cols + n, y);
-                    }
+                    for (int r = 1; r < kMaxSplit; ++r)
+                        if (r < p.split) {
+                            y[0] += v[r].x;
+                            y[1] += v[r].y;
+                            y[2] += v[r].z;
+                            y[3] += v[r].w;
+                        }
+                    finish4(p, y, x.e, (size_t)(x.m0 + row), n);
                 }
             } else {
                 // (x is in registers of every lane; its chunk's rows are x.m0 + c0 + i)
@@ -811,12 +856,9 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     }
     tc_fence_before();
     __syncthreads();
-    // No block leaves while a peer may still reach its memory. SPLIT: a block that has its sums has heard
-    // the last of its peers; one that gave up waits until they have left or given up too.
-    if (kPair || (MODE == SPLIT && *abort_flag)) {
-        if constexpr (MODE == SPLIT) {
-            if (warp < kEpiWarp || !sent) cluster_wait();       // the first phase, where it was not waited for
-        }
+    // no block leaves while a peer may still reach its memory, or a copy may still read it
+    if constexpr (kCluster) {
+        if (MODE == SPLIT && !sent) cluster_wait();        // the first phase, where it was not waited for
         cluster_arrive();
         cluster_wait();
     }
