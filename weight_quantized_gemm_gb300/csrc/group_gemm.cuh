@@ -24,9 +24,11 @@
 // groups' tile counts once, and finds a tile's group by binary search.
 //
 // SPLIT: with too few tiles to fill the GPU, the blocks of a cluster share a tile, each taking a part
-// of K. Each block is sent its share of the channels' partial sums by all of them (one bulk copy to
-// distributed shared memory each, counted by a barrier: no fence between blocks) and adds them in
-// rank order. No workspace, no atomics, one launch. A cluster has one tile at most.
+// of K. Each block is sent its share of the channels' partial sums by all of them (asynchronous stores to
+// distributed shared memory, counted by a barrier: no fence between blocks) and adds them in rank
+// order. Tiles of up to 32 rows store their sums one by one; larger ones (4 bytes at a time they
+// took 4 us for 64 rows) turn them in shared memory and send one bulk copy to each block, which for
+// a few rows takes 0.5 us longer. No workspace, no atomics, one launch. A cluster has one tile at most.
 //
 // Every wait is bounded (see ptx.cuh); after an abort the copies and MMAs in flight are waited for,
 // and a cluster's blocks leave together.
@@ -229,6 +231,10 @@ __device__ __forceinline__ uint32_t peer(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void peer_signal(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// A value to another block's shared memory, counted in bytes by a barrier of that block.
+__device__ __forceinline__ void peer_store(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr), "f"(v), "r"(bar) : "memory");
+}
 // Bulk copy of this block's shared memory into another's, counted in bytes by a barrier of that block.
 __device__ __forceinline__ void peer_copy(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "r"(src),
@@ -413,7 +419,7 @@ template <int F, int BN, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     using P = Plan<F, BN, MODE>;
     constexpr int S = P::kStages;
-    constexpr bool kPair = MODE == PAIR, kCluster = MODE != SOLO;
+    constexpr bool kPair = MODE == PAIR, kCluster = MODE != SOLO, kDirect = MODE == SPLIT && BN == 32;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * P::kStage + P::kRed);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 10);
@@ -768,28 +774,42 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + ((tj & 1) ? (uint32_t)P::kAcc1 : 0u);
             constexpr int kParts = BN / 32;      // chunks of 16 columns of each column half
             if constexpr (MODE == SPLIT) {
-                // the partial sums as [block][row][channel of its share] where the ring was (its MMAs are
-                // done), then one copy to each block
+                // the partial sums arrive as [block][row][channel of the share]
                 const int share = kCh / p.split, ch = 32 * q + lane, held = x.rows * share * 4;
-                float* const own = reinterpret_cast<float*>(smem) + (size_t)(ch / share) * x.rows * share + ch % share;
-                for (int j = 0; j < kParts; ++j) {
-                    const int c0 = 16 * (kParts * h + j);
-                    if (c0 >= x.rows) break;
-                    float v[16];
-                    tmem_ld16(acc + (uint32_t)c0, v);
+                if (threadIdx.x == kEpiWarp * 32) ptx::mbar_expect_tx(parts, (uint32_t)(p.split * held));
+                if constexpr (kDirect) {
+                    cluster_wait();
+                    sent = true;
+                    const uint32_t to = peer(red + rank * held + (uint32_t)(ch % share) * 4, ch / share), to_bar = peer(parts, ch / share);
+                    const int c0 = 16 * h;
+                    if (c0 < x.rows) {
+                        float v[16];
+                        tmem_ld16(acc + (uint32_t)c0, v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c0 + i < x.rows) own[(c0 + i) * share] = v[i];
+                        for (int i = 0; i < 16; ++i)
+                            if (c0 + i < x.rows) peer_store(to + (uint32_t)((c0 + i) * share) * 4, v[i], to_bar);
+                    }
                     __syncwarp();
-                }
-                ptx::fence_proxy_async_smem();
-                asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
-                cluster_wait();
-                sent = true;
-                if (threadIdx.x == kEpiWarp * 32) {
-                    ptx::mbar_expect_tx(parts, (uint32_t)(p.split * held));
-                    for (int r = 0; r < p.split; ++r)
-                        peer_copy(peer(red + rank * held, r), ring + r * held, (uint32_t)held, peer(parts, r));
+                } else {
+                    // turned where the ring was (its MMAs are done)
+                    float* const own = reinterpret_cast<float*>(smem) + (size_t)(ch / share) * x.rows * share + ch % share;
+                    for (int j = 0; j < kParts; ++j) {
+                        const int c0 = 16 * (kParts * h + j);
+                        if (c0 >= x.rows) break;
+                        float v[16];
+                        tmem_ld16(acc + (uint32_t)c0, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c0 + i < x.rows) own[(c0 + i) * share] = v[i];
+                        __syncwarp();
+                    }
+                    ptx::fence_proxy_async_smem();
+                    asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+                    cluster_wait();
+                    sent = true;
+                    if (threadIdx.x == kEpiWarp * 32)
+                        for (int r = 0; r < p.split; ++r)
+                            peer_copy(peer(red + rank * held, r), ring + r * held, (uint32_t)held, peer(parts, r));
                 }
                 if (!__all_sync(0xffffffffu, cluster_bar_wait(parts, 0u, abort_flag, p.status, p.wait_ns))) break;
                 // this block's share of the channels (a power of two from 16 up), all rows, four channels a thread
@@ -856,8 +876,10 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     }
     tc_fence_before();
     __syncthreads();
-    // no block leaves while a peer may still reach its memory, or a copy may still read it
-    if constexpr (kCluster) {
+    // No block leaves while a peer may still reach its memory, or a copy may still read it. (With its sums,
+    // each stored by its sender, a block has heard the last of its peers; one that gave up waits until
+    // they have left or given up too.)
+    if (kCluster && (!kDirect || *abort_flag)) {
         if (MODE == SPLIT && !sent) cluster_wait();        // the first phase, where it was not waited for
         cluster_arrive();
         cluster_wait();
