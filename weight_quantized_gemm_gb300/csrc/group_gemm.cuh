@@ -216,7 +216,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// (relaxed: the barrier orders lifetimes; what the blocks exchange is ordered by mbarriers, and the
+// mbarriers' initialization by its own fence. A release would wait for the thread's memory accesses.)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // Address of this block's shared-memory location in the cluster's block `rank`.
 __device__ __forceinline__ uint32_t peer(uint32_t saddr, uint32_t rank) {
@@ -494,10 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     };
 
     bool sent = false;   // SPLIT: this thread has waited for the peers' barriers
-    // Stages of the first tile that are loaded before the block barrier: where neither the tile table
-    // nor another block is needed. (The same in every lane, or the compiler takes each TMA instruction's
-    // operands for the lane's own.)
-    const int ahead = !kPair && !p.offsets && worker < dense_m * p.n_tiles ? min(S, nks) : 0;
     if (warp == 0 && elect_one()) {
         for (int s = 0; s < S; ++s) {
             // the TMA warp, and one scale warp (PAIR: one a half in both blocks)
@@ -516,10 +514,6 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
         ptx::prefetch_tmap(&maps.a);
         ptx::prefetch_tmap(&maps.b);
         if (F != HALF) ptx::prefetch_tmap(&maps.sb);
-        if (ahead > 0) {
-            const Tile x = tile_of(worker);
-            for (int i = 0; i < ahead; ++i) issue(x, i, i);
-        }
     }
     if (warp == 1) {
         // (one block fits an SM, so the columns are free; PAIR: both blocks take part)
@@ -556,19 +550,22 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     // the peers' barriers are initialized before anyone arrives on them (SPLIT: the wait comes later)
     if constexpr (kCluster) cluster_arrive();
     if constexpr (kPair) cluster_wait();
-    __syncthreads();
+    // The block barrier. The TMA warp only reports that it has initialized the barriers, and goes on to
+    // its first loads, where it needs neither the tile table nor another block.
+    if (warp == 0 && !kPair && !p.offsets) asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");
+    else asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
     tc_fence_after();
     const int total = p.offsets ? before[p.E] : dense_m * p.n_tiles;
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);       // (not for the TMA warp)
     if (warp == 0) {
         // ---------------- TMA
         if (elect_one()) {
-            int g = ahead, s = ahead % S;
-            uint32_t ph = (uint32_t)(ahead / S) & 1u;
+            int g = 0, s = 0;
+            uint32_t ph = 0;
             bool stop = false;
             for (int t = worker; t < total && !stop; t += workers) {
                 const Tile x = tile_of(t);
-                for (int i = t == worker ? ahead : 0; i < nks; ++i) {
+                for (int i = 0; i < nks; ++i) {
                     if (*abort_flag || (g >= S && !wait(empty(s), ph ^ 1u))) {
                         stop = true;
                         break;
