@@ -45,33 +45,49 @@ struct Raw {
             }
         }
     }
-    // bits of the largest |x| as float32 (an infinity or NaN is larger than any number)
+    // Bits of the largest |x| as float32 (an infinity or NaN is larger than any number): the bits of
+    // positive values order as whole numbers do, two 16-bit ones at a time.
     __device__ __forceinline__ uint32_t top() const {
-        float x[kUnit];
-        to_float(x);
-        uint32_t t = 0;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+        if constexpr (DT == DT_F32) {
+            uint32_t t = 0;
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) t = max(t, abs_bits(x[i]));
-        return t;
+            for (int i = 0; i < kUnit; ++i) t = max(t, w[i] & 0x7FFFFFFFu);
+            return t;
+        } else {
+            constexpr uint32_t kAbs = 0x7FFF7FFFu;
+            uint32_t t = w[0] & kAbs;
+#pragma unroll
+            for (int i = 1; i < kUnit / 2 - 1; i += 2) t = __vimax3_u16x2(t, w[i] & kAbs, w[i + 1] & kAbs);
+            t = __vimax3_u16x2(t, w[kUnit / 2 - 1] & kAbs, 0u);
+            t = max(t & 0xFFFFu, t >> 16);
+            return DT == DT_BF16 ? t << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)t)));
+        }
     }
 };
 
-// Codes of one NVFP4 block of row-scaled values y: the e2m1 value nearest to y / s. The quotient
-// must land on a tie exactly where y does: for float32 input that is the correctly rounded
-// quotient. 16-bit input (at most 11 significant bits) is either on a tie or at least 2^-13 away
-// from it (ties are 0.25 and more), so y * (1 / s), wrong by a few 2^-23, is rounded to a multiple
-// of 2^-16 by adding and subtracting 192, which puts it back on the tie or keeps it off.
+// Codes of one NVFP4 block of values x with row factor mul (a power of two) and block scale s: the
+// e2m1 value nearest to x * mul / s. The quotient must land on a tie exactly where the value does.
+// float32: the correctly rounded quotient does, from the rounded reciprocal of s by one correction step
+// (Markstein 1990; s has 4 significant bits). 16-bit values (at most 11 significant bits) are either
+// on a tie or at least 2^-13 away from it (ties are 0.25 and more), so x * (mul / s), wrong by a few
+// 2^-23, is rounded to a multiple of 2^-16 by adding and subtracting 192, which puts it back on the
+// tie or keeps it off.
 template <int DT>
-__device__ __forceinline__ uint2 nv_codes(float (&y)[kUnit], float s) {
-    const float r = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+__device__ __forceinline__ uint2 nv_codes(const float (&x)[kUnit], float mul, float s) {
+    const float r = s > 0.f ? __fdiv_rn(1.f, s) : 0.f, rm = r * mul;
+    float q[kUnit];
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) {
-        float q;
-        if constexpr (DT == DT_F32) q = s > 0.f ? __fdiv_rn(y[i], s) : 0.f;
-        else q = __fsub_rn(__fmaf_rn(y[i], r, 192.f), 192.f);
-        y[i] = copysignf(q, y[i]);
+        if constexpr (DT == DT_F32) {
+            const float y = x[i] * mul, q0 = y * r;
+            q[i] = __fmaf_rn(__fmaf_rn(-q0, s, y), r, q0);
+        } else {
+            q[i] = __fsub_rn(__fmaf_rn(x[i], rm, 192.f), 192.f);
+        }
+        q[i] = copysignf(q[i], x[i]);
     }
-    return make_uint2(pack8(y), pack8(y + 8));
+    return mul != 0.f ? make_uint2(pack8(q), pack8(q + 8)) : make_uint2(0, 0);
 }
 
 struct QuantArgs {
@@ -115,78 +131,74 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(const QuantArgs a) {
         float x[kUnit];
         raw.to_float(x);
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) x[i] = mul != 0.f ? x[i] * mul : 0.f;
-        reinterpret_cast<uint2*>(a.codes)[(size_t)m * (a.K / kUnit) + u] = make_uint2(pack8(x), pack8(x + 8));
+        for (int i = 0; i < kUnit; ++i) x[i] *= mul;
+        reinterpret_cast<uint2*>(a.codes)[(size_t)m * (a.K / kUnit) + u] =
+            mul != 0.f ? make_uint2(pack8(x), pack8(x + 8)) : make_uint2(0, 0);
     }
     if ((u & 1) == 0 && u < a.units_out) a.scales[scale_index(a, m, u >> 1)] = in ? (uint8_t)byte : (uint8_t)0;
 }
 
-// NVFP4: one thread block per row, which it reads once while up to kKeep units a thread stay in
-// registers (rows of up to 16384 values; longer ones are read again for the codes).
-constexpr int kNvThreads = 256;
+// NVFP4: the row's largest value comes first, so each thread keeps its kKeep units of the row in
+// registers between the two steps (rows of up to 16384 values; the rest of longer ones is read
+// again). A row takes as few warps as that allows, and a thread block of kNvThreads as many rows as
+// fit: with one row a block, rows of 4096 had one load a thread in flight (17 us for 4096 rows
+// against 10).
+constexpr int kNvThreads = 256, kKeep = 4;
 template <int DT>
 __global__ void __launch_bounds__(kNvThreads) nv_quant_kernel(const QuantArgs a) {
-    constexpr int kKeep = DT == DT_F32 ? 2 : 4;
     __shared__ uint32_t s_top[kNvThreads / 32];
-    const int m = blockIdx.x, units = a.K / kUnit, step = blockDim.x;
+    const int units = a.K / kUnit, step = blockDim.x, t = threadIdx.x;      // threads of a row; this one
+    const int m = blockIdx.x * blockDim.y + threadIdx.y;
     const uint8_t* row = source_row(a, m);
     Raw<DT> keep[kKeep];
     uint32_t top = 0;
     if (row) {
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            const int u = threadIdx.x + i * step;
-            if (u < units) {
-                keep[i].load(row, u);
-                top = max(top, keep[i].top());
-            }
-        }
-        for (int u = threadIdx.x + kKeep * step; u < units; u += step) {
+        for (int i = 0; i < kKeep; ++i)
+            if (t + i * step < units) keep[i].load(row, t + i * step);
+            else keep[i].zero();
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) top = max(top, keep[i].top());
+        for (int u = t + kKeep * step; u < units; u += step) {
             Raw<DT> raw;
             raw.load(row, u);
             top = max(top, raw.top());
         }
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < step / 32; ++w) top = max(top, s_top[w]);
+    const int warps = step / 32;
+    if (warps > 1) {
+        if ((t & 31) == 0) s_top[threadIdx.y * warps + (t >> 5)] = top;
+        __syncthreads();
+        for (int w = 0; w < warps; ++w) top = max(top, s_top[threadIdx.y * warps + w]);
+    }
+    if (m >= a.rows_out) return;
     float mul;
     const float g = nv_row_scale(top, &mul);
-    if (threadIdx.x == 0 && m < a.M) a.row_scale[m] = g;
+    if (t == 0 && m < a.M) a.row_scale[m] = g;
     auto emit = [&](const Raw<DT>& raw, int u) {
-        float y[kUnit];
-        raw.to_float(y);
-        uint32_t t = 0;
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-            y[i] = mul != 0.f ? y[i] * mul : 0.f;
-            t = max(t, abs_bits(y[i]));
-        }
-        float s;
-        a.scales[scale_index(a, m, u)] = (uint8_t)nv_scale(t, &s);
-        reinterpret_cast<uint2*>(a.codes)[(size_t)m * units + u] = nv_codes<DT>(y, s);
+        float x[kUnit], s;
+        raw.to_float(x);
+        const uint32_t most = mul != 0.f ? __float_as_uint(__uint_as_float(raw.top()) * mul) : 0u;
+        a.scales[scale_index(a, m, u)] = (uint8_t)nv_scale(most, &s);
+        reinterpret_cast<uint2*>(a.codes)[(size_t)m * units + u] = nv_codes<DT>(x, mul, s);
     };
-    if (m < a.M) {
-        if (row) {
+    if (row) {
 #pragma unroll
-            for (int i = 0; i < kKeep; ++i) {
-                const int u = threadIdx.x + i * step;
-                if (u < units) emit(keep[i], u);
-            }
-            for (int u = threadIdx.x + kKeep * step; u < units; u += step) {
-                Raw<DT> raw;
-                raw.load(row, u);
-                emit(raw, u);
-            }
-        } else {
-            for (int u = threadIdx.x; u < units; u += step) {
-                a.scales[scale_index(a, m, u)] = 0;
-                reinterpret_cast<uint2*>(a.codes)[(size_t)m * units + u] = make_uint2(0, 0);
-            }
+        for (int i = 0; i < kKeep; ++i)
+            if (t + i * step < units) emit(keep[i], t + i * step);
+        for (int u = t + kKeep * step; u < units; u += step) {
+            Raw<DT> raw;
+            raw.load(row, u);
+            emit(raw, u);
+        }
+    } else if (m < a.M) {
+        for (int u = t; u < units; u += step) {
+            a.scales[scale_index(a, m, u)] = 0;
+            reinterpret_cast<uint2*>(a.codes)[(size_t)m * units + u] = make_uint2(0, 0);
         }
     }
-    for (int u = threadIdx.x + (m < a.M ? units : 0); u < a.units_out; u += step) a.scales[scale_index(a, m, u)] = 0;
+    for (int u = t + (m < a.M ? units : 0); u < a.units_out; u += step) a.scales[scale_index(a, m, u)] = 0;
 }
 
 // The inverse: y = code * block scale * row scale, rounded once to y's type.
@@ -289,19 +301,13 @@ __global__ void __launch_bounds__(128) fp4_pack_kernel(const PackArgs a) {
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             byte = mx_scale(top, &mul);
 #pragma unroll
-            for (int i = 0; i < kUnit; ++i) x[i] = mul != 0.f ? x[i] * mul : 0.f;
-            c = make_uint2(pack8(x), pack8(x + 8));
+            for (int i = 0; i < kUnit; ++i) x[i] *= mul;
+            c = mul != 0.f ? make_uint2(pack8(x), pack8(x + 8)) : make_uint2(0, 0);
             j = u >> 1;
         } else {
-            uint32_t t = 0;
             float s;
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) {
-                x[i] = mul != 0.f ? x[i] * mul : 0.f;
-                t = max(t, abs_bits(x[i]));
-            }
-            byte = nv_scale(t, &s);
-            c = nv_codes<DT_F32>(x, s);
+            byte = nv_scale(mul != 0.f ? __float_as_uint(__uint_as_float(top) * mul) : 0u, &s);
+            c = nv_codes<DT_F32>(x, mul, s);
             j = u;
         }
         if (n < a.N) reinterpret_cast<uint2*>(a.codes)[(size_t)n * units + u] = c;
@@ -321,9 +327,9 @@ cudaError_t quant_dt(const QuantArgs& a, int fmt, cudaStream_t s) {
         const dim3 grid((a.rows_out + 7) / 8, (a.units_out + 31) / 32);
         mx_quant_kernel<DT><<<grid, dim3(32, 8), 0, s>>>(a);
     } else {
-        const int units = a.K / kUnit;
-        const int threads = units >= kNvThreads ? kNvThreads : (units + 31) / 32 * 32;
-        nv_quant_kernel<DT><<<a.rows_out, threads, 0, s>>>(a);
+        const int warps = (a.K / kUnit + kKeep * 32 - 1) / (kKeep * 32);      // of a row
+        const int row = 32 * (warps < kNvThreads / 32 ? warps : kNvThreads / 32), rows = kNvThreads / row;
+        nv_quant_kernel<DT><<<(a.rows_out + rows - 1) / rows, dim3(row, rows), 0, s>>>(a);
     }
     return cudaGetLastError();
 }

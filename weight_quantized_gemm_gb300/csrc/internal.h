@@ -174,7 +174,7 @@ inline cudaError_t launch_group_gemm(const GroupGemmArgs& a, int fmt, cudaStream
 }
 // The router's launches: up to kRouteSmallTokens tokens in one thread block, else kRouteBlocks blocks
 // at most, with a histogram of E counts each in the workspace.
-constexpr int kRouteSmallTokens = 128;
+constexpr int kRouteSmallTokens = 32;
 constexpr int kRouteBlocks = kTargetSms;
 inline bool route_needs_workspace(int T) { return T > kRouteSmallTokens; }
 cudaError_t launch_moe_route(int T, int E, int k, const void* logits, int dtype, long long ld, int renorm, int32_t* expert,

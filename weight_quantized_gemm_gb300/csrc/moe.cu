@@ -10,17 +10,18 @@ namespace qg {
 namespace {
 
 // ---------------------------------------------------------------- routing
-// One warp per token: lane i holds the logits of experts i, i + 32, ... as order-preserving integer
-// keys, and each of the k rounds takes the largest key by a warp reduction, ties to the lowest expert
-// (a second reduction over the experts that hold it). A stable counting sort of the pairs by expert
-// follows: histograms, exclusive prefix sums, then each pair's rank among the pairs before it by
-// warp matches, so the order depends on nothing but the input. A few tokens run in one thread
-// block and one launch; more run in two, where the second launch's blocks each sum the first's
-// histograms themselves (at most kRouteBlocks x E counts, from L2) instead of waiting for a third
-// launch that scans them.
+// A warp per token: lane i holds the logits of E / 32 neighbouring experts as order-preserving integer
+// keys, and each of the k rounds takes the largest key by a warp reduction; of several lanes that
+// hold it the lowest, and in it the lowest expert, is the lowest expert of all. Each warp runs several
+// tokens side by side, since a round is a chain of dependent warp operations. A stable counting sort
+// of the pairs by expert follows: histograms, exclusive prefix sums, then each pair's rank among the
+// pairs before it by warp matches, so the order depends on nothing but the input. A few tokens run in
+// one thread block and one launch (128 tokens of 128 experts there: 19 us against 8 in two launches);
+// more run in two, where the second launch's blocks each sum the first's histograms themselves (at
+// most kRouteBlocks x E counts, from L2) instead of waiting for a third launch that scans them.
 constexpr int kSortWarps = 8;         // warps that rank a block's pairs
 constexpr int kSmallThreads = 1024;
-constexpr int kBigThreads = 512;
+constexpr int kBigThreads = 512;      // two blocks on an SM
 
 struct RouteArgs {
     int T, E, k, renorm;
@@ -54,76 +55,82 @@ __device__ __forceinline__ float from_key(uint32_t k) {
 // exp(x - top), where equal infinities count as equal values
 __device__ __forceinline__ float rel_exp(float x, float top) { return x == top ? 1.f : expf(x - top); }
 
-// Token t's choice by the calling warp: lane j < k ends with its j-th expert (-1: none left) and weight.
-template <int DT, int EL>
-__device__ __forceinline__ void choose(const RouteArgs& a, int t, int lane, int* expert, float* weight) {
-    uint32_t key[EL];
+// The choices of tokens t, t + step, ... (kSide of them, those below t1) by the calling warp: writes
+// expert and weight and counts each expert's pairs.
+template <int DT, int EL, int kSide>
+__device__ __forceinline__ void choose(const RouteArgs& a, int t, int step, int t1, int lane, int32_t* counts) {
+    uint32_t key[kSide][EL], best[kSide], first[kSide], mine[kSide];
+    float all[kSide];
 #pragma unroll
-    for (int j = 0; j < EL; ++j) {
-        const int e = lane + 32 * j;
-        key[j] = e < a.E ? to_key(load_as_float<DT>(a.logits, (size_t)((long long)t * a.ld) + e)) : 0u;
+    for (int i = 0; i < kSide; ++i) {
+        best[i] = first[i] = mine[i] = 0u;
+        all[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < EL; ++j) {
+            const int e = lane * EL + j;
+            key[i][j] = t + i * step < t1 && e < a.E ? to_key(load_as_float<DT>(a.logits, (size_t)((long long)(t + i * step) * a.ld) + e)) : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < EL; ++j) best[i] = max(best[i], key[i][j]);
     }
-    uint32_t best = 0, chosen_key = 0, first = 0;
-    int best_j = 0, chosen = -1;
-#pragma unroll
-    for (int j = 0; j < EL; ++j)
-        if (key[j] > best) { best = key[j]; best_j = j; }
-    float all = 0.f;
     for (int r = 0; r < a.k; ++r) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (r == 0) {
-            first = top;
-            if (!a.renorm && top) {
-                const float m = from_key(top);
+        uint32_t top[kSide];
 #pragma unroll
-                for (int j = 0; j < EL; ++j)
-                    if (key[j]) all += rel_exp(from_key(key[j]), m);
+        for (int i = 0; i < kSide; ++i) top[i] = __reduce_max_sync(0xffffffffu, best[i]);
 #pragma unroll
-                for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            }
-        }
-        if (!top) break;
-        const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(lane + 32 * best_j) : 0xffffffffu);
-        if (lane == r) {
-            chosen = (int)e;
-            chosen_key = top;
-        }
-        if ((int)(e & 31u) == lane) {   // its holder takes it out
-            best = 0;
+        for (int i = 0; i < kSide; ++i) {
+            if (r == 0) first[i] = top[i];
+            if (lane == r) mine[i] = top[i];       // this lane's choice has the r-th largest key (0: none is left)
+            const uint32_t holders = __ballot_sync(0xffffffffu, best[i] == top[i]);
+            if (t + i * step < t1) {
+                const size_t at = (size_t)(t + i * step) * a.k + r;
+                if (!top[i]) {
+                    if (lane == 0) a.expert[at] = -1;
+                } else if (lane == __ffs(holders) - 1) {
+                    uint32_t rest = 0;
+                    bool taken = false;
 #pragma unroll
-            for (int j = 0; j < EL; ++j) {
-                if (lane + 32 * j == (int)e) key[j] = 0u;
-                if (key[j] > best) { best = key[j]; best_j = j; }
+                    for (int j = 0; j < EL; ++j) {
+                        if (!taken && key[i][j] == top[i]) {
+                            taken = true;
+                            key[i][j] = 0u;
+                            a.expert[at] = lane * EL + j;
+                            atomicAdd(counts + lane * EL + j, 1);
+                        }
+                        rest = max(rest, key[i][j]);
+                    }
+                    best[i] = rest;
+                }
             }
         }
     }
-    const float w = chosen >= 0 ? rel_exp(from_key(chosen_key), from_key(first)) : 0.f;
-    if (a.renorm) {
-        all = w;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    for (int i = 0; i < kSide; ++i) {
+        if (t + i * step >= t1) continue;      // (the same for the whole warp)
+        const float top = from_key(first[i]), w = mine[i] ? rel_exp(from_key(mine[i]), top) : 0.f;
+        all[i] = w;
+        if (!a.renorm && first[i]) {
+            // over all experts: the ones not chosen are still in key, the chosen ones' terms are w
+#pragma unroll
+            for (int j = 0; j < EL; ++j)
+                if (key[i][j]) all[i] += rel_exp(from_key(key[i][j]), top);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all[i] += __shfl_xor_sync(0xffffffffu, all[i], o);
+        if (lane < a.k) a.weight[(size_t)(t + i * step) * a.k + lane] = mine[i] ? w / all[i] : 0.f;
     }
-    *expert = chosen;
-    *weight = chosen >= 0 ? w / all : 0.f;
 }
 
 // The choice of tokens [t0, t1) by all warps of the block; counts[e] gets the block's pairs per
 // expert (shared memory, cleared here; integer sums, so their order does not matter).
 template <int DT, int EL>
 __device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int t1, int32_t* counts) {
+    constexpr int kSide = EL <= 4 ? 4 : (EL <= 8 ? 2 : 1);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) counts[e] = 0;
     __syncthreads();
-    const int lane = threadIdx.x & 31;
-    for (int t = t0 + (int)(threadIdx.x >> 5); t < t1; t += blockDim.x >> 5) {
-        int e;
-        float w;
-        choose<DT, EL>(a, t, lane, &e, &w);
-        if (lane < a.k) {
-            a.expert[(size_t)t * a.k + lane] = e;
-            a.weight[(size_t)t * a.k + lane] = w;
-            if (e >= 0) atomicAdd(counts + e, 1);
-        }
-    }
+    const int warps = blockDim.x >> 5;
+    for (int t = t0 + (int)(threadIdx.x >> 5); t < t1; t += kSide * warps)
+        choose<DT, EL, kSide>(a, t, warps, t1, threadIdx.x & 31, counts);
     __syncthreads();
 }
 
@@ -248,7 +255,7 @@ cudaError_t route_el(RouteArgs a, cudaStream_t s) {
         route_small_kernel<DT, EL><<<1, kSmallThreads, (2 * a.E + 1) * sizeof(int32_t) + sort, s>>>(a);
         return cudaGetLastError();
     }
-    const int want = (a.T + 15) / 16;
+    const int want = (a.T + 15) / 16;      // a token a warp at least
     const int blocks = want < kRouteBlocks ? want : kRouteBlocks;
     a.per_block = (a.T + blocks - 1) / blocks;
     route_choose_kernel<DT, EL><<<blocks, kBigThreads, a.E * sizeof(int32_t), s>>>(a);
