@@ -1,6 +1,5 @@
 // The C ABI of include/qgemm.h for 4-bit floating point and mixture-of-experts layers: argument
 // checks and size queries. As in qgemm_api.cu, every check runs before the first launch.
-#include <limits.h>
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -162,7 +161,7 @@ int qgemm_moe_route(int T, int E, int k, const void* logits, int dtype, long lon
     if (E > QGEMM_MAX_EXPERTS || k > QGEMM_MAX_TOPK)
         return fail(QGEMM_ERR_UNSUPPORTED, "E=%d or k=%d exceeds %d experts or %d choices", E, k, QGEMM_MAX_EXPERTS,
                     QGEMM_MAX_TOPK);
-    if ((long long)T * k > INT_MAX) return fail(QGEMM_ERR_UNSUPPORTED, "T * k = %lld pairs exceed int32", (long long)T * k);
+    if ((long long)T * k > 1 << 30) return fail(QGEMM_ERR_UNSUPPORTED, "T * k = %lld exceeds 2^30 pairs", (long long)T * k);
     if (!offsets) return fail(QGEMM_ERR_ARG, "null offsets");
     if (T > 0 && (!logits || !expert || !weight || !slot || !row))
         return fail(QGEMM_ERR_ARG, "null logits, expert, weight, slot or row");

@@ -12,16 +12,18 @@ namespace {
 // ---------------------------------------------------------------- routing
 // A warp per token: lane i holds the logits of E / 32 neighbouring experts as order-preserving integer
 // keys, and each of the k rounds takes the largest key by a warp reduction; of several lanes that
-// hold it the lowest, and in it the lowest expert, is the lowest expert of all. Each warp runs several
-// tokens side by side, since a round is a chain of dependent warp operations. A stable counting sort
-// of the pairs by expert follows: histograms, exclusive prefix sums, then each pair's rank among the
-// pairs before it by warp matches, so the order depends on nothing but the input. A few tokens run in
-// one thread block and one launch (128 tokens of 128 experts there: 19 us against 8 in two launches);
-// more run in two, where the second launch's blocks each sum the first's histograms themselves (at
-// most kRouteBlocks x E counts, from L2) instead of waiting for a third launch that scans them.
+// hold it the lowest, and in it the lowest expert, is the lowest expert of all. A lane's keys are put
+// in order first (up to 8 of them), so that taking one out of the warp is a shift: what bounds the
+// routing of many tokens is the number of instructions (600 a token while each round searched the
+// lane's keys). A stable counting sort of the pairs by expert follows: each pair's rank among the
+// block's pairs of its expert by warp matches, then the counts of the experts and blocks before, so the
+// order depends on nothing but the input. A few tokens run in one thread block and one launch (128
+// tokens of 128 experts there: 19 us against 8 in two launches); more run in two, where the second
+// launch's blocks each sum the first's histograms themselves (at most kRouteBlocks x E counts, from
+// L2) instead of waiting for a third launch that scans them.
 constexpr int kSortWarps = 8;         // warps that rank a block's pairs
-constexpr int kSmallThreads = 1024;
-constexpr int kBigThreads = 512;      // two blocks on an SM
+constexpr int kRouteThreads = 1024;
+constexpr int kHeldPairs = 4096;      // experts of a block's pairs held in shared memory (more are read back)
 
 struct RouteArgs {
     int T, E, k, renorm;
@@ -55,96 +57,122 @@ __device__ __forceinline__ float from_key(uint32_t k) {
 // exp(x - top), where equal infinities count as equal values
 __device__ __forceinline__ float rel_exp(float x, float top) { return x == top ? 1.f : expf(x - top); }
 
-// The choices of tokens t, t + step, ... (kSide of them, those below t1) by the calling warp: writes
-// expert and weight and counts each expert's pairs.
-template <int DT, int EL, int kSide>
-__device__ __forceinline__ void choose(const RouteArgs& a, int t, int step, int t1, int lane, int32_t* counts) {
-    uint32_t key[kSide][EL], best[kSide], first[kSide], mine[kSide];
-    float all[kSide];
+// Token t's choice by the calling warp: writes expert (also to held, from pair p0 on) and weight, and
+// counts each expert's pairs.
+template <int DT, int EL>
+__device__ __forceinline__ void choose(const RouteArgs& a, int t, int lane, int32_t* counts, int16_t* held, size_t p0) {
+    constexpr bool kOrdered = EL <= 8;
+    uint32_t key[EL], id[EL];
+    const size_t from = (size_t)((long long)t * a.ld) + lane * EL;
 #pragma unroll
-    for (int i = 0; i < kSide; ++i) {
-        best[i] = first[i] = mine[i] = 0u;
-        all[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < EL; ++j) {
-            const int e = lane * EL + j;
-            key[i][j] = t + i * step < t1 && e < a.E ? to_key(load_as_float<DT>(a.logits, (size_t)((long long)(t + i * step) * a.ld) + e)) : 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < EL; ++j) best[i] = max(best[i], key[i][j]);
+    for (int j = 0; j < EL; ++j) {
+        key[j] = lane * EL + j < a.E ? to_key(load_as_float<DT>(a.logits, from + j)) : 0u;
+        id[j] = j;
     }
+    uint32_t ids = 0, best = 0;      // kOrdered: the keys' places in the lane, 4 bits each
+    if constexpr (kOrdered) {
+        // exchanges of neighbours: equal keys keep their order
+#pragma unroll
+        for (int pass = 0; pass < EL; ++pass)
+#pragma unroll
+            for (int j = pass & 1; j + 1 < EL; j += 2) {
+                const bool swap = key[j + 1] > key[j];
+                const uint32_t hi = max(key[j], key[j + 1]), lo = min(key[j], key[j + 1]);
+                const uint32_t i0 = swap ? id[j + 1] : id[j], i1 = swap ? id[j] : id[j + 1];
+                key[j] = hi;
+                key[j + 1] = lo;
+                id[j] = i0;
+                id[j + 1] = i1;
+            }
+#pragma unroll
+        for (int j = 0; j < EL; ++j) ids |= id[j] << (4 * j);
+        best = key[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < EL; ++j) best = max(best, key[j]);
+    }
+    uint32_t first = 0, mine = 0;    // the largest key; lane r's: the r-th largest (0: none is left)
+    int expert = -1;
     for (int r = 0; r < a.k; ++r) {
-        uint32_t top[kSide];
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (top == 0) break;
+        if (r == 0) first = top;
+        const int holder = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+        int place;
+        if constexpr (kOrdered) {
+            place = (int)(ids & 15u);
+        } else {
+            place = 0;
 #pragma unroll
-        for (int i = 0; i < kSide; ++i) top[i] = __reduce_max_sync(0xffffffffu, best[i]);
+            for (int j = EL - 1; j > 0; --j) place = key[j] == top ? j : place;
+            if (key[0] == top) place = 0;
+        }
+        const int e = __shfl_sync(0xffffffffu, lane * EL + place, holder);
+        if (lane == r) {
+            mine = top;
+            expert = e;
+        }
+        if (lane == holder) {
+            if constexpr (kOrdered) {
 #pragma unroll
-        for (int i = 0; i < kSide; ++i) {
-            if (r == 0) first[i] = top[i];
-            if (lane == r) mine[i] = top[i];       // this lane's choice has the r-th largest key (0: none is left)
-            const uint32_t holders = __ballot_sync(0xffffffffu, best[i] == top[i]);
-            if (t + i * step < t1) {
-                const size_t at = (size_t)(t + i * step) * a.k + r;
-                if (!top[i]) {
-                    if (lane == 0) a.expert[at] = -1;
-                } else if (lane == __ffs(holders) - 1) {
-                    uint32_t rest = 0;
-                    bool taken = false;
+                for (int j = 0; j + 1 < EL; ++j) key[j] = key[j + 1];
+                key[EL - 1] = 0u;
+                ids >>= 4;
+                best = key[0];
+            } else {
+                best = 0;
 #pragma unroll
-                    for (int j = 0; j < EL; ++j) {
-                        if (!taken && key[i][j] == top[i]) {
-                            taken = true;
-                            key[i][j] = 0u;
-                            a.expert[at] = lane * EL + j;
-                            atomicAdd(counts + lane * EL + j, 1);
-                        }
-                        rest = max(rest, key[i][j]);
-                    }
-                    best[i] = rest;
+                for (int j = 0; j < EL; ++j) {
+                    if (j == place) key[j] = 0u;
+                    best = max(best, key[j]);
                 }
             }
         }
     }
+    const float top = from_key(first), w = mine ? rel_exp(from_key(mine), top) : 0.f;
+    float all = w;
+    if (!a.renorm) {
+        // over all experts: the ones not chosen are still in key, the chosen ones' terms are w
 #pragma unroll
-    for (int i = 0; i < kSide; ++i) {
-        if (t + i * step >= t1) continue;      // (the same for the whole warp)
-        const float top = from_key(first[i]), w = mine[i] ? rel_exp(from_key(mine[i]), top) : 0.f;
-        all[i] = w;
-        if (!a.renorm && first[i]) {
-            // over all experts: the ones not chosen are still in key, the chosen ones' terms are w
+        for (int j = 0; j < EL; ++j)
+            if (key[j]) all += rel_exp(from_key(key[j]), top);
+    }
 #pragma unroll
-            for (int j = 0; j < EL; ++j)
-                if (key[i][j]) all[i] += rel_exp(from_key(key[i][j]), top);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) all[i] += __shfl_xor_sync(0xffffffffu, all[i], o);
-        if (lane < a.k) a.weight[(size_t)(t + i * step) * a.k + lane] = mine[i] ? w / all[i] : 0.f;
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane < a.k) {
+        const size_t at = (size_t)t * a.k + lane;
+        a.expert[at] = expert;
+        a.weight[at] = mine ? w / all : 0.f;
+        if (at - p0 < kHeldPairs) held[at - p0] = (int16_t)expert;
+        if (expert >= 0) atomicAdd(counts + expert, 1);
     }
 }
 
 // The choice of tokens [t0, t1) by all warps of the block; counts[e] gets the block's pairs per
 // expert (shared memory, cleared here; integer sums, so their order does not matter).
 template <int DT, int EL>
-__device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int t1, int32_t* counts) {
-    constexpr int kSide = EL <= 4 ? 4 : (EL <= 8 ? 2 : 1);
+__device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int t1, int32_t* counts, int16_t* held) {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) counts[e] = 0;
     __syncthreads();
     const int warps = blockDim.x >> 5;
-    for (int t = t0 + (int)(threadIdx.x >> 5); t < t1; t += kSide * warps)
-        choose<DT, EL, kSide>(a, t, warps, t1, threadIdx.x & 31, counts);
+    for (int t = t0 + (int)(threadIdx.x >> 5); t < t1; t += warps)
+        choose<DT, EL>(a, t, threadIdx.x & 31, counts, held, (size_t)t0 * a.k);
     __syncthreads();
 }
 
-// Stable placement of pairs [p0, p1): base[e] = position of the block's first pair of expert e.
-// start: [kSortWarps][E] shared memory. Every warp of the block calls it.
-__device__ __forceinline__ void place_block(const RouteArgs& a, int p0, int p1, const int32_t* base, int32_t* start) {
+// Stable positions of pairs [p0, p1) to slot: base[e] (none: 0) plus the pair's rank among the block's
+// pairs of its expert; with base, the token to row, too. start: [kSortWarps][E] shared memory. Every
+// thread of the block calls it.
+__device__ __forceinline__ void place_block(const RouteArgs& a, int p0, int p1, const int16_t* held, const int32_t* base, int32_t* start) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < kSortWarps * a.E; i += blockDim.x) start[i] = 0;
     __syncthreads();
     const int seg = ((p1 - p0 + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-    const int b = min(p0 + warp * seg, p1), e1 = min(b + seg, p1);
+    const int b = min(p0 + warp * seg, p1), e1 = min(b + seg, p1), full = b + (e1 - b + 31) / 32 * 32;
+    auto expert = [&](int p) { return p >= e1 ? -1 : (p - p0 < kHeldPairs ? (int)held[p - p0] : a.expert[p]); };
     if (warp < kSortWarps) {
-        for (int p = b + lane; p < b + (e1 - b + 31) / 32 * 32; p += 32) {
-            const int e = p < e1 ? a.expert[p] : -1;
+        for (int p = b + lane; p < full; p += 32) {
+            const int e = expert(p);
             const uint32_t same = __match_any_sync(0xffffffffu, e);
             if (e >= 0 && lane == __ffs(same) - 1) start[warp * a.E + e] += __popc(same);
             __syncwarp();
@@ -152,7 +180,8 @@ __device__ __forceinline__ void place_block(const RouteArgs& a, int p0, int p1, 
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        int at = base[e];
+        int at = base ? base[e] : 0;
+#pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
             const int c = start[w * a.E + e];
             start[w * a.E + e] = at;
@@ -161,13 +190,13 @@ __device__ __forceinline__ void place_block(const RouteArgs& a, int p0, int p1, 
     }
     __syncthreads();
     if (warp < kSortWarps) {
-        for (int p = b + lane; p < b + (e1 - b + 31) / 32 * 32; p += 32) {
-            const int e = p < e1 ? a.expert[p] : -1;
+        for (int p = b + lane; p < full; p += 32) {
+            const int e = expert(p);
             const uint32_t same = __match_any_sync(0xffffffffu, e);
             int at = -1;
             if (e >= 0) {
                 at = start[warp * a.E + e] + __popc(same & ((1u << lane) - 1u));
-                a.row[at] = p / a.k;
+                if (base) a.row[at] = p / a.k;
             }
             if (p < e1) a.slot[p] = at;
             __syncwarp();
@@ -198,31 +227,34 @@ __device__ __forceinline__ void prefix(const int32_t* v, int32_t* out, int E) {
 }
 
 template <int DT, int EL>
-__global__ void __launch_bounds__(kSmallThreads) route_small_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads) route_small_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
+    __shared__ int16_t held[kHeldPairs];
     int32_t *counts = sm, *first = sm + a.E, *start = first + a.E + 1;
-    choose_block<DT, EL>(a, 0, a.T, counts);     // (its last barrier orders the experts it wrote, too)
+    choose_block<DT, EL>(a, 0, a.T, counts, held);
     prefix(counts, first, a.E);
     for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.offsets[e] = first[e];
     for (int p = first[a.E] + threadIdx.x; p < a.T * a.k; p += blockDim.x) a.row[p] = -1;
-    place_block(a, 0, a.T * a.k, first, start);
+    place_block(a, 0, a.T * a.k, held, first, start);
 }
 
 template <int DT, int EL>
-__global__ void __launch_bounds__(kBigThreads) route_choose_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
+    __shared__ int16_t held[kHeldPairs];
     const int t0 = min(blockIdx.x * a.per_block, a.T), t1 = min(t0 + a.per_block, a.T);
-    choose_block<DT, EL>(a, t0, t1, sm);
+    choose_block<DT, EL>(a, t0, t1, sm, held);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(size_t)blockIdx.x * a.E + e] = sm[e];
+    place_block(a, t0 * a.k, t1 * a.k, held, nullptr, sm + a.E);
 }
 
-__global__ void __launch_bounds__(kBigThreads) route_place_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
-    int32_t *total = sm, *before = sm + a.E, *first = before + a.E, *start = first + a.E + 1;
+    int32_t *total = sm, *before = sm + a.E, *first = before + a.E;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the choices are written
     for (int e = threadIdx.x; e < 2 * a.E; e += blockDim.x) sm[e] = 0;
     __syncthreads();
-    // the pairs per expert in all blocks, and in the blocks before this one: 16 histograms at a time
-    // to a group of threads
+    // the pairs per expert in all blocks, and in the blocks before this one
     const int groups = max((int)blockDim.x / a.E, 1);
     for (int i = threadIdx.x; i < groups * a.E; i += blockDim.x) {
         const int g = i / a.E, e = i - g * a.E;
@@ -242,27 +274,44 @@ __global__ void __launch_bounds__(kBigThreads) route_place_kernel(const RouteArg
         for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.offsets[e] = first[e];
         for (int p = first[a.E] + threadIdx.x; p < a.T * a.k; p += blockDim.x) a.row[p] = -1;
     }
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) before[e] += first[e];
-    __syncthreads();
-    const int t0 = min(blockIdx.x * a.per_block, a.T), t1 = min(t0 + a.per_block, a.T);
-    place_block(a, t0 * a.k, t1 * a.k, before, start);
+    const int t0 = min(blockIdx.x * a.per_block, a.T), p0 = t0 * a.k, p1 = min(t0 + a.per_block, a.T) * a.k;
+    for (int p = p0 + threadIdx.x; p < p1; p += blockDim.x) {
+        const int e = __ldg(a.expert + p);
+        if (e < 0) continue;
+        const int at = first[e] + before[e] + a.slot[p];
+        a.slot[p] = at;
+        a.row[at] = p / a.k;
+    }
 }
 
 template <int DT, int EL>
 cudaError_t route_el(RouteArgs a, cudaStream_t s) {
     const size_t sort = (size_t)kSortWarps * a.E * sizeof(int32_t);
     if (!route_needs_workspace(a.T)) {
-        route_small_kernel<DT, EL><<<1, kSmallThreads, (2 * a.E + 1) * sizeof(int32_t) + sort, s>>>(a);
+        const int threads = 32 * (a.T > kSortWarps ? a.T : kSortWarps);     // a warp per token
+        route_small_kernel<DT, EL><<<1, threads, (2 * a.E + 1) * sizeof(int32_t) + sort, s>>>(a);
         return cudaGetLastError();
     }
-    const int want = (a.T + 15) / 16;      // a token a warp at least
+    // blocks of at least 8 tokens, a warp per token up to 32 of them
+    const int want = (a.T + 7) / 8;
     const int blocks = want < kRouteBlocks ? want : kRouteBlocks;
     a.per_block = (a.T + blocks - 1) / blocks;
-    route_choose_kernel<DT, EL><<<blocks, kBigThreads, a.E * sizeof(int32_t), s>>>(a);
+    const int warps = a.per_block < kSortWarps ? kSortWarps : (a.per_block < kRouteThreads / 32 ? a.per_block : kRouteThreads / 32);
+    route_choose_kernel<DT, EL><<<blocks, 32 * warps, a.E * sizeof(int32_t) + sort, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    route_place_kernel<<<blocks, kBigThreads, (3 * a.E + 1) * sizeof(int32_t) + sort, s>>>(a);
-    return cudaGetLastError();
+    // the second launch may come up while the first ends; it waits for it before it reads anything
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kRouteThreads);
+    cfg.dynamicSmemBytes = (3 * a.E + 1) * sizeof(int32_t);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, route_place_kernel, a);
 }
 
 template <int DT>
