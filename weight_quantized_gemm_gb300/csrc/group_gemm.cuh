@@ -78,10 +78,11 @@ struct Plan {
     static constexpr bool kOverlap = 2 * BN + kScaleCols > 512;
     static constexpr int kAcc1 = kOverlap ? (512 - kScaleCols - BN) / 16 * 16 : BN;
     static constexpr int kSaCol = kAcc1 + BN, kSbCol = kSaCol + 4 * kChunks;
-    static constexpr int kShared = kOverlap ? (BN - kAcc1 + 15) / 16 : 0;  // chunks of 16 columns with shared ones
+    static constexpr int kWide = BN == 32 ? 16 : 32;                       // columns of an epilogue chunk
+    static constexpr int kShared = kOverlap ? (BN - kAcc1 + kWide - 1) / kWide : 0;      // chunks with shared columns
     static_assert(kStage % 1024 == 0, "stages keep the 128-byte swizzle's alignment");
     static_assert(kStages >= 4, "ring");
-    static_assert(kAcc1 + BN + kScaleCols <= 512 && kShared <= 4, "tensor memory");
+    static_assert(kAcc1 + BN + kScaleCols <= 512, "tensor memory");
 };
 
 struct Params {
@@ -199,7 +200,7 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, in
     else
         ptx::tma_load_3d(dst, map, x, y, z, bar);
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
@@ -210,6 +211,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -281,34 +297,35 @@ struct Tile {
     int e, n0, m0, rows;       // expert, first channel (of this block), first row, rows
 };
 
-// Two neighbouring channels' values of the chunk's 16 rows, exchanged between the lanes of a pair: the
-// even lane ends with both channels of rows 0-7 (first[i], second[i]), the odd lane with rows 8-15.
-__device__ __forceinline__ void pair_up(const float (&v)[16], float (&first)[8], float (&second)[8], bool odd) {
+// Two neighbouring channels' values of the chunk's 2 W rows, exchanged between the lanes of a pair: the
+// even lane ends with both channels of the first W rows (first[i], second[i]), the odd lane of the rest.
+template <int W>
+__device__ __forceinline__ void pair_up(const float (&v)[2 * W], float (&first)[W], float (&second)[W], bool odd) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 8], 1);
+    for (int i = 0; i < W; ++i) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + W], 1);
         first[i] = odd ? got : v[i];
-        second[i] = odd ? v[i + 8] : got;
+        second[i] = odd ? v[i + W] : got;
     }
 }
 
-template <int ACT>
-__device__ __forceinline__ void act16(float (&v)[16]) {
+template <int ACT, int W>
+__device__ __forceinline__ void act_all(float (&v)[W]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = act_fixed<ACT>(v[i]);
+    for (int i = 0; i < W; ++i) v[i] = act_fixed<ACT>(v[i]);
 }
 
-// The rest of the epilogue for 16 rows m .. m + 15 (the first `live` of them) of channel n: activation,
+// The rest of the epilogue for 2 W rows from m on (the first `live` of them) of channel n: activation,
 // residual, rounding, stores. One choice of activation and type per chunk, none per value. 16-bit
-// outputs leave as pairs of channels (64 contiguous bytes a row), of rows 0-7 from the even lanes
-// and 8-15 from the odd ones; SwiGLU pairs become one channel the same way.
-template <int CDT>
-__device__ __forceinline__ void store_chunk(const Params& p, float (&v)[16], int n, int m, int live, bool odd) {
+// outputs leave as pairs of channels (64 contiguous bytes a row), of the first W rows from the even
+// lanes and the others from the odd ones; SwiGLU pairs become one channel the same way.
+template <int CDT, int W>
+__device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], int n, int m, int live, bool odd) {
     constexpr size_t kEsz = CDT == DT_F32 ? 4 : 2;
     switch (p.act) {
-        case ACT_RELU: act16<ACT_RELU>(v); break;
-        case ACT_SILU: act16<ACT_SILU>(v); break;
-        case ACT_GELU_TANH: act16<ACT_GELU_TANH>(v); break;
+        case ACT_RELU: act_all<ACT_RELU>(v); break;
+        case ACT_SILU: act_all<ACT_SILU>(v); break;
+        case ACT_GELU_TANH: act_all<ACT_GELU_TANH>(v); break;
         default: break;
     }
     const bool glu = p.act == ACT_SWIGLU;
@@ -328,23 +345,23 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[16], int
             if (i < rows) store_out_rt(out + i * step, 0, y[i], CDT);
     };
     if (glu || (CDT != DT_F32 && (p.N & 1) == 0)) {
-        float a[8], b[8];
-        pair_up(v, a, b, odd);
-        const int row = m + (odd ? 8 : 0), rows = live - (odd ? 8 : 0);
+        float a[W], b[W];
+        pair_up<W>(v, a, b, odd);
+        const int row = m + (odd ? W : 0), rows = live - (odd ? W : 0);
         if (n >= p.N) return;              // (N is even here: both lanes of a pair)
         if (glu) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] = act_fixed<ACT_SILU>(a[i]) * b[i];
-            column(a, row, n >> 1, rows, std::integral_constant<int, 8>());
+            for (int i = 0; i < W; ++i) a[i] = act_fixed<ACT_SILU>(a[i]) * b[i];
+            column(a, row, n >> 1, rows, std::integral_constant<int, W>());
         } else if constexpr (CDT != DT_F32) {
             const size_t at = ((size_t)row * p.cols + (n & ~1)) * kEsz;
             if (p.residual) {
-                uint32_t r[8];
+                uint32_t r[W];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < W; ++i)
                     r[i] = i < rows ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.residual) + at + i * step)) : 0u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < W; ++i) {
                     if constexpr (CDT == DT_F16) {
                         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
                         a[i] += f.x;
@@ -357,7 +374,7 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[16], int
             }
             uint8_t* out = static_cast<uint8_t*>(p.C) + at;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < W; ++i) {
                 uint32_t w;
                 if constexpr (CDT == DT_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b[i]), "f"(a[i]));
                 else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b[i]), "f"(a[i]));
@@ -365,7 +382,7 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[16], int
             }
         }
     } else if (n < p.N) {
-        column(v, m, n, live, std::integral_constant<int, 16>());
+        column(v, m, n, live, std::integral_constant<int, 2 * W>());
     }
 }
 
@@ -781,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                     const int c0 = 16 * h;
                     if (c0 < x.rows) {
                         float v[16];
-                        tmem_ld16(acc + (uint32_t)c0, v);
+                        tmem_ld(acc + (uint32_t)c0, v);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (c0 + i < x.rows) peer_store(to + (uint32_t)((c0 + i) * share) * 4, v[i], to_bar);
@@ -794,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                         const int c0 = 16 * (kParts * h + j);
                         if (c0 >= x.rows) break;
                         float v[16];
-                        tmem_ld16(acc + (uint32_t)c0, v);
+                        tmem_ld(acc + (uint32_t)c0, v);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             if (c0 + i < x.rows) own[(c0 + i) * share] = v[i];
@@ -831,21 +848,21 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                     finish4(p, y, x.e, (size_t)(x.m0 + row), n);
                 }
             } else {
-                // (x is in registers of every lane; its chunk's rows are x.m0 + c0 + i)
                 const int n = x.n0 + 32 * q + lane;
                 const size_t en = (size_t)x.e * p.N + min(n, p.N - 1);
                 const float ws = p.b_scale ? __ldg(p.b_scale + en) : 1.f;
                 const float bias = p.bias ? __ldg(p.bias + en) : 0.f;
+                constexpr int kWide = P::kWide, kMine = BN / (2 * kWide);     // chunks of a column half
 #pragma unroll 1
-                for (int j = 0; j < kParts; ++j) {
+                for (int j = 0; j < kMine; ++j) {
                     // chunks alternate between the halves; overlapping accumulators share the first one's
                     // last columns and the second one's first: those go first
-                    const int i2 = 2 * j + h, c0 = 16 * (P::kOverlap && !(tj & 1) ? 2 * kParts - 1 - i2 : i2);
-                    const int live = min(16, x.rows - c0);       // rows of this chunk (none: <= 0)
-                    float v[16];
+                    const int i2 = 2 * j + h, c0 = kWide * (P::kOverlap && !(tj & 1) ? 2 * kMine - 1 - i2 : i2);
+                    const int live = min(kWide, x.rows - c0);       // rows of this chunk (none: <= 0)
+                    float v[kWide];
                     __syncwarp();
-                    if (live > 0) tmem_ld16(acc + (uint32_t)c0, v);
-                    if (j == (P::kOverlap ? (P::kShared + 1) / 2 - 1 : kParts - 1)) {
+                    if (live > 0) tmem_ld(acc + (uint32_t)c0, v);
+                    if (j == (P::kOverlap ? (P::kShared + 1) / 2 - 1 : kMine - 1)) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
@@ -857,15 +874,15 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                     if (live <= 0) continue;
                     const int m = x.m0 + c0;
                     if (p.a_scale) {
-                        const float as = __ldg(p.a_scale + m + min(lane & 15, live - 1));
+                        const float as = __ldg(p.a_scale + m + min(lane & (kWide - 1), live - 1));
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] *= __shfl_sync(0xffffffffu, as, i);
+                        for (int i = 0; i < kWide; ++i) v[i] *= __shfl_sync(0xffffffffu, as, i);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], ws, bias);
-                    if (p.c_dtype == DT_BF16) store_chunk<DT_BF16>(p, v, n, m, live, odd);
-                    else if (p.c_dtype == DT_F16) store_chunk<DT_F16>(p, v, n, m, live, odd);
-                    else store_chunk<DT_F32>(p, v, n, m, live, odd);
+                    for (int i = 0; i < kWide; ++i) v[i] = fmaf(v[i], ws, bias);
+                    if (p.c_dtype == DT_BF16) store_chunk<DT_BF16, kWide / 2>(p, v, n, m, live, odd);
+                    else if (p.c_dtype == DT_F16) store_chunk<DT_F16, kWide / 2>(p, v, n, m, live, odd);
+                    else store_chunk<DT_F32, kWide / 2>(p, v, n, m, live, odd);
                 }
                 __syncwarp();
             }
