@@ -309,10 +309,19 @@ __device__ __forceinline__ void pair_up(const float (&v)[2 * W], float (&first)[
     }
 }
 
+// v * sigmoid(v), for the tensor-core tiles: the exponential and the reciprocal without the handling
+// of subnormal numbers, which cannot show in 1 + e^-v (half the instructions of epilogue.cuh's form, the
+// same few units in the last place).
+__device__ __forceinline__ float silu(float v) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return v * r;
+}
 template <int ACT, int W>
 __device__ __forceinline__ void act_all(float (&v)[W]) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = act_fixed<ACT>(v[i]);
+    for (int i = 0; i < W; ++i) v[i] = ACT == ACT_SILU ? silu(v[i]) : act_fixed<ACT>(v[i]);
 }
 
 // The rest of the epilogue for 2 W rows from m on (the first `live` of them) of channel n: activation,
@@ -351,7 +360,7 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], 
         if (n >= p.N) return;              // (N is even here: both lanes of a pair)
         if (glu) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) a[i] = act_fixed<ACT_SILU>(a[i]) * b[i];
+            for (int i = 0; i < W; ++i) a[i] = silu(a[i]) * b[i];
             column(a, row, n >> 1, rows, std::integral_constant<int, W>());
         } else if constexpr (CDT != DT_F32) {
             const size_t at = ((size_t)row * p.cols + (n & ~1)) * kEsz;
