@@ -654,14 +654,20 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             int tu = tf, q = first, gb = 0;
             auto write = [&](uint4 (&v)[4]) {
                 if (tu >= total) return false;
+                // a piece's stages together: one wait, one fence
+                bool go = true;
+                int slot[kPer];
 #pragma unroll
                 for (int d = 0; d < kPer; ++d) {
-                    const int i = q * kPer + d - ks0;
-                    if (i < 0 || i >= nks) continue;
-                    const int g = gb + i, s = g % S;
-                    const bool go = !*abort_flag && (g < S || wait(empty(s), (uint32_t)(g / S - 1) & 1u));
-                    if (!__all_sync(0xffffffffu, go)) return false;
-                    const uint32_t dst = ring + (uint32_t)s * P::kStage + P::kA + P::kB + P::kSA + half * 512 + lane * 16;
+                    const int i = q * kPer + d - ks0, g = gb + i;
+                    slot[d] = i < 0 || i >= nks ? -1 : g % S;
+                    if (slot[d] >= 0 && g >= S) go = go && wait(empty(slot[d]), (uint32_t)(g / S - 1) & 1u);
+                }
+                if (!__all_sync(0xffffffffu, go)) return false;
+#pragma unroll
+                for (int d = 0; d < kPer; ++d) {
+                    if (slot[d] < 0) continue;
+                    const uint32_t dst = ring + (uint32_t)slot[d] * P::kStage + P::kA + P::kB + P::kSA + half * 512 + lane * 16;
 #pragma unroll
                     for (int c = 0; c < P::kChunks; ++c) {
                         constexpr int kWords = P::kChunks;       // words of a row per stage
@@ -673,9 +679,12 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                                      "r"(word(v[1])), "r"(word(v[2])), "r"(word(v[3]))
                                      : "memory");
                     }
-                    ptx::fence_proxy_async_smem();       // visible to the tensor core's copies
-                    __syncwarp();
-                    if (lane == 0) {
+                }
+                ptx::fence_proxy_async_smem();       // visible to the tensor core's copies
+                __syncwarp();
+                if (lane < kPer) {
+                    const int s = kPer == 2 && lane == 1 ? slot[kPer - 1] : slot[0];
+                    if (s >= 0) {
                         if constexpr (kPair) peer_signal(lead(full(s)));
                         else ptx::mbar_arrive(full(s));
                     }
