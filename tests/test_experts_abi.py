@@ -45,7 +45,7 @@ QUANT = dict(M=4, K=128, X=FAKE, x_dtype=2, ldx=128, x_rows=4, rows=None, fmt=4,
     (dict(M=-1), ARG), (dict(K=0), ARG), (dict(K=96), UNSUP), (dict(fmt=2), ARG), (dict(x_dtype=3), ARG), (dict(layout=2), ARG),
     (dict(ldx=127), ARG), (dict(x_rows=3), ARG), (dict(x_rows=-1), ARG), (dict(X=None), ARG), (dict(codes=None), ARG),
     (dict(scales=None), ARG), (dict(row_scale=None), ARG), (dict(X=FAKE + 2), ALIGN), (dict(codes=FAKE + 8), ALIGN),
-    (dict(rows=FAKE + 4), ALIGN), (dict(ldx=130), ALIGN), (dict(K=1 << 26, ldx=1 << 26), UNSUP), (dict(M=0, X=None), 0)])
+    (dict(rows=FAKE + 4), ALIGN), (dict(ldx=130), ALIGN), (dict(M=(1 << 30) + 1, x_rows=(1 << 31) - 1), UNSUP), (dict(K=1 << 26, ldx=1 << 26), UNSUP), (dict(M=0, X=None), 0)])
 def test_quant_refuses(args, code):
     assert call("qgemm_fp4_quant", QUANT, args) == code
 
@@ -78,7 +78,7 @@ RUN = dict(M=4, K=128, N=64, fmt=3, A=FAKE, As=FAKE, a_scale=None, Bp=FAKE, Bs=F
     (dict(fmt=2), ARG), (dict(fmt=5), ARG), (dict(M=-1), ARG), (dict(N=-1), ARG), (dict(K=0), ARG), (dict(K=96), UNSUP),
     (dict(act=5), ARG), (dict(act=-1), ARG), (dict(act=4, N=63), UNSUP), (dict(c_dtype=3), ARG), (dict(A=None), ARG), (dict(As=None), ARG),
     (dict(Bs=None), ARG), (dict(C=None), ARG), (dict(C=FAKE + 2), ALIGN), (dict(a_scale=FAKE + 4), ALIGN), (dict(bias=FAKE + 8), ALIGN),
-    (dict(residual=FAKE + 2), ALIGN), (dict(M=0, A=None), 0), (dict(N=0), 0)])
+    (dict(residual=FAKE + 2), ALIGN), (dict(M=(1 << 31) - 1), UNSUP), (dict(N=(1 << 30) + 2), UNSUP), (dict(M=0, A=None), 0), (dict(N=0), 0)])
 def test_run_refuses(args, code):
     assert call("qgemm_fp4_run", RUN, args) == code
 

@@ -44,7 +44,7 @@ def check_route(x, k, renorm):
 
 @pytest.mark.parametrize("renorm", [0, 1])
 @pytest.mark.parametrize("T,E,k,dt", [(1, 8, 2, 2), (1, 1, 1, 0), (8, 64, 8, 2), (33, 60, 4, 1), (128, 128, 8, 0), (129, 16, 1, 2),
-                                      (700, 256, 8, 0), (2500, 33, 6, 2), (300, 1024, 32, 0), (5000, 8, 8, 1), (64, 1000, 32, 2)])
+                                      (700, 256, 8, 0), (2500, 33, 6, 2), (5, 1024, 32, 0), (32, 1023, 32, 2), (20000, 64, 30, 2), (300, 1024, 32, 0), (5000, 8, 8, 1), (64, 1000, 32, 2)])
 def test_route(T, E, k, dt, renorm):
     g = torch.Generator(device=DEV).manual_seed(T + E + k)
     x = torch.randn(T, E, generator=g, device=DEV).to(torch_dtype(dt))
@@ -162,6 +162,38 @@ def test_grouped_offsets_out_of_range():
             hi = min(max(off[e + 1], lo), T)
             want[lo:hi] = (a[lo:hi].float() @ b[e].float().T).cpu()
         assert torch.allclose(C.cpu(), want, rtol=1e-3, atol=1e-3)
+
+
+@pytest.mark.parametrize("fmt", [2, 3])
+def test_grouped_weights_past_32_bits(fmt):
+    """Experts whose weights lie more than 2^32 bytes (and 2^31 values) into the array."""
+    E, N, K = (300, 2048, 4096) if fmt == 2 else (300, 4096, 8192)
+    T, per = 6, 2
+    last = [0, 254, 299]
+    b = torch.randint(0, 256, (E, N, K // 2 if fmt == 3 else 2 * K), dtype=torch.uint8, device=DEV)
+    sizes = torch.zeros(E, dtype=torch.int64)
+    sizes[last] = per
+    offsets = torch.cat((torch.zeros(1, dtype=torch.int64), sizes.cumsum(0))).to(torch.int32).to(DEV)
+    if fmt == 3:
+        a, a_s, _ = gpu_quant(torch.randn(T, K, device=DEV), T, K, 3)
+        one = qg.qgemm_fp4_scales_bytes(N, K, 3, 1)
+        b_s = torch.randint(118, 122, (E * one,), dtype=torch.uint8, device=DEV)
+    else:
+        b = b.view(torch.int16).bitwise_and_(0x3FFF).view(torch.bfloat16)      # finite, below 2
+        a, a_s, b_s = torch.randn(T, K, device=DEV).bfloat16(), None, None
+    C = torch.zeros(T, N, device=DEV)
+    qg.qgemm_grouped_run(T, E, K, N, fmt, offsets, a, a_s, None, b, b_s, None, None, 0, C, 0)
+    assert qg.qgemm_status() == 0
+    for i, e in enumerate(last):
+        rows = slice(per * i, per * (i + 1))
+        if fmt == 3:
+            a64 = ref.values(ref.unpack(a[rows].cpu().numpy()), a_s.cpu().numpy().reshape(T, -1)[rows, : K // 32], None, 3)
+            tiles = b_s[e * one : (e + 1) * one].cpu().numpy().reshape(N // 128, K // 128, 32, 4, 4)
+            sc = tiles.transpose(0, 3, 2, 1, 4).reshape(N, K // 32)
+            b64 = ref.values(ref.unpack(b[e].cpu().numpy()), sc, None, 3)
+        else:
+            a64, b64 = host(a[rows]), host(b[e])
+        check_out(C[rows], *ref.product(a64, b64, None, None, None, 0, None), 0)
 
 
 # ---------------------------------------------------------------- combination

@@ -108,6 +108,21 @@ def test_quant_gather_and_strides(fmt):
 
 
 @pytest.mark.parametrize("fmt", [MX, NV])
+def test_quant_and_dequant_past_32_bits(fmt):
+    """Rows more than 2^32 bytes and 2^31 values into X, Y and past 2^30 into the codes."""
+    M, K = 530000, 4160
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=DEV).normal_()
+    codes, sb, rs = gpu_quant(x, M, K, fmt)
+    y = torch.empty_like(x)
+    qg.qgemm_fp4_dequant(M, K, fmt, 0, codes, sb, rs, y, 2)
+    for m in (0, 258111, 516223, M - 1):                # around 2^30 and 2^31 values, and the last
+        c, byte, row = ref.quantize(host(x[m : m + 1]), fmt)
+        assert np.array_equal(ref.unpack(codes[m : m + 1].cpu().numpy()), c)
+        want = ref.values(c, byte, row, fmt)
+        assert np.array_equal(host(y[m : m + 1]), want)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
 @pytest.mark.parametrize("dt", [0, 1, 2])
 def test_dequant(fmt, dt):
     """Every code under every scale byte; one rounding to the output type."""

@@ -29,12 +29,14 @@ bool all_aligned16(P... p) {
 }
 bool valid_dtype(int d) { return d == QGEMM_F32 || d == QGEMM_F16 || d == QGEMM_BF16; }
 bool is_fp4(int fmt) { return fmt == QGEMM_FMT_MXFP4 || fmt == QGEMM_FMT_NVFP4; }
+constexpr int kMaxRows = 1 << 30;      // of one call, so that rounding up to a tile stays an int
 bool valid_layout(int l) { return l == QGEMM_SCALES_ROWS || l == QGEMM_SCALES_TILED; }
 
 int check_fp4(int rows, int K, int fmt, const char* name) {
     if (!is_fp4(fmt)) return fail(QGEMM_ERR_ARG, "format %d is not a 4-bit format", fmt);
     if (rows < 0 || K <= 0) return fail(QGEMM_ERR_ARG, "invalid sizes %s=%d K=%d", name, rows, K);
     if (K % 64 != 0) return fail(QGEMM_ERR_UNSUPPORTED, "K=%d is not a multiple of 64", K);
+    if (rows > kMaxRows) return fail(QGEMM_ERR_UNSUPPORTED, "%s=%d exceeds %d rows", name, rows, kMaxRows);
     if (K > 16 * 32 * 65535) return fail(QGEMM_ERR_UNSUPPORTED, "K=%d exceeds the launch limit", K);
     return QGEMM_OK;
 }
@@ -50,6 +52,7 @@ int check_product(int M, int E, int K, int N, int fmt, const void* A, const void
     if (K % 64 != 0) return fail(QGEMM_ERR_UNSUPPORTED, "K=%d is not a multiple of 64", K);
     if (act == QGEMM_ACT_SWIGLU && N % 2 != 0)
         return fail(QGEMM_ERR_UNSUPPORTED, "SwiGLU pairs channels: N=%d is odd", N);
+    if (M > kMaxRows || N > kMaxRows) return fail(QGEMM_ERR_UNSUPPORTED, "M=%d or N=%d exceeds %d", M, N, kMaxRows);
     if (M == 0 || N == 0 || E == 0) return QGEMM_OK;
     if (!A || !Bp || !C) return fail(QGEMM_ERR_ARG, "null A, Bp or C");
     if (is_fp4(fmt) && (!As || !Bs)) return fail(QGEMM_ERR_ARG, "null block scales");

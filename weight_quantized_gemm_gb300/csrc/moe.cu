@@ -23,7 +23,8 @@ namespace {
 // L2) instead of waiting for a third launch that scans them.
 constexpr int kSortWarps = 8;         // warps that rank a block's pairs
 constexpr int kRouteThreads = 1024;
-constexpr int kHeldPairs = 4096;      // experts of a block's pairs held in shared memory (more are read back)
+constexpr int kHeldPairs = 3584;      // experts of a block's pairs held in shared memory (more are read back)
+static_assert((2 * 1024 + 1 + kSortWarps * 1024) * 4 + kHeldPairs * 2 <= 48 * 1024, "shared memory at 1024 experts");
 
 struct RouteArgs {
     int T, E, k, renorm;
