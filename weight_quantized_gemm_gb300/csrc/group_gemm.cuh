@@ -324,12 +324,27 @@ __device__ __forceinline__ void act_all(float (&v)[W]) {
     for (int i = 0; i < W; ++i) v[i] = ACT == ACT_SILU ? silu(v[i]) : act_fixed<ACT>(v[i]);
 }
 
-// The rest of the epilogue for 2 W rows from m on (the first `live` of them) of channel n: activation,
-// residual, rounding, stores. One choice of activation and type per chunk, none per value. 16-bit
-// outputs leave as pairs of channels (64 contiguous bytes a row), of the first W rows from the even
-// lanes and the others from the odd ones; SwiGLU pairs become one channel the same way.
-template <int CDT, int W>
-__device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], int n, int m, int live, bool odd) {
+template <int CDT>
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+    uint32_t w;
+    if constexpr (CDT == DT_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+// Of two words that hold two rows (halves) of one channel each, exchanged between lanes `mask` apart:
+// both channels of the first row (lower lane) or of the second (upper lane).
+__device__ __forceinline__ uint32_t both_channels(uint32_t own, int mask, bool upper) {
+    return __byte_perm(own, __shfl_xor_sync(0xffffffffu, own, mask), upper ? 0x3276u : 0x5410u);
+}
+
+// The rest of the epilogue for 2 W rows from m on (the first `live` of them; FULL: all) of channel n:
+// activation, residual, rounding, stores. One choice of activation and type per chunk, none per value;
+// the number of instructions here is what bounds tiles of short K. 16-bit outputs are rounded two rows to
+// a word and leave as pairs of channels (64 contiguous bytes a row), of the first W rows from the even
+// lanes and the others from the odd ones; SwiGLU pairs become one channel the same way, and channels of
+// neighbouring pairs leave together.
+template <int CDT, int W, bool FULL>
+__device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], int n, int m, int live, int lane) {
     constexpr size_t kEsz = CDT == DT_F32 ? 4 : 2;
     switch (p.act) {
         case ACT_RELU: act_all<ACT_RELU>(v); break;
@@ -337,7 +352,7 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], 
         case ACT_GELU_TANH: act_all<ACT_GELU_TANH>(v); break;
         default: break;
     }
-    const bool glu = p.act == ACT_SWIGLU;
+    const bool glu = p.act == ACT_SWIGLU, odd = lane & 1;
     const size_t step = (size_t)p.cols * kEsz;
     // `count` values of one channel in consecutive rows
     auto column = [&](float* y, int row, int col, int rows, auto count) {
@@ -350,49 +365,59 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], 
         }
         uint8_t* out = static_cast<uint8_t*>(p.C) + at * kEsz;
 #pragma unroll
-        for (int i = 0; i < kCount; ++i)
-            if (i < rows) store_out_rt(out + i * step, 0, y[i], CDT);
+        for (int i = 0; i < kCount; ++i, out += step)
+            if (i < rows) store_out_rt(out, 0, y[i], CDT);
     };
-    if (glu || (CDT != DT_F32 && (p.N & 1) == 0)) {
+    const int half = odd ? W : 0;      // this lane's rows after an exchange with its neighbour
+    if (glu) {
         float a[W], b[W];
         pair_up<W>(v, a, b, odd);
-        const int row = m + (odd ? W : 0), rows = live - (odd ? W : 0);
+#pragma unroll
+        for (int i = 0; i < W; ++i) a[i] = silu(a[i]) * b[i];
+        if (CDT != DT_F32 && !p.residual && (p.cols & 1) == 0) {
+            const int second = (lane >> 1) & 1;
+            uint8_t* out = static_cast<uint8_t*>(p.C) + ((size_t)(m + half + second) * p.cols + ((n >> 1) & ~1)) * kEsz;
+#pragma unroll
+            for (int i = 0; i < W; i += 2, out += 2 * step) {
+                const uint32_t w = both_channels(round2<CDT>(a[i], a[i + 1]), 2, second);
+                if (n < p.N && (FULL || half + second + i < live)) *reinterpret_cast<uint32_t*>(out) = w;
+            }
+        } else if (n < p.N) {
+            column(a, m + half, n >> 1, live - half, std::integral_constant<int, W>());
+        }
+    } else if (CDT != DT_F32 && (p.N & 1) == 0) {
+        const size_t at = ((size_t)(m + half) * p.cols + (n & ~1)) * kEsz;
+        uint8_t* out = static_cast<uint8_t*>(p.C) + at;
+        if (!p.residual) {
+#pragma unroll
+            for (int i = 0; i < W; ++i, out += step) {
+                const uint32_t w = both_channels(round2<CDT>(v[i], v[i + W]), 1, odd);
+                if (n < p.N && (FULL || half + i < live)) *reinterpret_cast<uint32_t*>(out) = w;
+            }
+            return;
+        }
+        float a[W], b[W];
+        pair_up<W>(v, a, b, odd);
         if (n >= p.N) return;              // (N is even here: both lanes of a pair)
-        if (glu) {
+        uint32_t r[W];
 #pragma unroll
-            for (int i = 0; i < W; ++i) a[i] = silu(a[i]) * b[i];
-            column(a, row, n >> 1, rows, std::integral_constant<int, W>());
-        } else if constexpr (CDT != DT_F32) {
-            const size_t at = ((size_t)row * p.cols + (n & ~1)) * kEsz;
-            if (p.residual) {
-                uint32_t r[W];
+        for (int i = 0; i < W; ++i)
+            r[i] = half + i < live ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.residual) + at + i * step)) : 0u;
 #pragma unroll
-                for (int i = 0; i < W; ++i)
-                    r[i] = i < rows ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.residual) + at + i * step)) : 0u;
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    if constexpr (CDT == DT_F16) {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
-                        a[i] += f.x;
-                        b[i] += f.y;
-                    } else {
-                        a[i] += __uint_as_float(r[i] << 16);
-                        b[i] += __uint_as_float(r[i] & 0xFFFF0000u);
-                    }
-                }
-            }
-            uint8_t* out = static_cast<uint8_t*>(p.C) + at;
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                uint32_t w;
-                if constexpr (CDT == DT_F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b[i]), "f"(a[i]));
-                else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b[i]), "f"(a[i]));
-                if (i < rows) *reinterpret_cast<uint32_t*>(out + i * step) = w;
-            }
+        for (int i = 0; i < W; ++i, out += step) {
+            float2 f;
+            if constexpr (CDT == DT_F16) f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+            else f = make_float2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u));
+            if (half + i < live) *reinterpret_cast<uint32_t*>(out) = round2<CDT>(a[i] + f.x, b[i] + f.y);
         }
     } else if (n < p.N) {
         column(v, m, n, live, std::integral_constant<int, 2 * W>());
     }
+}
+template <int CDT, int W>
+__device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], int n, int m, int live, int lane) {
+    if (W == 16 && live == 2 * W) store_chunk<CDT, W, W == 16>(p, v, n, m, live, lane);
+    else store_chunk<CDT, W, false>(p, v, n, m, live, lane);
 }
 
 __device__ __forceinline__ float element(const void* p, size_t i, int dt) {
@@ -796,7 +821,6 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     } else {
         // ---------------- epilogue
         const int q = warp & 3, h = (warp - kEpiWarp) >> 2;
-        const bool odd = lane & 1;
         const float* const part = reinterpret_cast<const float*>(smem + S * P::kStage);
         int tj = 0;
         for (int t = worker; t < total; t += workers, ++tj) {
@@ -896,11 +920,13 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
 #pragma unroll
                         for (int i = 0; i < kWide; ++i) v[i] *= __shfl_sync(0xffffffffu, as, i);
                     }
+                    if (p.b_scale || p.bias) {
 #pragma unroll
-                    for (int i = 0; i < kWide; ++i) v[i] = fmaf(v[i], ws, bias);
-                    if (p.c_dtype == DT_BF16) store_chunk<DT_BF16, kWide / 2>(p, v, n, m, live, odd);
-                    else if (p.c_dtype == DT_F16) store_chunk<DT_F16, kWide / 2>(p, v, n, m, live, odd);
-                    else store_chunk<DT_F32, kWide / 2>(p, v, n, m, live, odd);
+                        for (int i = 0; i < kWide; ++i) v[i] = fmaf(v[i], ws, bias);
+                    }
+                    if (p.c_dtype == DT_BF16) store_chunk<DT_BF16, kWide / 2>(p, v, n, m, live, lane);
+                    else if (p.c_dtype == DT_F16) store_chunk<DT_F16, kWide / 2>(p, v, n, m, live, lane);
+                    else store_chunk<DT_F32, kWide / 2>(p, v, n, m, live, lane);
                 }
                 __syncwarp();
             }
