@@ -4,6 +4,7 @@
 // byte once, so HBM bounds them; a thread takes 16 consecutive values of a row (one NVFP4 block, half
 // an MXFP4 block, whose two halves are neighbouring lanes), which makes 8 bytes of codes.
 #include "fp4.cuh"
+#include "ptx.cuh"
 
 namespace qg {
 namespace {
@@ -116,6 +117,8 @@ __device__ __forceinline__ const uint8_t* source_row(const QuantArgs& a, int m) 
 // MXFP4: every block is by itself. Block: 32 units (512 values) x 8 rows.
 template <int DT>
 __global__ void __launch_bounds__(256) mx_quant_kernel(const QuantArgs a) {
+    ptx::grid_release();
+    ptx::grid_wait();
     const int u = blockIdx.y * 32 + threadIdx.x, m = blockIdx.x * 8 + threadIdx.y;
     if (m >= a.rows_out) return;               // whole warps: a warp is 32 units of one row
     const bool in = m < a.M && u < a.K / kUnit;
@@ -149,6 +152,8 @@ __global__ void __launch_bounds__(kNvThreads) nv_quant_kernel(const QuantArgs a)
     __shared__ uint32_t s_top[kNvThreads / 32];
     const int units = a.K / kUnit, step = blockDim.x, t = threadIdx.x;      // threads of a row; this one
     const int m = blockIdx.x * blockDim.y + threadIdx.y;
+    ptx::grid_release();
+    ptx::grid_wait();
     const uint8_t* row = source_row(a, m);
     Raw<DT> keep[kKeep];
     uint32_t top = 0;
@@ -212,6 +217,8 @@ struct DequantArgs {
 };
 template <int FMT, int DT>
 __global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantArgs a) {
+    ptx::grid_release();
+    ptx::grid_wait();
     const int units = a.K / kUnit;
     const int u = blockIdx.y * 32 + threadIdx.x, m = blockIdx.x * 8 + threadIdx.y;
     if (m >= a.M || u >= units) return;
@@ -325,24 +332,22 @@ template <int DT>
 cudaError_t quant_dt(const QuantArgs& a, int fmt, cudaStream_t s) {
     if (fmt == GF_MXFP4) {
         const dim3 grid((a.rows_out + 7) / 8, (a.units_out + 31) / 32);
-        mx_quant_kernel<DT><<<grid, dim3(32, 8), 0, s>>>(a);
+        return launch_behind(mx_quant_kernel<DT>, grid, dim3(32, 8), 0, 1, s, a);
     } else {
         const int warps = (a.K / kUnit + kKeep * 32 - 1) / (kKeep * 32);      // of a row
         const int row = 32 * (warps < kNvThreads / 32 ? warps : kNvThreads / 32), rows = kNvThreads / row;
-        nv_quant_kernel<DT><<<(a.rows_out + rows - 1) / rows, dim3(row, rows), 0, s>>>(a);
+        return launch_behind(nv_quant_kernel<DT>, (a.rows_out + rows - 1) / rows, dim3(row, rows), 0, 1, s, a);
     }
-    return cudaGetLastError();
 }
 
 template <int FMT>
 cudaError_t dequant_fmt(const DequantArgs& a, int dt, cudaStream_t s) {
     const dim3 grid((a.M + 7) / 8, (a.K / kUnit + 31) / 32), block(32, 8);
     switch (dt) {
-        case DT_F32: fp4_dequant_kernel<FMT, DT_F32><<<grid, block, 0, s>>>(a); break;
-        case DT_F16: fp4_dequant_kernel<FMT, DT_F16><<<grid, block, 0, s>>>(a); break;
-        default: fp4_dequant_kernel<FMT, DT_BF16><<<grid, block, 0, s>>>(a); break;
+        case DT_F32: return launch_behind(fp4_dequant_kernel<FMT, DT_F32>, grid, block, 0, 1, s, a);
+        case DT_F16: return launch_behind(fp4_dequant_kernel<FMT, DT_F16>, grid, block, 0, 1, s, a);
+        default: return launch_behind(fp4_dequant_kernel<FMT, DT_BF16>, grid, block, 0, 1, s, a);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

@@ -576,6 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
     }
+    ptx::grid_release();
+    ptx::grid_wait();      // the earlier kernels' results (offsets, operands) are there, and C may be written
     if (p.offsets && warp == 2) {
         // group starts and the tiles before each group
         int carry = 0;
@@ -1019,18 +1021,7 @@ cudaError_t launch(const GroupGemmArgs& a, int fmt, int split, long long tiles, 
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kSmem);
     if (e != cudaSuccess) return e;
     const long long most = kTargetSms / split;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * split));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = P::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)split;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = MODE == SOLO ? 0 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, maps, p);
+    return launch_behind(kern, dim3((unsigned)((tiles < most ? tiles : most) * split)), dim3(kThreads), P::kSmem, (unsigned)split, s, maps, p);
 }
 
 // Tile height and cluster size. A call's time beyond its launch is about

@@ -142,6 +142,26 @@ inline int w4a8_exact_splits(int K) { return K <= kW4A8ExactK ? 1 : (K + kW4A8Ch
 cudaError_t launch_w4a8_rescale(int M, int N, const int32_t* acc, const float* as, const int32_t* rowsum,
                                 const float* T, const Epilogue& ep, void* C, int c_dtype, cudaStream_t s);
 
+// Launches a kernel that may come up behind the one before it in the stream (it calls ptx::grid_wait
+// before it touches memory); cluster: blocks of a thread-block cluster.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, unsigned cluster, cudaStream_t s, A&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ---------------------------------------------------------------- 4-bit floating point, experts
 size_t fp4_scales_bytes(int rows, int K, int fmt, int layout);
 cudaError_t launch_fp4_quant(int M, int K, const void* X, int x_dtype, long long ldx, int x_rows, const int32_t* rows,

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace qg {
 namespace {
@@ -231,6 +232,8 @@ template <int DT, int EL>
 __global__ void __launch_bounds__(kRouteThreads) route_small_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
     __shared__ int16_t held[kHeldPairs];
+    ptx::grid_release();
+    ptx::grid_wait();
     int32_t *counts = sm, *first = sm + a.E, *start = first + a.E + 1;
     choose_block<DT, EL>(a, 0, a.T, counts, held);
     prefix(counts, first, a.E);
@@ -243,6 +246,8 @@ template <int DT, int EL>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
     __shared__ int16_t held[kHeldPairs];
+    // (not released early: the second launch's blocks, waiting beside these, made 1024 tokens 8.5 -> 11 us)
+    ptx::grid_wait();
     const int t0 = min(blockIdx.x * a.per_block, a.T), t1 = min(t0 + a.per_block, a.T);
     choose_block<DT, EL>(a, t0, t1, sm, held);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(size_t)blockIdx.x * a.E + e] = sm[e];
@@ -252,7 +257,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
     int32_t *total = sm, *before = sm + a.E, *first = before + a.E;
-    asm volatile("griddepcontrol.wait;" ::: "memory");      // the choices are written
+    ptx::grid_release();
+    ptx::grid_wait();
     for (int e = threadIdx.x; e < 2 * a.E; e += blockDim.x) sm[e] = 0;
     __syncthreads();
     // the pairs per expert in all blocks, and in the blocks before this one
@@ -290,29 +296,16 @@ cudaError_t route_el(RouteArgs a, cudaStream_t s) {
     const size_t sort = (size_t)kSortWarps * a.E * sizeof(int32_t);
     if (!route_needs_workspace(a.T)) {
         const int threads = 32 * (a.T > kSortWarps ? a.T : kSortWarps);     // a warp per token
-        route_small_kernel<DT, EL><<<1, threads, (2 * a.E + 1) * sizeof(int32_t) + sort, s>>>(a);
-        return cudaGetLastError();
+        return launch_behind(route_small_kernel<DT, EL>, 1, threads, (2 * a.E + 1) * sizeof(int32_t) + sort, 1, s, a);
     }
     // blocks of at least 8 tokens, a warp per token up to 32 of them
     const int want = (a.T + 7) / 8;
     const int blocks = want < kRouteBlocks ? want : kRouteBlocks;
     a.per_block = (a.T + blocks - 1) / blocks;
     const int warps = a.per_block < kSortWarps ? kSortWarps : (a.per_block < kRouteThreads / 32 ? a.per_block : kRouteThreads / 32);
-    route_choose_kernel<DT, EL><<<blocks, 32 * warps, a.E * sizeof(int32_t) + sort, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // the second launch may come up while the first ends; it waits for it before it reads anything
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kRouteThreads);
-    cfg.dynamicSmemBytes = (3 * a.E + 1) * sizeof(int32_t);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, route_place_kernel, a);
+    cudaError_t e = launch_behind(route_choose_kernel<DT, EL>, blocks, 32 * warps, a.E * sizeof(int32_t) + sort, 1, s, a);
+    if (e == cudaSuccess) e = launch_behind(route_place_kernel, blocks, kRouteThreads, (3 * a.E + 1) * sizeof(int32_t), 1, s, a);
+    return e;
 }
 
 template <int DT>
@@ -392,6 +385,8 @@ __device__ __forceinline__ void store_vec(void* p, size_t i, const float* x) {
 // block (64, 4): 64 runs of V columns of 4 tokens
 template <int DT, int ODT, int V>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
+    ptx::grid_release();
+    ptx::grid_wait();
     const int t = blockIdx.x * 4 + threadIdx.y;
     const int n = (blockIdx.y * 64 + threadIdx.x) * V;
     if (t >= a.T || n >= a.N) return;
@@ -427,14 +422,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
 
 template <int DT, int ODT>
 cudaError_t combine_v(const CombineArgs& a, cudaStream_t s) {
-    if (a.N % 8 == 0) {
-        const dim3 grid((a.T + 3) / 4, (a.N / 8 + 63) / 64);
-        combine_kernel<DT, ODT, 8><<<grid, dim3(64, 4), 0, s>>>(a);
-    } else {
-        const dim3 grid((a.T + 3) / 4, (a.N + 63) / 64);
-        combine_kernel<DT, ODT, 1><<<grid, dim3(64, 4), 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    const int columns = a.N % 8 == 0 ? a.N / 8 : a.N;
+    const dim3 grid((a.T + 3) / 4, (columns + 63) / 64), block(64, 4);
+    return a.N % 8 == 0 ? launch_behind(combine_kernel<DT, ODT, 8>, grid, block, 0, 1, s, a)
+                        : launch_behind(combine_kernel<DT, ODT, 1>, grid, block, 0, 1, s, a);
 }
 template <int DT>
 cudaError_t combine_dt(const CombineArgs& a, int out_dtype, cudaStream_t s) {
