@@ -4,7 +4,7 @@
 #include <stdio.h>
 
 #include "../../include/qgemm.h"
-#include "internal.h"
+#include "experts.h"
 
 namespace {
 

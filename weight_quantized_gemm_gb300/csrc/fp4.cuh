@@ -12,7 +12,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "internal.h"
+#include "experts.h"
 
 namespace qg {
 namespace fp4 {

@@ -3,8 +3,8 @@
 // Formulas and formats: fp4.cuh and include/qgemm.h. All three kernels move each input and output
 // byte once, so HBM bounds them; a thread takes 16 consecutive values of a row (one NVFP4 block, half
 // an MXFP4 block, whose two halves are neighbouring lanes), which makes 8 bytes of codes.
+#include "experts.cuh"
 #include "fp4.cuh"
-#include "ptx.cuh"
 
 namespace qg {
 namespace {
@@ -117,8 +117,8 @@ __device__ __forceinline__ const uint8_t* source_row(const QuantArgs& a, int m) 
 // MXFP4: every block is by itself. Block: 32 units (512 values) x 8 rows.
 template <int DT>
 __global__ void __launch_bounds__(256) mx_quant_kernel(const QuantArgs a) {
-    ptx::grid_release();
-    ptx::grid_wait();
+    grid_release();
+    grid_wait();
     const int u = blockIdx.y * 32 + threadIdx.x, m = blockIdx.x * 8 + threadIdx.y;
     if (m >= a.rows_out) return;               // whole warps: a warp is 32 units of one row
     const bool in = m < a.M && u < a.K / kUnit;
@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kNvThreads) nv_quant_kernel(const QuantArgs a)
     __shared__ uint32_t s_top[kNvThreads / 32];
     const int units = a.K / kUnit, step = blockDim.x, t = threadIdx.x;      // threads of a row; this one
     const int m = blockIdx.x * blockDim.y + threadIdx.y;
-    ptx::grid_release();
-    ptx::grid_wait();
+    grid_release();
+    grid_wait();
     const uint8_t* row = source_row(a, m);
     Raw<DT> keep[kKeep];
     uint32_t top = 0;
@@ -217,8 +217,8 @@ struct DequantArgs {
 };
 template <int FMT, int DT>
 __global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantArgs a) {
-    ptx::grid_release();
-    ptx::grid_wait();
+    grid_release();
+    grid_wait();
     const int units = a.K / kUnit;
     const int u = blockIdx.y * 32 + threadIdx.x, m = blockIdx.x * 8 + threadIdx.y;
     if (m >= a.M || u >= units) return;

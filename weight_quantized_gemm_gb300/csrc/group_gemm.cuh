@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "epilogue.cuh"
+#include "experts.cuh"
 #include "fp4.cuh"
 #include "ptx.cuh"
 
@@ -576,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
     }
-    ptx::grid_release();
-    ptx::grid_wait();      // the earlier kernels' results (offsets, operands) are there, and C may be written
+    grid_release();
+    grid_wait();      // the earlier kernels' results (offsets, operands) are there, and C may be written
     if (p.offsets && warp == 2) {
         // group starts and the tiles before each group
         int carry = 0;

@@ -10,17 +10,12 @@ namespace qg {
 
 enum Fmt { FMT_FLOAT = 0, FMT_INT4 = 1, FMT_INT8 = 2 };
 enum Dt { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2 };
-// Operand formats of the 4-bit floating-point and grouped products, and the layouts of their block
-// scales (the C ABI's QGEMM_FMT_* and QGEMM_SCALES_* values).
-enum GroupFmt { GF_F16 = 1, GF_BF16 = 2, GF_MXFP4 = 3, GF_NVFP4 = 4 };
-enum ScaleLayout { SC_ROWS = 0, SC_TILED = 1 };
 
 inline size_t dt_size(int dt) { return dt == DT_F32 ? 4 : 2; }
 
 // Output epilogue (epilogue.cuh): C = act(acc + bias) + residual, applied in float32 before the
 // one rounding to C's type. The activation codes are the C ABI's QGEMM_ACT_* values.
-// ACT_SWIGLU (channel pairs to one output) is the grouped and 4-bit products' alone.
-enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU_TANH = 3, ACT_SWIGLU = 4 };
+enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU_TANH = 3 };
 struct Epilogue {
     const float* bias = nullptr;        // [N] float32, or none
     const void* residual = nullptr;     // [M][N] in C's type, or none (may be C itself)
@@ -142,74 +137,12 @@ inline int w4a8_exact_splits(int K) { return K <= kW4A8ExactK ? 1 : (K + kW4A8Ch
 cudaError_t launch_w4a8_rescale(int M, int N, const int32_t* acc, const float* as, const int32_t* rowsum,
                                 const float* T, const Epilogue& ep, void* C, int c_dtype, cudaStream_t s);
 
-// Launches a kernel that may come up behind the one before it in the stream (it calls ptx::grid_wait
-// before it touches memory); cluster: blocks of a thread-block cluster.
-template <class... P, class... A>
-cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, unsigned cluster, cudaStream_t s, A&&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-}
-
-// ---------------------------------------------------------------- 4-bit floating point, experts
-size_t fp4_scales_bytes(int rows, int K, int fmt, int layout);
-cudaError_t launch_fp4_quant(int M, int K, const void* X, int x_dtype, long long ldx, int x_rows, const int32_t* rows,
-                             int fmt, int layout, void* codes, void* scales, float* row_scale, cudaStream_t s);
-cudaError_t launch_fp4_dequant(int M, int K, int fmt, int layout, const void* codes, const void* scales,
-                               const float* row_scale, void* Y, int y_dtype, cudaStream_t s);
-cudaError_t launch_fp4_pack(const float* W, int K, int N, int fmt, void* codes, void* scales, float* row_scale,
-                            cudaStream_t s);
-struct GroupGemmArgs {
-    int M, E, K, N;             // M rows in all; E experts (1 for a dense product)
-    const int32_t* offsets;     // [E + 1] first row of each expert, or none: all rows are expert 0's
-    const void* A;
-    const void* As;             // block scales, ROWS layout (4-bit formats)
-    const float* a_scale;       // [M] or none
-    const void* B;              // [E][N][K]
-    const void* Bs;             // [E] x TILED layout
-    const float* b_scale;       // [E][N] or none
-    const float* bias;          // [E][N] or none
-    int act;
-    const void* residual;       // C's type and shape, or none
-    void* C;
-    int c_dtype;
-};
-cudaError_t launch_group_gemm_half(const GroupGemmArgs& a, int fmt, cudaStream_t s);
-cudaError_t launch_group_gemm_mxfp4(const GroupGemmArgs& a, int fmt, cudaStream_t s);
-cudaError_t launch_group_gemm_nvfp4(const GroupGemmArgs& a, int fmt, cudaStream_t s);
-inline cudaError_t launch_group_gemm(const GroupGemmArgs& a, int fmt, cudaStream_t s) {
-    return fmt == GF_MXFP4 ? launch_group_gemm_mxfp4(a, fmt, s)
-                           : (fmt == GF_NVFP4 ? launch_group_gemm_nvfp4(a, fmt, s) : launch_group_gemm_half(a, fmt, s));
-}
-// The router's launches: up to kRouteSmallTokens tokens in one thread block, else kRouteBlocks blocks
-// at most, with a histogram of E counts each in the workspace.
-constexpr int kRouteSmallTokens = 32;
-constexpr int kRouteBlocks = kTargetSms;
-inline bool route_needs_workspace(int T) { return T > kRouteSmallTokens; }
-cudaError_t launch_moe_route(int T, int E, int k, const void* logits, int dtype, long long ld, int renorm, int32_t* expert,
-                             float* weight, int32_t* slot, int32_t* row, int32_t* offsets, void* workspace, cudaStream_t s);
-cudaError_t launch_moe_combine(int T, int k, int N, int R, const void* Y, int y_dtype, const int32_t* slot,
-                               const float* weight, const void* residual, void* out, int out_dtype, cudaStream_t s);
-
 // library options (qgemm_set_option)
 int option_overlap();
 long long option_wait_ns();   // bound of each pipeline wait in the TMA-fed kernels
 int option_stall();           // diagnostic stall of the next launches (QGEMM_OPT_DEBUG_STALL)
 // Records `detail` as the thread's last error and returns `code` (the C ABI's error path).
 int api_fail(int code, const char* detail);
-// Counts a compute call towards QGEMM_OPT_FAULT_INJECT; true for the call that is to fail.
-bool api_inject_fault();
 // Bp bytes of a shape (0 if the shape is invalid) and, in *table_bytes, its T bytes (0 in FLOAT).
 size_t api_packed_bytes(int K, int N, int mode, int block, int w_dtype, size_t* table_bytes);
 

@@ -4,8 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "experts.cuh"
+#include "experts.h"
 
 namespace qg {
 namespace {
@@ -232,8 +232,8 @@ template <int DT, int EL>
 __global__ void __launch_bounds__(kRouteThreads) route_small_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
     __shared__ int16_t held[kHeldPairs];
-    ptx::grid_release();
-    ptx::grid_wait();
+    grid_release();
+    grid_wait();
     int32_t *counts = sm, *first = sm + a.E, *start = first + a.E + 1;
     choose_block<DT, EL>(a, 0, a.T, counts, held);
     prefix(counts, first, a.E);
@@ -246,8 +246,6 @@ template <int DT, int EL>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
     __shared__ int16_t held[kHeldPairs];
-    // (not released early: the second launch's blocks, waiting beside these, made 1024 tokens 8.5 -> 11 us)
-    ptx::grid_wait();
     const int t0 = min(blockIdx.x * a.per_block, a.T), t1 = min(t0 + a.per_block, a.T);
     choose_block<DT, EL>(a, t0, t1, sm, held);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.hist[(size_t)blockIdx.x * a.E + e] = sm[e];
@@ -257,8 +255,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
     int32_t *total = sm, *before = sm + a.E, *first = before + a.E;
-    ptx::grid_release();
-    ptx::grid_wait();
+    grid_wait();
     for (int e = threadIdx.x; e < 2 * a.E; e += blockDim.x) sm[e] = 0;
     __syncthreads();
     // the pairs per expert in all blocks, and in the blocks before this one
@@ -303,7 +300,10 @@ cudaError_t route_el(RouteArgs a, cudaStream_t s) {
     const int blocks = want < kRouteBlocks ? want : kRouteBlocks;
     a.per_block = (a.T + blocks - 1) / blocks;
     const int warps = a.per_block < kSortWarps ? kSortWarps : (a.per_block < kRouteThreads / 32 ? a.per_block : kRouteThreads / 32);
-    cudaError_t e = launch_behind(route_choose_kernel<DT, EL>, blocks, 32 * warps, a.E * sizeof(int32_t) + sort, 1, s, a);
+    // (the first launch neither comes up early nor lets the second: blocks that wait beside the ones that
+    // choose made 1024 tokens 8.5 -> 11 us)
+    route_choose_kernel<DT, EL><<<blocks, 32 * warps, a.E * sizeof(int32_t) + sort, s>>>(a);
+    cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) e = launch_behind(route_place_kernel, blocks, kRouteThreads, (3 * a.E + 1) * sizeof(int32_t), 1, s, a);
     return e;
 }
@@ -385,8 +385,8 @@ __device__ __forceinline__ void store_vec(void* p, size_t i, const float* x) {
 // block (64, 4): 64 runs of V columns of 4 tokens
 template <int DT, int ODT, int V>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
-    ptx::grid_release();
-    ptx::grid_wait();
+    grid_release();
+    grid_wait();
     const int t = blockIdx.x * 4 + threadIdx.y;
     const int n = (blockIdx.y * 64 + threadIdx.x) * V;
     if (t >= a.T || n >= a.N) return;

@@ -114,12 +114,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
-// Programmatic dependent launch: a kernel launched with the attribute may come up while the kernel
-// before it in the stream still runs, once every block of that one has released it. grid_wait then
-// waits until the earlier kernels are complete and their writes visible; nothing that they write, or
-// read and this kernel writes, is touched before it.
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/qgemm.h"
+#include "experts.h"
 #include "internal.h"
 
 namespace {
