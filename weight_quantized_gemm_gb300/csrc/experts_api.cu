@@ -37,7 +37,7 @@ int check_fp4(int rows, int K, int fmt, const char* name) {
     if (rows < 0 || K <= 0) return fail(QGEMM_ERR_ARG, "invalid sizes %s=%d K=%d", name, rows, K);
     if (K % 64 != 0) return fail(QGEMM_ERR_UNSUPPORTED, "K=%d is not a multiple of 64", K);
     if (rows > kMaxRows) return fail(QGEMM_ERR_UNSUPPORTED, "%s=%d exceeds %d rows", name, rows, kMaxRows);
-    if (K > 16 * 32 * 65535) return fail(QGEMM_ERR_UNSUPPORTED, "K=%d exceeds the launch limit", K);
+    if (K > 8 * 32 * 65535) return fail(QGEMM_ERR_UNSUPPORTED, "K=%d exceeds the launch limit", K);
     return QGEMM_OK;
 }
 

@@ -27,14 +27,15 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void to_float(float (&x)[kUnit]) const {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+    // values 8 h .. 8 h + 7
+    __device__ __forceinline__ void eight(int h, float (&x)[8]) const {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v) + h * (DT == DT_F32 ? 8 : 4);
         if constexpr (DT == DT_F32) {
 #pragma unroll
-            for (int i = 0; i < kUnit; ++i) x[i] = __uint_as_float(w[i]);
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < kUnit / 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 if constexpr (DT == DT_F16) {
                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(w + i));
                     x[2 * i] = f.x;
@@ -74,12 +75,13 @@ struct Raw {
 // on a tie or at least 2^-13 away from it (ties are 0.25 and more), so x * (mul / s), wrong by a few
 // 2^-23, is rounded to a multiple of 2^-16 by adding and subtracting 192, which puts it back on the
 // tie or keeps it off.
+// r = 1 / s (0 for s = 0); eight values at a time, which keeps the registers that a thread needs low.
 template <int DT>
-__device__ __forceinline__ uint2 nv_codes(const float (&x)[kUnit], float mul, float s) {
-    const float r = s > 0.f ? __fdiv_rn(1.f, s) : 0.f, rm = r * mul;
-    float q[kUnit];
+__device__ __forceinline__ uint32_t nv_codes8(const float (&x)[8], float mul, float s, float r) {
+    const float rm = r * mul;
+    float q[8];
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) {
+    for (int i = 0; i < 8; ++i) {
         if constexpr (DT == DT_F32) {
             const float y = x[i] * mul, q0 = y * r;
             q[i] = __fmaf_rn(__fmaf_rn(-q0, s, y), r, q0);
@@ -88,8 +90,9 @@ __device__ __forceinline__ uint2 nv_codes(const float (&x)[kUnit], float mul, fl
         }
         q[i] = copysignf(q[i], x[i]);
     }
-    return mul != 0.f ? make_uint2(pack8(q), pack8(q + 8)) : make_uint2(0, 0);
+    return mul != 0.f ? pack8(q) : 0u;
 }
+__device__ __forceinline__ float inverse(float s) { return s > 0.f ? __fdiv_rn(1.f, s) : 0.f; }
 
 struct QuantArgs {
     int M, K;
@@ -131,40 +134,46 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(const QuantArgs a) {
     float mul;
     const uint32_t byte = mx_scale(top, &mul);
     if (in) {
-        float x[kUnit];
-        raw.to_float(x);
+        uint32_t c[2];
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) x[i] *= mul;
-        reinterpret_cast<uint2*>(a.codes)[(size_t)m * (a.K / kUnit) + u] =
-            mul != 0.f ? make_uint2(pack8(x), pack8(x + 8)) : make_uint2(0, 0);
+        for (int h = 0; h < 2; ++h) {
+            float x[8];
+            raw.eight(h, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] *= mul;
+            c[h] = mul != 0.f ? pack8(x) : 0u;
+        }
+        reinterpret_cast<uint2*>(a.codes)[(size_t)m * (a.K / kUnit) + u] = make_uint2(c[0], c[1]);
     }
     if ((u & 1) == 0 && u < a.units_out) a.scales[scale_index(a, m, u >> 1)] = in ? (uint8_t)byte : (uint8_t)0;
 }
 
-// NVFP4: the row's largest value comes first, so each thread keeps its kKeep units of the row in
-// registers between the two steps (rows of up to 16384 values; the rest of longer ones is read
-// again). A row takes as few warps as that allows, and a thread block of kNvThreads as many rows as
-// fit: with one row a block, rows of 4096 had one load a thread in flight (17 us for 4096 rows
-// against 10).
-constexpr int kNvThreads = 256, kKeep = 4;
+// NVFP4: the row's largest value comes first, so each thread keeps kKeep units of the row in
+// registers between the two steps (rows of up to 16384 values, float32 8192; the rest of longer ones
+// is read again). A row takes as few warps as that allows, and a thread block of kNvThreads as many
+// rows as fit: with one row a block, rows of 4096 had one load a thread in flight (17 us for 4096 rows
+// against 11). Four blocks an SM: while one computes, the others load.
+constexpr int kNvThreads = 256;
 template <int DT>
-__global__ void __launch_bounds__(kNvThreads) nv_quant_kernel(const QuantArgs a) {
+constexpr int kKeep = DT == DT_F32 ? 2 : 4;
+template <int DT>
+__global__ void __launch_bounds__(kNvThreads, 4) nv_quant_kernel(const QuantArgs a) {
     __shared__ uint32_t s_top[kNvThreads / 32];
     const int units = a.K / kUnit, step = blockDim.x, t = threadIdx.x;      // threads of a row; this one
     const int m = blockIdx.x * blockDim.y + threadIdx.y;
     grid_release();
     grid_wait();
     const uint8_t* row = source_row(a, m);
-    Raw<DT> keep[kKeep];
+    Raw<DT> keep[kKeep<DT>];
     uint32_t top = 0;
     if (row) {
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i)
+        for (int i = 0; i < kKeep<DT>; ++i)
             if (t + i * step < units) keep[i].load(row, t + i * step);
             else keep[i].zero();
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) top = max(top, keep[i].top());
-        for (int u = t + kKeep * step; u < units; u += step) {
+        for (int i = 0; i < kKeep<DT>; ++i) top = max(top, keep[i].top());
+        for (int u = t + kKeep<DT> * step; u < units; u += step) {
             Raw<DT> raw;
             raw.load(row, u);
             top = max(top, raw.top());
@@ -182,17 +191,24 @@ __global__ void __launch_bounds__(kNvThreads) nv_quant_kernel(const QuantArgs a)
     const float g = nv_row_scale(top, &mul);
     if (t == 0 && m < a.M) a.row_scale[m] = g;
     auto emit = [&](const Raw<DT>& raw, int u) {
-        float x[kUnit], s;
-        raw.to_float(x);
+        float s;
         const uint32_t most = mul != 0.f ? __float_as_uint(__uint_as_float(raw.top()) * mul) : 0u;
         a.scales[scale_index(a, m, u)] = (uint8_t)nv_scale(most, &s);
-        reinterpret_cast<uint2*>(a.codes)[(size_t)m * units + u] = nv_codes<DT>(x, mul, s);
+        const float r = inverse(s);
+        uint32_t c[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float x[8];
+            raw.eight(h, x);
+            c[h] = nv_codes8<DT>(x, mul, s, r);
+        }
+        reinterpret_cast<uint2*>(a.codes)[(size_t)m * units + u] = make_uint2(c[0], c[1]);
     };
     if (row) {
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i)
+        for (int i = 0; i < kKeep<DT>; ++i)
             if (t + i * step < units) emit(keep[i], t + i * step);
-        for (int u = t + kKeep * step; u < units; u += step) {
+        for (int u = t + kKeep<DT> * step; u < units; u += step) {
             Raw<DT> raw;
             raw.load(row, u);
             emit(raw, u);
@@ -215,43 +231,48 @@ struct DequantArgs {
     const float* row_scale;
     void* Y;
 };
+// A thread writes 32 bytes: 16 values, or 8 of float32 (64 bytes a thread took half as long again).
+template <int DT>
+constexpr int kOut = DT == DT_F32 ? 8 : 16;
 template <int FMT, int DT>
 __global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantArgs a) {
+    constexpr int kN = kOut<DT>;
     grid_release();
     grid_wait();
-    const int units = a.K / kUnit;
+    const int units = a.K / kN;
     const int u = blockIdx.y * 32 + threadIdx.x, m = blockIdx.x * 8 + threadIdx.y;
     if (m >= a.M || u >= units) return;
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(a.codes) + (size_t)m * units + u);
-    const int j = FMT == GF_MXFP4 ? u >> 1 : u;
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes) + ((size_t)m * units + u) * (kN / 8);
+    const int j = u * kN / Format<FMT>::kBlock;
     const uint32_t byte = __ldg(a.scales + (a.layout == SC_ROWS ? (size_t)m * a.pitch + j : tiled_index(m, j, a.ktiles)));
     const float s = FMT == GF_MXFP4 ? mx_scale_value(byte) : nv_scale_value(byte);
     const float g = a.row_scale ? __ldg(a.row_scale + m) : 1.f;
-    float y[kUnit];
-    unpack8(c.x, y);
-    unpack8(c.y, y + 8);
-    uint32_t w[DT == DT_F32 ? 16 : 8];
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) y[i] = y[i] * s * g;
-    if constexpr (DT == DT_F32) {
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) w[i] = __float_as_uint(y[i]);
+    float y[kN];
+    if constexpr (kN == 16) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes));
+        unpack8(c.x, y);
+        unpack8(c.y, y + 8);
     } else {
+        unpack8(__ldg(codes), y);
+    }
+    uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < kUnit / 2; ++i) {
-            if constexpr (DT == DT_F16) {
-                const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            } else {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
+    for (int i = 0; i < kN; ++i) y[i] = y[i] * s * g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (DT == DT_F32) {
+            w[i] = __float_as_uint(y[i]);
+        } else if constexpr (DT == DT_F16) {
+            const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
-    constexpr int kVecs = Raw<DT>::kVecs;
-    uint4* out = static_cast<uint4*>(a.Y) + ((size_t)m * units + u) * kVecs;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    uint4* out = static_cast<uint4*>(a.Y) + ((size_t)m * units + u) * 2;
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // A float32 weight [K][N] to codes [N][K/2] with TILED scales: 32 channels x 64 of K at a time
@@ -314,7 +335,14 @@ __global__ void __launch_bounds__(128) fp4_pack_kernel(const PackArgs a) {
         } else {
             float s;
             byte = nv_scale(mul != 0.f ? __float_as_uint(__uint_as_float(top) * mul) : 0u, &s);
-            c = nv_codes<DT_F32>(x, mul, s);
+            const float r = inverse(s);
+            float lo[8], hi[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                lo[i] = x[i];
+                hi[i] = x[8 + i];
+            }
+            c = make_uint2(nv_codes8<DT_F32>(lo, mul, s, r), nv_codes8<DT_F32>(hi, mul, s, r));
             j = u;
         }
         if (n < a.N) reinterpret_cast<uint2*>(a.codes)[(size_t)n * units + u] = c;
@@ -334,7 +362,7 @@ cudaError_t quant_dt(const QuantArgs& a, int fmt, cudaStream_t s) {
         const dim3 grid((a.rows_out + 7) / 8, (a.units_out + 31) / 32);
         return launch_behind(mx_quant_kernel<DT>, grid, dim3(32, 8), 0, 1, s, a);
     } else {
-        const int warps = (a.K / kUnit + kKeep * 32 - 1) / (kKeep * 32);      // of a row
+        const int warps = (a.K / kUnit + kKeep<DT> * 32 - 1) / (kKeep<DT> * 32);      // of a row
         const int row = 32 * (warps < kNvThreads / 32 ? warps : kNvThreads / 32), rows = kNvThreads / row;
         return launch_behind(nv_quant_kernel<DT>, (a.rows_out + rows - 1) / rows, dim3(row, rows), 0, 1, s, a);
     }
@@ -342,7 +370,8 @@ cudaError_t quant_dt(const QuantArgs& a, int fmt, cudaStream_t s) {
 
 template <int FMT>
 cudaError_t dequant_fmt(const DequantArgs& a, int dt, cudaStream_t s) {
-    const dim3 grid((a.M + 7) / 8, (a.K / kUnit + 31) / 32), block(32, 8);
+    const int n = dt == DT_F32 ? kOut<DT_F32> : kOut<DT_BF16>;
+    const dim3 grid((a.M + 7) / 8, (a.K / n + 31) / 32), block(32, 8);
     switch (dt) {
         case DT_F32: return launch_behind(fp4_dequant_kernel<FMT, DT_F32>, grid, block, 0, 1, s, a);
         case DT_F16: return launch_behind(fp4_dequant_kernel<FMT, DT_F16>, grid, block, 0, 1, s, a);
