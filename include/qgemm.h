@@ -309,7 +309,8 @@ size_t qgemm_moe_route_workspace_bytes(int T, int E, int k);
  *     and Bp codes, As ROWS scales, Bs the experts' TILED scales one after another, each of
  *     qgemm_fp4_scales_bytes(N, K, fmt, QGEMM_SCALES_TILED) bytes).
  *   offsets: int32 [E + 1] on the device, nondecreasing (qgemm_moe_route's); a group may be empty, and rows
- *     outside [offsets[0], offsets[E]) are neither read nor written in C. Entries are held to [0, T].
+ *     outside [offsets[0], offsets[E]) are neither read nor written in C. Entries are held to [0, T] and to the
+ *     largest entry before them.
  *   a_scale [T], b_scale [E][N], bias [E][N]: float32 or NULL. act, C, c_dtype, K, N: as qgemm_fp4_run.
  * T is the rows that A and C hold; the host never reads the offsets. E <= QGEMM_MAX_EXPERTS. */
 int qgemm_grouped_run(int T, int E, int K, int N, int fmt, const int32_t* offsets, const void* A, const void* As,

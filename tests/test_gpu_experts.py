@@ -196,6 +196,62 @@ def test_grouped_weights_past_32_bits(fmt):
         check_out(C[rows], *ref.product(a64, b64, None, None, None, 0, None), 0)
 
 
+@pytest.mark.parametrize("T,N,K", [(70, 130, 1024), (20, 256, 4096), (300, 200, 512)])
+def test_grouped_offsets_that_go_back(T, N, K):
+    """Entries below an earlier one count as it: groups never overlap, also where blocks share tiles."""
+    off = [0, T // 2, 0, T, 3, T, 0, T - 1, T, -5, T + 9]
+    E = len(off) - 1
+    a, b = torch.randn(T, K, device=DEV).bfloat16(), torch.randn(E, N, K, device=DEV).bfloat16()
+    C = torch.full((T, N), 5.0, device=DEV)
+    qg.qgemm_grouped_run(T, E, K, N, 2, torch.tensor(off, dtype=torch.int32, device=DEV), a, None, None, b, None, None, None, 0, C, 0)
+    assert qg.qgemm_status() == 0
+    for rows, e in ((slice(0, T // 2), 0), (slice(T // 2, T), 2)):
+        check_out(C[rows], *ref.product(host(a[rows]), host(b[e]), None, None, None, 0, None), 0)
+
+
+@pytest.mark.parametrize("fmt", [2, 3, 4])
+def test_layer_inputs_of_the_call_before(fmt):
+    """Kernels come up behind the one before them: every call reads what that one wrote, on buffers
+    that change from call to call without a wait in between."""
+    T, K, N, E = 96, 1024, 512, 4
+    off = torch.tensor([0, 24, 48, 72, 96], dtype=torch.int32, device=DEV)
+    b = torch.randn(E, N, K, device=DEV) * 0.05
+    if fmt == 2:
+        Bt = [b.bfloat16(), None, None]
+    else:
+        Q = [gpu_quant(b[e], N, K, fmt, 1) for e in range(E)]
+        Bt = [torch.cat([q[i] for q in Q]) if Q[0][i] is not None else None for i in range(3)]
+    xs = [torch.randn(T, K, device=DEV).bfloat16() for _ in range(6)]
+    slot, one = torch.arange(T, dtype=torch.int32, device=DEV).view(T, 1), torch.ones(T, 1, device=DEV)
+
+    def step(x, a, C, out):
+        if fmt == 2:
+            qg.qgemm_moe_combine(T, 1, K, T, x, 2, slot, one, None, a[0], 2)
+        else:
+            qg.qgemm_fp4_quant(T, K, x, 2, K, T, None, fmt, 0, *a)
+        qg.qgemm_grouped_run(T, E, K, N, fmt, off, a[0], *(a[1:] if fmt != 2 else (None, None)), *Bt, None, 0, C, 2)
+        qg.qgemm_moe_combine(T, 1, N, T, C, 2, slot, one, None, out, 2)
+
+    def buffers():
+        a = [torch.empty(T, K, dtype=torch.bfloat16, device=DEV)] if fmt == 2 else list(gpu_quant(xs[0], T, K, fmt))
+        return a, torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+
+    want = []
+    for x in xs:
+        a, C = buffers()
+        out = torch.empty_like(C)
+        step(x, a, C, out)
+        torch.cuda.synchronize()
+        want.append(out)
+    a, C = buffers()
+    outs = [torch.empty_like(C) for _ in range(60)]
+    for i, out in enumerate(outs):                      # one set of buffers for all
+        step(xs[i % 6], a, C, out)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, want[i % 6]), i
+
+
 # ---------------------------------------------------------------- combination
 @pytest.mark.parametrize("T,k,N,ydt,odt,residual", [(1, 1, 1, 0, 0, False), (8, 4, 2560, 2, 2, True), (5, 3, 77, 1, 0, True),
                                                     (130, 8, 1024, 2, 1, False), (33, 6, 520, 0, 2, True), (9, 32, 130, 1, 1, False),

@@ -1,6 +1,11 @@
 // Device helpers shared by the 4-bit floating-point and mixture-of-experts kernels.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+
 namespace qg {
 
 // Programmatic dependent launch: a kernel launched with the attribute may come up while the kernel
@@ -9,5 +14,18 @@ namespace qg {
 // read and this kernel writes, is touched before it.
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// What an earlier kernel may have written after this one came up is read with ordinary loads: the
+// read-only path (__ldg) is for memory that nothing writes while the kernel lives.
+template <class T>
+__device__ __forceinline__ T load(const T* p) {
+    return *p;
+}
+template <int DT>
+__device__ __forceinline__ float load_as_float(const void* p, size_t i) {
+    if constexpr (DT == DT_F32) return load(static_cast<const float*>(p) + i);
+    else if constexpr (DT == DT_F16) return __half2float(load(static_cast<const __half*>(p) + i));
+    else return __bfloat162float(load(static_cast<const __nv_bfloat16*>(p) + i));
+}
 
 }  // namespace qg

@@ -21,7 +21,7 @@ struct Raw {
     __device__ __forceinline__ void load(const void* row, int u) {
         const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (size_t)u * kUnit * (DT == DT_F32 ? 4 : 2));
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) v[i] = __ldg(p + i);
+        for (int i = 0; i < kVecs; ++i) v[i] = qg::load(p + i);
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -113,7 +113,7 @@ __device__ __forceinline__ size_t scale_index(const QuantArgs& a, int m, int j) 
 // Row m's values (null: a row of zeros: past the end, or gathered from outside X).
 __device__ __forceinline__ const uint8_t* source_row(const QuantArgs& a, int m) {
     if (m >= a.M) return nullptr;
-    const int r = a.rows ? __ldg(a.rows + m) : m;
+    const int r = a.rows ? load(a.rows + m) : m;
     return r >= 0 && r < a.x_rows ? static_cast<const uint8_t*>(a.X) + (long long)r * a.ldx_bytes : nullptr;
 }
 
@@ -244,16 +244,16 @@ __global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantArgs a) {
     if (m >= a.M || u >= units) return;
     const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes) + ((size_t)m * units + u) * (kN / 8);
     const int j = u * kN / Format<FMT>::kBlock;
-    const uint32_t byte = __ldg(a.scales + (a.layout == SC_ROWS ? (size_t)m * a.pitch + j : tiled_index(m, j, a.ktiles)));
+    const uint32_t byte = load(a.scales + (a.layout == SC_ROWS ? (size_t)m * a.pitch + j : tiled_index(m, j, a.ktiles)));
     const float s = FMT == GF_MXFP4 ? mx_scale_value(byte) : nv_scale_value(byte);
-    const float g = a.row_scale ? __ldg(a.row_scale + m) : 1.f;
+    const float g = a.row_scale ? load(a.row_scale + m) : 1.f;
     float y[kN];
     if constexpr (kN == 16) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes));
+        const uint2 c = load(reinterpret_cast<const uint2*>(codes));
         unpack8(c.x, y);
         unpack8(c.y, y + 8);
     } else {
-        unpack8(__ldg(codes), y);
+        unpack8(load(codes), y);
     }
     uint32_t w[8];
 #pragma unroll

@@ -362,7 +362,7 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], 
         if (p.residual) {
 #pragma unroll
             for (int i = 0; i < kCount; ++i)
-                if (i < rows) y[i] += load_c<CDT>(p.residual, at + (size_t)i * p.cols);
+                if (i < rows) y[i] += load_as_float<CDT>(p.residual, at + (size_t)i * p.cols);
         }
         uint8_t* out = static_cast<uint8_t*>(p.C) + at * kEsz;
 #pragma unroll
@@ -403,7 +403,7 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], 
         uint32_t r[W];
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            r[i] = half + i < live ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.residual) + at + i * step)) : 0u;
+            r[i] = half + i < live ? load(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.residual) + at + i * step)) : 0u;
 #pragma unroll
         for (int i = 0; i < W; ++i, out += step) {
             float2 f;
@@ -422,17 +422,17 @@ __device__ __forceinline__ void store_chunk(const Params& p, float (&v)[2 * W], 
 }
 
 __device__ __forceinline__ float element(const void* p, size_t i, int dt) {
-    return dt == DT_F32 ? load_c<DT_F32>(p, i) : (dt == DT_F16 ? load_c<DT_F16>(p, i) : load_c<DT_BF16>(p, i));
+    return dt == DT_F32 ? load_as_float<DT_F32>(p, i) : (dt == DT_F16 ? load_as_float<DT_F16>(p, i) : load_as_float<DT_BF16>(p, i));
 }
 // Scales, bias and the rest of the epilogue for channels n .. n + 3 of expert e in C's row m (SPLIT).
 __device__ __forceinline__ void finish4(const Params& p, float (&y)[4], int e, size_t m, int n) {
     const size_t en = (size_t)e * p.N + n;
     const int live = min(4, p.N - n);
-    const float as = p.a_scale ? __ldg(p.a_scale + m) : 1.f;
+    const float as = p.a_scale ? load(p.a_scale + m) : 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float ws = p.b_scale && i < live ? __ldg(p.b_scale + en + i) : 1.f;
-        const float bias = p.bias && i < live ? __ldg(p.bias + en + i) : 0.f;
+        const float ws = p.b_scale && i < live ? load(p.b_scale + en + i) : 1.f;
+        const float bias = p.bias && i < live ? load(p.bias + en + i) : 0.f;
         y[i] = fmaf(y[i] * as, ws, bias);
     }
     const bool glu = p.act == ACT_SWIGLU;
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             x.e = a;
             t -= before[a];
             lo = start[a];
-            hi = max(start[a + 1], lo);
+            hi = start[a + 1];
             mt = (hi - lo + BN - 1) / BN;
         }
         x.n0 = t / mt * P::kTileCh + (kPair ? (int)rank * kCh : 0);      // this block's channels
@@ -580,13 +580,21 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
     grid_release();
     grid_wait();      // the earlier kernels' results (offsets, operands) are there, and C may be written
     if (p.offsets && warp == 2) {
-        // group starts and the tiles before each group
-        int carry = 0;
+        // Group starts and the tiles before each group. An entry is held to [0, M] and to the largest
+        // before it, so that groups never overlap and have no more tiles than the launch allowed for.
+        int carry = 0, reached = 0;
         for (int e0 = 0; e0 <= p.E; e0 += 32) {
             const int e = e0 + lane;
-            const int lo = e <= p.E ? min(max(__ldg(p.offsets + e), 0), p.M) : 0;
-            const int hi = e < p.E ? max(min(max(__ldg(p.offsets + e + 1), 0), p.M), lo) : lo;
-            const int tiles = (hi - lo + BN - 1) / BN * p.n_tiles;
+            int lo = max(min(max(e <= p.E ? load(p.offsets + e) : 0, 0), p.M), reached);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, lo, o);
+                if (lane >= o) lo = max(lo, y);
+            }
+            // the group's end: the next lane's start, or for the last lane the next entry
+            int hi = __shfl_down_sync(0xffffffffu, lo, 1);
+            if (lane == 31 && e < p.E) hi = max(min(max(load(p.offsets + e + 1), 0), p.M), lo);
+            const int tiles = e < p.E ? (hi - lo + BN - 1) / BN * p.n_tiles : 0;
             int sum = tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -598,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                 before[e] = carry + sum - tiles;
             }
             carry += __shfl_sync(0xffffffffu, sum, 31);
+            reached = __shfl_sync(0xffffffffu, lo, 31);
         }
     }
     tc_fence_before();
@@ -670,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                 if (tf >= total) return;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    v[j] = 32 * j < rows ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)(32 * j) * p.pitch) + qf) : make_uint4(0, 0, 0, 0);
+                    v[j] = 32 * j < rows ? load(reinterpret_cast<const uint4*>(src + (size_t)(32 * j) * p.pitch) + qf) : make_uint4(0, 0, 0, 0);
                 qf += kStep;
                 if (qf > last) {
                     qf = first;
@@ -895,8 +904,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             } else {
                 const int n = x.n0 + 32 * q + lane;
                 const size_t en = (size_t)x.e * p.N + min(n, p.N - 1);
-                const float ws = p.b_scale ? __ldg(p.b_scale + en) : 1.f;
-                const float bias = p.bias ? __ldg(p.bias + en) : 0.f;
+                const float ws = p.b_scale ? load(p.b_scale + en) : 1.f;
+                const float bias = p.bias ? load(p.bias + en) : 0.f;
                 constexpr int kWide = P::kWide, kMine = BN / (2 * kWide);     // chunks of a column half
 #pragma unroll 1
                 for (int j = 0; j < kMine; ++j) {
@@ -919,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
                     if (live <= 0) continue;
                     const int m = x.m0 + c0;
                     if (p.a_scale) {
-                        const float as = __ldg(p.a_scale + m + min(lane & (kWide - 1), live - 1));
+                        const float as = load(p.a_scale + m + min(lane & (kWide - 1), live - 1));
 #pragma unroll
                         for (int i = 0; i < kWide; ++i) v[i] *= __shfl_sync(0xffffffffu, as, i);
                     }
