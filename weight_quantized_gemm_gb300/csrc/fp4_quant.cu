@@ -3,6 +3,9 @@
 // Formulas and formats: fp4.cuh and include/qgemm.h. All three kernels move each input and output
 // byte once, so HBM bounds them; a thread takes 16 consecutive values of a row (one NVFP4 block, half
 // an MXFP4 block, whose two halves are neighbouring lanes), which makes 8 bytes of codes.
+// 16384 x 14336 in bf16: MXFP4 92 us (6.4 TB/s), NVFP4 115 us (5.2 TB/s: a row's codes wait for its
+// largest value, so loads and stores of a block alternate), back 93 us (6.5 TB/s); 4 rows 3 us, which
+// is the launch and one row's two steps.
 #include "experts.cuh"
 #include "fp4.cuh"
 

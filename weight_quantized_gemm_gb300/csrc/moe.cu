@@ -21,7 +21,9 @@ namespace {
 // order depends on nothing but the input. A few tokens run in one thread block and one launch (128
 // tokens of 128 experts there: 19 us against 8 in two launches); more run in two, where the second
 // launch's blocks each sum the first's histograms themselves (at most kRouteBlocks x E counts, from
-// L2) instead of waiting for a third launch that scans them.
+// L2) instead of waiting for a third launch that scans them. 8 tokens of 64 experts, top 8: 3.3 us (a
+// launch and one pass of the chain above); 16384 tokens of 128, top 8: 18 us, where reading the logits
+// takes 1.3.
 constexpr int kSortWarps = 8;         // warps that rank a block's pairs
 constexpr int kRouteThreads = 1024;
 constexpr int kHeldPairs = 3584;      // experts of a block's pairs held in shared memory (more are read back)
@@ -315,7 +317,8 @@ cudaError_t route_dt(const RouteArgs& a, cudaStream_t s) {
 // ---------------------------------------------------------------- combining
 // out[t] = sum_j weight[t][j] * Y[slot[t][j]] + residual[t], in float32, in the order of j, rounded
 // once. HBM bounds it (k rows in, one out, each byte once); a thread takes 8 columns of one token and
-// has up to four rows' loads in flight.
+// has up to four rows' loads in flight. 16384 tokens of 8 x 2560 in bf16: 111 us, 6.8 TB/s, the measured
+// copy rate; 8 tokens of 4 x 4096: 1.6 us.
 struct CombineArgs {
     int T, k, N, R;
     const void* Y;
