@@ -319,7 +319,7 @@ int qgemm_grouped_run(int T, int E, int K, int N, int fmt, const int32_t* offset
 
 /* Each token's weighted sum of its experts' rows: out[t] = sum_j weight[t][j] * Y[slot[t][j]] + residual[t], in
  * float32 in the order of j, rounded once to out_dtype. Y: [R][N] in y_dtype; a slot outside [0, R) adds
- * nothing. residual: [T][N] in out_dtype or NULL; it may be out itself. */
+ * nothing. residual: [T][N] in out_dtype or NULL; it may be out itself. T * k (T for k = 0) <= 2^30. */
 int qgemm_moe_combine(int T, int k, int N, int R, const void* Y, int y_dtype, const int32_t* slot, const float* weight,
                       const void* residual, void* out, int out_dtype, void* stream);
 

@@ -120,6 +120,11 @@ def test_combine_refuses(args, code):
     assert call("qgemm_moe_combine", COMBINE, args) == code
 
 
+@pytest.mark.parametrize("args", [dict(T=(1 << 30) + 1, k=1), dict(T=(1 << 31) - 1, k=0), dict(T=1, k=(1 << 31) - 1), dict(T=1 << 27, k=9)])
+def test_combine_refuses_too_many_pairs(args):
+    assert call("qgemm_moe_combine", COMBINE, args) == UNSUP
+
+
 def test_swiglu_stays_with_the_new_products():
     assert qg.load().qgemm_run_fused(1, 128, 64, 1, 64, FAKE, 2, FAKE, FAKE, None, 4, None, FAKE, 2, FAKE, 1 << 20, None) == ARG
 

@@ -185,6 +185,8 @@ int qgemm_moe_combine(int T, int k, int N, int R, const void* Y, int y_dtype, co
     if (T < 0 || k < 0 || N < 0 || R < 0) return fail(QGEMM_ERR_ARG, "invalid sizes T=%d k=%d N=%d R=%d", T, k, N, R);
     if (!valid_dtype(y_dtype) || !valid_dtype(out_dtype))
         return fail(QGEMM_ERR_ARG, "unknown dtype (y_dtype %d, out_dtype %d)", y_dtype, out_dtype);
+    if ((long long)T * (k > 0 ? k : 1) > kMaxRows)
+        return fail(QGEMM_ERR_UNSUPPORTED, "T * k = %lld exceeds 2^30 pairs", (long long)T * (k > 0 ? k : 1));
     if (T == 0 || N == 0) return QGEMM_OK;
     if (!out || (k > 0 && (!slot || !weight)) || (R > 0 && !Y)) return fail(QGEMM_ERR_ARG, "null Y, slot, weight or out");
     if (!all_aligned16(Y, slot, weight, residual, out)) return fail(QGEMM_ERR_ALIGN, "pointers must be 16-byte aligned");
