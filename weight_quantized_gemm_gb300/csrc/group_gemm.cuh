@@ -35,10 +35,12 @@
 //               6.3 TB/s; and for the smallest the launch, the first loads and the join: 1 x 4096 x 11008
 //               6.7 us (3.4 TB/s), 16 x 4096 x 4096 5.1 us;
 //   many rows   16 bits: the tensor cores (2048 x 4096 x 14336 122 us, 1970 TFLOPS). 4 bits: an MMA of a
-//               pair takes 97 cycles, six times the 16-bit rate, and then the tile's end shows: the
-//               accumulators' common columns are waited for, and the epilogue takes issue slots and L1
-//               bandwidth beside the MMAs. MXFP4 2048 x 4096 x 14336 41 us (5.9 PFLOPS; tensor pipe 58 %,
-//               HBM 16 %), SwiGLU over 32768 rows of 32 experts, 2560 x 5120, 161 us (5.3 PFLOPS).
+//               pair takes 97 cycles, six times the 16-bit rate, and a stage's four MMAs no longer cover what
+//               goes on beside them: 36 KB from L2 to each SM, the scale copies and the epilogue. Each of
+//               these left out makes a tenth to a seventh; tiles of 240 rows, whose accumulators share no
+//               columns, make nothing (44 us and 161 -> 167 below). MXFP4 2048 x 4096 x 14336 41 us (5.9
+//               PFLOPS; tensor pipe 58 %, HBM 16 %), SwiGLU over 32768 rows of 32 experts, 2560 x 5120,
+//               161 us (5.3 PFLOPS).
 //
 // Every wait is bounded (see ptx.cuh); after an abort the copies and MMAs in flight are waited for,
 // and a cluster's blocks leave together.
