@@ -37,7 +37,7 @@
 //   many rows   16 bits: the tensor cores (2048 x 4096 x 14336 122 us, 1970 TFLOPS). 4 bits: an MMA of a
 //               pair takes 97 cycles, six times the 16-bit rate, and a stage's four MMAs no longer cover what
 //               goes on beside them: 36 KB from L2 to each SM, the scale copies and the epilogue. Each of
-//               these left out makes a tenth to a seventh; tiles of 240 rows, whose accumulators share no
+//               these left out makes about a fifth; tiles of 240 rows, whose accumulators share no
 //               columns, make nothing (44 us and 161 -> 167 below). MXFP4 2048 x 4096 x 14336 41 us (5.9
 //               PFLOPS; tensor pipe 58 %, HBM 16 %), SwiGLU over 32768 rows of 32 experts, 2560 x 5120,
 //               161 us (5.3 PFLOPS).
