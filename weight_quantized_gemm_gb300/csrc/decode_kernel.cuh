@@ -416,11 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p) {
     const int nu = (int)blockIdx.x < groups ? (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
     const int n_step = (int)gridDim.x * 16;
 
-    // Let the next kernel on the stream launch (it only takes SMs as these blocks exit), start
-    // the weight stream, then wait for the previous kernel's results before touching A or C.
+    // Start the weight stream, then wait for the previous kernel's results before touching A or C,
+    // then let the next kernel on the stream launch (it only takes SMs as these blocks exit): a kernel
+    // that reads its weight before its own wait must find every kernel but its predecessor complete.
     // Both griddepcontrol instructions are no-ops unless the launch carried the programmatic
     // serialization attribute.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int issue_ui = 0;
     uint32_t issue_st = ring_s;
 #pragma unroll
@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(DecodeArgs p) {
         issue_st = (i + 1 == D) ? ring_s : issue_st + R::kStageBytes;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     const uint16_t* A = static_cast<const uint16_t*>(p.A);
     // B operand kept in registers (NT == 1): breg[j] for the warp's sub-block j; sreg[j] = the

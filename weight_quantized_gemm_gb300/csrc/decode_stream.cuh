@@ -188,10 +188,6 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     }
     __syncthreads();
     if (*abort_flag) return;
-    // Let the next kernel on the stream launch (it takes SMs only as these blocks exit). The
-    // weight stream does not depend on earlier kernels; A and C are touched after
-    // griddepcontrol.wait. Both are no-ops without the programmatic serialization attribute.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == kCWarps) {
         // ---------------- producer (lane 0): the remaining stages, each once its slot is free
@@ -220,7 +216,12 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
     }
 
     // ---------------- consumers
+    // The weight stream does not depend on the previous kernel; A and C are touched after
+    // griddepcontrol.wait. Only then may the next kernel on the stream launch (it takes SMs only as
+    // these blocks exit): it may read its weight before its own wait, and must find every kernel but
+    // this one complete. Both are no-ops without the programmatic serialization attribute.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint16_t* A = static_cast<const uint16_t*>(p.A);
     // the warp's sub-block jj = c * SPS + j (stage c of a unit): global index
     // (sl_begin + c * bz + warp) * SPS + j; B operand fragments and column sums in registers

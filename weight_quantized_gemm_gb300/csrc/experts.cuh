@@ -11,7 +11,9 @@ namespace qg {
 // Programmatic dependent launch: a kernel launched with the attribute may come up while the kernel
 // before it in the stream still runs, once every block of that one has released it. grid_wait then
 // waits until the earlier kernels are complete and their writes visible; nothing that they write, or
-// read and this kernel writes, is touched before it.
+// read and this kernel writes, is touched before it. A kernel releases the next one only after its own
+// wait: whatever comes up then knows every kernel but the one just before it to be complete, which the
+// decode kernels rely on when they read a weight before they wait (QGEMM_OPT_LAUNCH_OVERLAP).
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -123,8 +123,8 @@ __device__ __forceinline__ const uint8_t* source_row(const QuantArgs& a, int m) 
 // MXFP4: every block is by itself. Block: 32 units (512 values) x 8 rows.
 template <int DT>
 __global__ void __launch_bounds__(256) mx_quant_kernel(const QuantArgs a) {
-    grid_release();
     grid_wait();
+    grid_release();
     const int u = blockIdx.y * 32 + threadIdx.x, m = blockIdx.x * 8 + threadIdx.y;
     if (m >= a.rows_out) return;               // whole warps: a warp is 32 units of one row
     const bool in = m < a.M && u < a.K / kUnit;
@@ -164,8 +164,8 @@ __global__ void __launch_bounds__(kNvThreads, 4) nv_quant_kernel(const QuantArgs
     __shared__ uint32_t s_top[kNvThreads / 32];
     const int units = a.K / kUnit, step = blockDim.x, t = threadIdx.x;      // threads of a row; this one
     const int m = blockIdx.x * blockDim.y + threadIdx.y;
-    grid_release();
     grid_wait();
+    grid_release();
     const uint8_t* row = source_row(a, m);
     Raw<DT> keep[kKeep<DT>];
     uint32_t top = 0;
@@ -240,8 +240,8 @@ constexpr int kOut = DT == DT_F32 ? 8 : 16;
 template <int FMT, int DT>
 __global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantArgs a) {
     constexpr int kN = kOut<DT>;
-    grid_release();
     grid_wait();
+    grid_release();
     const int units = a.K / kN;
     const int u = blockIdx.y * 32 + threadIdx.x, m = blockIdx.x * 8 + threadIdx.y;
     if (m >= a.M || u >= units) return;

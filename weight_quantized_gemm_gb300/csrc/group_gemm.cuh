@@ -589,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1) group_gemm_kernel(const __grid_co
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
     }
-    grid_release();
     grid_wait();      // the earlier kernels' results (offsets, operands) are there, and C may be written
+    grid_release();
     if (p.offsets && warp == 2) {
         // Group starts and the tiles before each group. An entry is held to [0, M] and to the largest
         // before it, so that groups never overlap and have no more tiles than the launch allowed for.

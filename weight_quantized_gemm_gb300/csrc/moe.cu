@@ -228,8 +228,8 @@ template <int DT, int EL>
 __global__ void __launch_bounds__(kRouteThreads) route_small_kernel(const RouteArgs a) {
     extern __shared__ int32_t sm[];
     __shared__ int16_t held[kHeldPairs];
-    grid_release();
     grid_wait();
+    grid_release();
     int32_t *counts = sm, *first = sm + a.E, *start = first + a.E + 1;
     choose_block<DT, EL>(a, 0, a.T, counts, held);
     prefix(counts, first, a.E);
@@ -398,8 +398,8 @@ __device__ __forceinline__ void store_vec(void* p, size_t i, const float* x) {
 // block (64, 4): 64 runs of V columns of 4 tokens
 template <int DT, int ODT, int V>
 __global__ void __launch_bounds__(256, DT == DT_F32 ? 4 : 6) combine_kernel(const CombineArgs a) {
-    grid_release();
     grid_wait();
+    grid_release();
     const int t = blockIdx.x * 4 + threadIdx.y;
     const int n = (blockIdx.y * 64 + threadIdx.x) * V;
     if (t >= a.T || n >= a.N) return;
