@@ -331,10 +331,17 @@ __device__ __forceinline__ float silu(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return v * r;
 }
+// max(v, 0) that keeps a NaN: an operand's NaN scale marks its row or channel of C behind every
+// activation (fmaxf would make it 0).
+__device__ __forceinline__ float relu(float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+    return r;
+}
 template <int ACT, int W>
 __device__ __forceinline__ void act_all(float (&v)[W]) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = ACT == ACT_SILU ? silu(v[i]) : act_fixed<ACT>(v[i]);
+    for (int i = 0; i < W; ++i) v[i] = ACT == ACT_SILU ? silu(v[i]) : (ACT == ACT_RELU ? relu(v[i]) : act_fixed<ACT>(v[i]));
 }
 
 template <int CDT>
@@ -453,7 +460,7 @@ __device__ __forceinline__ void finish4(const Params& p, float (&y)[4], int e, s
         y[1] = act_fixed<ACT_SILU>(y[2]) * y[3];
     } else if (p.act != ACT_NONE) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = act_apply(p.act, y[i]);
+        for (int i = 0; i < 4; ++i) y[i] = p.act == ACT_RELU ? relu(y[i]) : act_apply(p.act, y[i]);
     }
     const int count = glu ? live >> 1 : live;
     const size_t at = m * p.cols + (glu ? n >> 1 : n);
