@@ -258,7 +258,8 @@ size_t qgemm_fp4_scales_bytes(int rows, int K, int fmt, int layout);
 int qgemm_fp4_quant(int M, int K, const void* X, int x_dtype, long long ldx, int x_rows, const int32_t* rows, int fmt,
                     int layout, void* codes, void* scales, float* row_scale, void* stream);
 
-/* The inverse: Y [M][K] in y_dtype = code * block scale * row scale (row_scale NULL: 1), rounded once. */
+/* The inverse: Y [M][K] = code * block scale * row scale (row_scale NULL: 1) in float32, rounded to y_dtype. The
+ * float32 product is rounded itself where a row scale is not a power of two (qgemm_fp4_quant's always are). */
 int qgemm_fp4_dequant(int M, int K, int fmt, int layout, const void* codes, const void* scales, const float* row_scale,
                       void* Y, int y_dtype, void* stream);
 

@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(kNvThreads, 4) nv_quant_kernel(const QuantArgs
     for (int u = t + (m < a.M ? units : 0); u < a.units_out; u += step) a.scales[scale_index(a, m, u)] = 0;
 }
 
-// The inverse: y = code * block scale * row scale, rounded once to y's type.
+// The inverse: y = code * block scale * row scale in float32, rounded to y's type. code * block scale is
+// exact, so float32 rounds once, and not at all where the row scale is a power of two (as nv_row_scale's).
 struct DequantArgs {
     int M, K;
     int layout, pitch, ktiles;
@@ -248,8 +249,15 @@ __global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantArgs a) {
     const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes) + ((size_t)m * units + u) * (kN / 8);
     const int j = u * kN / Format<FMT>::kBlock;
     const uint32_t byte = load(a.scales + (a.layout == SC_ROWS ? (size_t)m * a.pitch + j : tiled_index(m, j, a.ktiles)));
-    const float s = FMT == GF_MXFP4 ? mx_scale_value(byte) : nv_scale_value(byte);
-    const float g = a.row_scale ? load(a.row_scale + m) : 1.f;
+    float s = FMT == GF_MXFP4 ? mx_scale_value(byte) : nv_scale_value(byte), g = 1.f;
+    if (a.row_scale) {
+        g = load(a.row_scale + m);
+        // code * s must not overflow where g brings it back (both changes are exact)
+        if (FMT == GF_MXFP4 && fabsf(g) < 1.f) {
+            s *= 0.25f;
+            g *= 4.f;
+        }
+    }
     float y[kN];
     if constexpr (kN == 16) {
         const uint2 c = load(reinterpret_cast<const uint2*>(codes));
