@@ -277,7 +277,7 @@ int qgemm_fp4_pack(const float* W, int K, int N, int fmt, void* Bp, void* Bs, fl
  *   A: codes [M][K/2], As: scales (ROWS), a_scale: float32 [M] or NULL for 1 (NVFP4: the row scales);
  *   Bp: codes [N][K/2], Bs: scales (TILED), b_scale: float32 [N] or NULL for 1;
  *   bias: float32 [N] or NULL; act: QGEMM_ACT_* (SwiGLU: N even); residual: C's shape and type, or NULL;
- *   it may be C itself, but must not overlap C in any other way. K % 64 == 0; M and N are any.
+ *   it may be C itself, but must not overlap C in any other way. K % 64 == 0, K < 2^30; M and N up to 2^30.
  * All pointers 16-byte aligned. No workspace: results depend on the shape and the inputs alone. */
 int qgemm_fp4_run(int M, int K, int N, int fmt, const void* A, const void* As, const float* a_scale, const void* Bp,
                   const void* Bs, const float* b_scale, const float* bias, int act, const void* residual, void* C,

@@ -30,6 +30,7 @@ bool all_aligned16(P... p) {
 bool valid_dtype(int d) { return d == QGEMM_F32 || d == QGEMM_F16 || d == QGEMM_BF16; }
 bool is_fp4(int fmt) { return fmt == QGEMM_FMT_MXFP4 || fmt == QGEMM_FMT_NVFP4; }
 constexpr int kMaxRows = 1 << 30;      // of one call, so that rounding up to a tile stays an int
+constexpr int kMaxK = (1 << 30) - 64;  // of a product, so that a 16-bit row's bytes stay an int
 bool valid_layout(int l) { return l == QGEMM_SCALES_ROWS || l == QGEMM_SCALES_TILED; }
 
 int check_fp4(int rows, int K, int fmt, const char* name) {
@@ -50,6 +51,7 @@ int check_product(int M, int E, int K, int N, int fmt, const void* A, const void
     if (!valid_dtype(c_dtype)) return fail(QGEMM_ERR_ARG, "unknown c_dtype %d", c_dtype);
     if (act < QGEMM_ACT_NONE || act > QGEMM_ACT_SWIGLU) return fail(QGEMM_ERR_ARG, "unknown activation %d", act);
     if (K % 64 != 0) return fail(QGEMM_ERR_UNSUPPORTED, "K=%d is not a multiple of 64", K);
+    if (K > kMaxK) return fail(QGEMM_ERR_UNSUPPORTED, "K=%d exceeds %d", K, kMaxK);
     if (act == QGEMM_ACT_SWIGLU && N % 2 != 0)
         return fail(QGEMM_ERR_UNSUPPORTED, "SwiGLU pairs channels: N=%d is odd", N);
     if (M > kMaxRows || N > kMaxRows) return fail(QGEMM_ERR_UNSUPPORTED, "M=%d or N=%d exceeds %d", M, N, kMaxRows);
