@@ -245,7 +245,7 @@ size_t qgemm_w4a8_acc_workspace_bytes(int M, int K);
 #define QGEMM_SCALES_TILED 1
 
 /* Bytes of the codes and of the block scales of `rows` rows of K values (0 for invalid arguments;
- * K must be a multiple of 64). Both are multiples of 16 per row (ROWS) or per weight (TILED), so the
+ * K must be a multiple of 64, rows at most 2^30). Both are multiples of 16 per row (ROWS) or per weight (TILED), so the
  * weights of several experts can follow one another. */
 size_t qgemm_fp4_codes_bytes(int rows, int K);
 size_t qgemm_fp4_scales_bytes(int rows, int K, int fmt, int layout);

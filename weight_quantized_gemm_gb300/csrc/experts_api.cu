@@ -68,12 +68,12 @@ int check_product(int M, int E, int K, int N, int fmt, const void* A, const void
 extern "C" {
 
 size_t qgemm_fp4_codes_bytes(int rows, int K) {
-    if (rows < 0 || K <= 0 || K % 64 != 0) return 0;
+    if (rows < 0 || rows > kMaxRows || K <= 0 || K % 64 != 0) return 0;
     return (size_t)rows * K / 2;
 }
 
 size_t qgemm_fp4_scales_bytes(int rows, int K, int fmt, int layout) {
-    if (rows < 0 || K <= 0 || K % 64 != 0 || !is_fp4(fmt) || !valid_layout(layout)) return 0;
+    if (rows < 0 || rows > kMaxRows || K <= 0 || K % 64 != 0 || !is_fp4(fmt) || !valid_layout(layout)) return 0;
     return qg::fp4_scales_bytes(rows, K, fmt, layout);
 }
 
