@@ -44,3 +44,16 @@ def test_sizes_of_the_longest_rows(K):
         n = K // block
         assert qg.qgemm_fp4_scales_bytes(3, K, fmt, 0) == 3 * (-(-n // 16) * 16)
         assert qg.qgemm_fp4_scales_bytes(3, K, fmt, 1) == -(-n // 4) * 512
+
+
+@pytest.mark.parametrize("args", [dict(M=1 << 30, N=1 << 30), dict(M=1 << 30, N=1 << 24, act=0), dict(M=1, N=1 << 30, K=1 << 20)])
+def test_dense_refuses_tiles_past_counting(args):
+    assert call("qgemm_fp4_run", RUN, args) == UNSUP
+    assert "tiles" in qg.qgemm_last_error()
+
+
+@pytest.mark.parametrize("args", [dict(T=1 << 30, N=1 << 30, fmt=2), dict(T=4, E=1024, N=1 << 30, fmt=4), dict(T=1 << 30, E=1024, N=1 << 24),
+                                  dict(T=1, E=1024, N=1 << 20, K=1 << 14)])
+def test_grouped_refuses_tiles_past_counting(args):
+    assert call("qgemm_grouped_run", GROUPED, args) == UNSUP
+    assert "tiles" in qg.qgemm_last_error()

@@ -5,6 +5,7 @@
 
 #include "../../include/qgemm.h"
 #include "experts.h"
+#include "group_plan.h"
 
 namespace {
 
@@ -61,6 +62,11 @@ int check_product(int M, int E, int K, int N, int fmt, const void* A, const void
     if (!all_aligned16(A, As, a_scale, Bp, Bs, b_scale, bias, residual, C))
         return fail(QGEMM_ERR_ALIGN, "A, Bp, C, scales, bias and residual must be 16-byte aligned");
     return QGEMM_OK;
+}
+
+int check_tiles(const qg::GroupGemmArgs& a, int fmt) {
+    if (qg::gg::countable(a, fmt)) return QGEMM_OK;
+    return fail(QGEMM_ERR_UNSUPPORTED, "M=%d K=%d N=%d with %d weights make more tiles than can be counted", a.M, a.K, a.N, a.E);
 }
 
 }  // namespace
@@ -132,8 +138,10 @@ int qgemm_fp4_run(int M, int K, int N, int fmt, const void* A, const void* As, c
     if (!is_fp4(fmt)) return fail(QGEMM_ERR_ARG, "format %d is not a 4-bit format", fmt);
     const int rc = check_product(M, 1, K, N, fmt, A, As, a_scale, Bp, Bs, b_scale, bias, act, residual, C, c_dtype);
     if (rc != QGEMM_OK || M == 0 || N == 0) return rc;
-    if (qg::api_inject_fault()) return injected();
     const qg::GroupGemmArgs a{M, 1, K, N, nullptr, A, As, a_scale, Bp, Bs, b_scale, bias, act, residual, C, c_dtype};
+    const int tc = check_tiles(a, fmt);
+    if (tc != QGEMM_OK) return tc;
+    if (qg::api_inject_fault()) return injected();
     return done(qg::launch_group_gemm(a, fmt, static_cast<cudaStream_t>(stream)), "fp4_run launch");
 }
 
@@ -146,8 +154,10 @@ int qgemm_grouped_run(int T, int E, int K, int N, int fmt, const int32_t* offset
     if (T == 0 || N == 0 || E == 0) return QGEMM_OK;
     if (!offsets) return fail(QGEMM_ERR_ARG, "null offsets");
     if (!aligned16(offsets)) return fail(QGEMM_ERR_ALIGN, "offsets must be 16-byte aligned");
-    if (qg::api_inject_fault()) return injected();
     const qg::GroupGemmArgs a{T, E, K, N, offsets, A, As, a_scale, Bp, Bs, b_scale, bias, act, nullptr, C, c_dtype};
+    const int tc = check_tiles(a, fmt);
+    if (tc != QGEMM_OK) return tc;
+    if (qg::api_inject_fault()) return injected();
     return done(qg::launch_group_gemm(a, fmt, static_cast<cudaStream_t>(stream)), "grouped_run launch");
 }
 

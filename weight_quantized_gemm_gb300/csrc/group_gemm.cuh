@@ -51,6 +51,7 @@
 #include "epilogue.cuh"
 #include "experts.cuh"
 #include "fp4.cuh"
+#include "group_plan.h"
 #include "ptx.cuh"
 
 namespace qg {
@@ -60,8 +61,6 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4, kEpiWarps = 8, kEpiThreads = kEpiWarps * 32;
 constexpr int kScaleWarp = 2;
 constexpr int kRowBytes = 128;                     // K bytes of a row per stage
-constexpr int kCh = 128;                           // channels per tile
-constexpr int kMaxSplit = 8;
 constexpr int kMaxStages = 10;
 constexpr long long kDrainNs = 20000000;           // limit of a wait for copies in flight after an abort
 constexpr size_t kSmemMax = 232448;
@@ -1053,49 +1052,9 @@ cudaError_t launch(const GroupGemmArgs& a, int fmt, int split, long long tiles, 
     return launch_behind(kern, dim3((unsigned)((tiles < most ? tiles : most) * split)), dim3(kThreads), P::kSmem, (unsigned)split, s, maps, p);
 }
 
-// Tile height and cluster size. A call's time beyond its launch is about
-//   rounds * stages / split * (stage of this height) + (last tile's epilogue) + (joining the parts of K),
-// rounds = tiles * split / blocks at a time, with the constants below (nanoseconds, fitted to MXFP4 calls).
-// Small tiles fill the GPU and end sooner; large ones read the operands fewer times:
-//   4096 x 4096, us       M = 100   300    512    1024  |  N = 14336:  M = 64   256    512    1024
-//   32 rows                  7.4                        |                11.6
-//   128 rows                10.1   8.6    9.1    13.9   |                 9.6   14.1   18.8   32.6
-//   256 rows, two blocks     9.7  12.2   12.3    13.3   |                10.5   13.3   19.3   25.8
-// Joining pays for few tiles of long K: 128 x 9728 x 2560 runs 12 us with K in four, M = 100 of 4096 x
-// 4096 no faster than without. A cluster has one tile, so a split call's tiles must all fit at once.
-struct Choice {
-    int bn, split;
-    long long tiles;       // at least as many as the call has
-};
-inline Choice choose(const GroupGemmArgs& a, int stages) {
-    static const struct { int bn, channels, blocks; long long stage, last, join; } kHeights[3] = {
-        {32, kCh, 1, 200, 500, 1200}, {128, kCh, 1, 280, 1500, 2500}, {256, 2 * kCh, 2, 360, 4000, 0}};
-    const long long groups = a.offsets ? (a.M < a.E ? a.M : a.E) : 1;     // that can have rows
-    Choice best{};
-    long long least = -1;
-    for (const auto& h : kHeights) {
-        const long long n_tiles = (a.N + h.channels - 1) / h.channels;
-        // the dense product's row tiles, or the most that ragged groups make, and about as many as they do
-        const long long most = a.offsets ? a.M / h.bn + groups : (a.M + h.bn - 1) / h.bn;
-        const long long mean = a.offsets ? (a.M / h.bn + groups / 2 > groups ? a.M / h.bn + groups / 2 : groups) : most;
-        for (int split = 1; split <= (h.join ? kMaxSplit : 1); split *= 2) {
-            if (split > 1 && (most * n_tiles * split > kTargetSms || stages / split < 2)) break;
-            const long long at_once = kTargetSms / (split * h.blocks);
-            const long long rounds = (mean * n_tiles + at_once - 1) / at_once;
-            const long long t = rounds * ((stages + split - 1) / split) * h.stage + h.last + (split > 1 ? h.join : 0);
-            if (least < 0 || t < least) {
-                least = t;
-                best = {h.bn, split, most * n_tiles};
-            }
-        }
-    }
-    return best;
-}
-
 template <int F>
 cudaError_t launch_form(const GroupGemmArgs& a, int fmt, cudaStream_t s) {
-    const Choice c = choose(a, F == HALF ? a.K / 64 : (a.K + 255) / 256);
-    if (c.tiles > 0x7fffffffLL || (long long)a.E * ((a.N + kCh - 1) / kCh) * ((a.K + 63) / 64) > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const Choice c = choose(a, fmt);       // (the call's checks have refused more tiles than can be counted)
     if (c.bn == 32) return c.split > 1 ? launch<F, 32, SPLIT>(a, fmt, c.split, c.tiles, s) : launch<F, 32, SOLO>(a, fmt, 1, c.tiles, s);
     if (c.bn == 128) return c.split > 1 ? launch<F, 128, SPLIT>(a, fmt, c.split, c.tiles, s) : launch<F, 128, SOLO>(a, fmt, 1, c.tiles, s);
     return launch<F, 256, PAIR>(a, fmt, 2, c.tiles, s);
