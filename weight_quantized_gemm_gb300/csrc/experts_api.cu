@@ -161,6 +161,16 @@ int qgemm_grouped_run(int T, int E, int K, int N, int fmt, const int32_t* offset
     return done(qg::launch_group_gemm(a, fmt, static_cast<cudaStream_t>(stream)), "grouped_run launch");
 }
 
+// Not part of the ABI: how a product is cut (rows of a tile, blocks that share its K), so that tests can tell
+// which form of the kernel a shape takes.
+void qg_group_plan(int M, int E, int grouped, int K, int N, int fmt, int* rows, int* split) {
+    static const int32_t some = 0;
+    const qg::GroupGemmArgs a{M, E, K, N, grouped ? &some : nullptr};
+    const qg::gg::Choice c = qg::gg::choose(a, fmt);
+    *rows = c.bn;
+    *split = c.split;
+}
+
 size_t qgemm_moe_route_workspace_bytes(int T, int E, int k) {
     if (T <= 0 || E <= 0 || k <= 0 || k > E || E > QGEMM_MAX_EXPERTS || k > QGEMM_MAX_TOPK) return 0;
     return qg::route_needs_workspace(T) ? (size_t)qg::kRouteBlocks * E * sizeof(int32_t) : 0;
