@@ -108,6 +108,8 @@ def _ptr(x):
     """Device (or host) address of a tensor, an int address, or None."""
     if x is None:
         return None
+    if type(x) is int:
+        return x
     try:
         return x.data_ptr()
     except AttributeError:
