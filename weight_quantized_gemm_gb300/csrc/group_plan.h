@@ -50,8 +50,12 @@ inline Choice choose(const GroupGemmArgs& a, int fmt) {
 }
 
 // The kernel counts tiles, and the weights' scale tiles, in 32 bits (with room for a step past the last).
+// (No height makes more tiles than the lowest, so most calls need no plan here.)
 inline bool countable(const GroupGemmArgs& a, int fmt) {
-    return choose(a, fmt).tiles <= 1LL << 30 && (long long)a.E * ((a.N + kCh - 1) / kCh) * ((a.K + 63) / 64) <= 1LL << 30;
+    constexpr long long kMost = 1LL << 30;
+    const long long ch_tiles = (a.N + kCh - 1) / kCh;
+    if ((long long)a.E * ch_tiles * ((a.K + 63) / 64) > kMost) return false;
+    return ((long long)a.M / 32 + (a.offsets ? a.E : 1)) * ch_tiles <= kMost || choose(a, fmt).tiles <= kMost;
 }
 
 }  // namespace gg
