@@ -464,7 +464,10 @@ __device__ __forceinline__ void finish4(const Params& p, float (&y)[4], int e, s
         y[1] = act_fixed<ACT_SILU>(y[2]) * y[3];
     } else if (p.act != ACT_NONE) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = p.act == ACT_RELU ? relu(y[i]) : act_apply(p.act, y[i]);
+        for (int i = 0; i < 4; ++i) {
+            const float v = act_apply(p.act, y[i]);
+            y[i] = isnan(y[i]) ? y[i] : v;       // (kept behind ReLU, as everywhere)
+        }
     }
     const int count = glu ? live >> 1 : live;
     const size_t at = m * p.cols + (glu ? n >> 1 : n);
