@@ -236,7 +236,13 @@ size_t qgemm_w4a8_acc_workspace_bytes(int M, int K);
  *   QGEMM_SCALES_TILED (weights): tiles of 128 rows x 4 scales, 512 bytes each, [ceil(rows / 128)][ceil(K /
  *     block / 4)]; the four scales of row r of a tile lie at 16 (r % 32) + 4 (r / 32), the order in which
  *     the tensor cores take them.
- *   Bytes past the last row or scale are written as zeros. */
+ *   Bytes past the last row or scale are written as zeros.
+ * The kernels of these calls and of the mixture-of-experts calls below (packing, and the first launch of a
+ * routing of many tokens, apart) are always launched with a programmatic dependency on the kernel before
+ * them in the stream: they may come up while it finishes, and wait for it to complete before they read or
+ * write anything, so nothing is asked of the caller. QGEMM_OPT_LAUNCH_OVERLAP does not govern them. A
+ * kernel lets the next one come up only after its own wait.
+ * qgemm_save and qgemm_load know the four modes above, not these formats. */
 #define QGEMM_FMT_F16 1   /* 16-bit operands of the grouped product (same numbers as the types) */
 #define QGEMM_FMT_BF16 2
 #define QGEMM_FMT_MXFP4 3
@@ -386,7 +392,9 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
  * kernel is finishing, begins streaming Bp and T at once, and waits for the previous kernel
  * to complete before it reads A or writes C or the workspace. This hides the launch and
  * weight-fetch latency of back-to-back layer calls. CONTRACT while enabled: the kernel
- * launched immediately before qgemm_run on the same stream must not write Bp or T.
+ * launched immediately before qgemm_run on the same stream must not write Bp or T. (Those before
+ * that one may: every kernel of this library lets its successor start only once its own
+ * predecessor is complete. A caller's own kernel with programmatic launch has to do the same.)
  * The setting is process-wide. */
 #define QGEMM_OPT_LAUNCH_OVERLAP 1
 
@@ -405,10 +413,11 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
 #define QGEMM_OPT_SPLIT_K 3
 
 /* QGEMM_OPT_WAIT_LIMIT_US (default 1000000, range 1..1000000). The TMA-fed kernels (the decode
- * kernel for M <= 16 and the tensor-core kernel) bound every wait of their pipelines by this many
- * microseconds of the GPU's global timer: a wait that runs out sets the status word that
+ * kernel for M <= 16, the tensor-core kernel and that of the 4-bit and grouped products) bound every
+ * wait of their pipelines by this many microseconds of the GPU's global timer: a wait that runs out sets the status word that
  * qgemm_status reports as QGEMM_ERR_TIMEOUT, every role of the thread block leaves its loop, the
- * copies and MMAs already issued are waited for (always with the full one-second bound) and the
+ * copies and MMAs already issued are waited for (always with the full one-second bound; 20 ms for a
+ * stage's copies in the 4-bit and grouped products, whose barrier may never complete then) and the
  * tensor memory is released before the block exits; that call's outputs are then undefined. A
  * bound shorter than a normal wait makes healthy calls time out: the option exists to exercise
  * that recovery path, and production code keeps the default. Process-wide. */
@@ -424,9 +433,9 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
 /* QGEMM_OPT_FAULT_INJECT (default 0, or the value of the environment variable QGEMM_FAULT_INJECT
  * when the library loads). Host-side fault injection: when n > 0, the n-th compute call from now
  * (qgemm_pack, qgemm_run, qgemm_run_fused, qgemm_run_noalloc, qgemm_act_quant, qgemm_w4a8_acc, the
- * qgemm_fp4_*, qgemm_grouped_run and qgemm_moe_* calls) passes its argument checks and then returns QGEMM_ERR_CUDA with the detail "simulated launch
- * failure" instead of launching, as a failed launch would; the count then stays 0. No GPU fault is
- * involved. For testing callers' error handling. Process-wide. */
+ * qgemm_fp4_*, qgemm_grouped_run and qgemm_moe_* calls) passes its argument checks and then returns
+ * QGEMM_ERR_CUDA with the detail "simulated launch failure" instead of launching, as a failed launch
+ * would; the count then stays 0. No GPU fault is involved. For testing callers' error handling. Process-wide. */
 #define QGEMM_OPT_FAULT_INJECT 6
 
 /* Set an option; returns its previous value, or QGEMM_ERR_ARG for an unknown option or value. */

@@ -3,9 +3,10 @@
 // Formulas and formats: fp4.cuh and include/qgemm.h. All three kernels move each input and output
 // byte once, so HBM bounds them; a thread takes 16 consecutive values of a row (one NVFP4 block, half
 // an MXFP4 block, whose two halves are neighbouring lanes), which makes 8 bytes of codes.
-// 16384 x 14336 in bf16: MXFP4 92 us (6.4 TB/s), NVFP4 115 us (5.2 TB/s: a row's codes wait for its
-// largest value, so loads and stores of a block alternate), back 93 us (6.5 TB/s); 4 rows 3 us, which
-// is the launch and one row's two steps.
+// 16384 x 14336 in bf16: MXFP4 91 us (6.5 TB/s), NVFP4 115 us (5.2 TB/s: a row's codes wait for its
+// largest value, so loads and stores of a block alternate; four blocks an SM leave it 16 to 20 bytes of
+// spills a thread), back 92 us from NVFP4 (6.5 TB/s) and 96 from MXFP4 (6.2); 4 rows 1.5 us in MXFP4 and 3
+// in NVFP4, which is the launch and one row's two steps.
 #include "experts.cuh"
 #include "fp4.cuh"
 
@@ -289,7 +290,8 @@ __global__ void __launch_bounds__(256) fp4_dequant_kernel(const DequantArgs a) {
 // A float32 weight [K][N] to codes [N][K/2] with TILED scales: 32 channels x 64 of K at a time
 // through shared memory (reads along N, writes along K); 128 threads, four units a channel. One
 // thread block per 32 channels runs through K; NVFP4 runs through it twice, first for the channels'
-// largest |w|. Offline work, so it is kept simple.
+// largest |w|. Offline work, so it is kept simple: one pass over K by a block behind
+// two barriers per 64 values is a chain of load latencies (4096 x 14336: MXFP4 194 us, NVFP4 367).
 struct PackArgs {
     const float* W;
     int K, N, ktiles;

@@ -30,17 +30,20 @@
 // took 4 us for 64 rows) turn them in shared memory and send one bulk copy to each block, which for
 // a few rows takes 0.5 us longer. No workspace, no atomics, one launch. A cluster has one tile at most.
 //
-// What bounds it, and what it measured (bf16 output, calls in a graph):
-//   few rows    the weight's bytes from HBM, once: 64 rows of 32 experts, 2560 x 9728, MXFP4: 48 us,
-//               6.3 TB/s; and for the smallest the launch, the first loads and the join: 1 x 4096 x 11008
-//               6.7 us (3.4 TB/s), 16 x 4096 x 4096 5.1 us;
+// What bounds it, and what it measured (bf16 output, no bias or activation, calls in a graph):
+//   few rows    the weight's bytes from HBM, once: 64 rows of 32 experts, 2560 x 9728, MXFP4: 49 us,
+//               6.3 TB/s (NVFP4 50 us). With fewer tiles than SMs the SMs that work: 1 x 4096 x 11008 is 86
+//               blocks of 16 stages, 6.8 us (3.3 TB/s; NVFP4 7.3). For the smallest the launch, the first
+//               loads and the join: 16 x 4096 x 4096 5.1 us;
 //   many rows   16 bits: the tensor cores (2048 x 4096 x 14336 122 us, 1970 TFLOPS). 4 bits: an MMA of a
 //               pair takes 97 cycles, six times the 16-bit rate, and a stage's four MMAs no longer cover what
 //               goes on beside them: 36 KB from L2 to each SM, the scale copies and the epilogue. Each of
 //               these left out makes about a fifth; tiles of 240 rows, whose accumulators share no
-//               columns, make nothing (44 us and 161 -> 167 below). MXFP4 2048 x 4096 x 14336 41 us (5.9
-//               PFLOPS; tensor pipe 58 %, HBM 16 %), SwiGLU over 32768 rows of 32 experts, 2560 x 5120,
-//               161 us (5.3 PFLOPS).
+//               columns, make nothing (44 us and 161 -> 167 below). MXFP4 2048 x 4096 x 14336 41 us (5.8
+//               PFLOPS; tensor pipe 57 %, HBM 14 %; 42.8 with SiLU, 46 to 47 with SiLU and bias on inputs that
+//               change from call to call), SwiGLU over 32768 rows of 32 experts, 2560 x 5120, 160 us (5.4
+//               PFLOPS; 171 to 173 on changing inputs). NVFP4 has twice the scales to copy: 56 us and 207
+//               to 215.
 //
 // Every wait is bounded (see ptx.cuh); after an abort the copies and MMAs in flight are waited for,
 // and a cluster's blocks leave together.

@@ -14,16 +14,18 @@ namespace {
 // A warp per token: lane i holds the logits of E / 32 neighbouring experts as order-preserving integer
 // keys, and each of the k rounds takes the largest key by a warp reduction; of several lanes that
 // hold it the lowest, and in it the lowest expert, is the lowest expert of all. A lane's keys are put
-// in order first (up to 8 of them), so that taking one out of the warp is a shift: what bounds the
-// routing of many tokens is the number of instructions (600 a token while each round searched the
-// lane's keys). A stable counting sort of the pairs by expert follows: each pair's rank among the
+// in order first (up to 8 of them), so that taking one out of the warp is a shift and not another search
+// through the lane's keys. A stable counting sort of the pairs by expert follows: each pair's rank among the
 // block's pairs of its expert by warp matches, then the counts of the experts and blocks before, so the
 // order depends on nothing but the input. A few tokens run in one thread block and one launch (128
 // tokens of 128 experts there: 19 us against 8 in two launches); more run in two, where the second
 // launch's blocks each sum the first's histograms themselves (at most kRouteBlocks x E counts, from
-// L2) instead of waiting for a third launch that scans them. 8 tokens of 64 experts, top 8: 3.3 us (a
+// L2) instead of waiting for a third launch that scans them. 8 tokens of 64 experts, top 8: 3.5 us (a
 // launch and one pass of the chain above); 16384 tokens of 128, top 8: 18 us, where reading the logits
-// takes 1.3.
+// takes 1.3. What bounds those is latency. Profiled by themselves on a cold cache the launches take 15.9 and
+// 12.1 us. The first issues 470 warp instructions a token, 6 us if the issue slots were full; they are half
+// busy, and warps wait for the block's barriers, for the rounds' chain of reduction, ballot and shuffle, and
+// for their logits. The second fills 18 % of its issue slots and waits for the histograms.
 constexpr int kSortWarps = 8;         // warps that rank a block's pairs
 constexpr int kRouteThreads = 1024;
 constexpr int kHeldPairs = 3584;      // experts of a block's pairs held in shared memory (more are read back)
