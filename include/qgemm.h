@@ -330,6 +330,74 @@ int qgemm_grouped_run(int T, int E, int K, int N, int fmt, const int32_t* offset
 int qgemm_moe_combine(int T, int k, int N, int R, const void* Y, int y_dtype, const int32_t* slot, const float* weight,
                       const void* residual, void* out, int out_dtype, void* stream);
 
+/* ---------------------------------------------------------------- around the layer */
+
+/* What stands directly before, beside and behind the layers of a served model: the norms that make a layer's
+ * input, the low-rank adapters of the requests in a batch, and the log probabilities behind the last layer.
+ * Buffers are on the current device; as the calls above, these are launched with a programmatic dependency and
+ * need no workspace. Results depend on the shape and the inputs alone. */
+
+#define QGEMM_MAX_ADAPTERS 1024
+#define QGEMM_MAX_RANK 256
+
+/* The rows of a batch in order of their adapter (once a step; it serves the adapters of every layer).
+ *   adapter int32 [M]: each row's adapter; a row whose entry is outside [0, L) has none.
+ *   row int32 [M]: the rows in order of adapter, then row; -1 past the last one that has an adapter.
+ *   offsets int32 [L + 1]: adapter l's rows are row[offsets[l]] .. row[offsets[l + 1] - 1].
+ * M <= 2^30, 1 <= L <= QGEMM_MAX_ADAPTERS. */
+int qgemm_lora_group(int M, int L, const int32_t* adapter, int32_t* row, int32_t* offsets, void* stream);
+
+/* Low-rank adapters beside a shared projection, each row by its own: for every row m that `row` lists under
+ * adapter l (offsets[l] <= i < offsets[l + 1], m = row[i]),
+ *   Y[m][n] += scale[l] * sum_{r < rank[l]} B[l][n][r] * (sum_k A[l][r][k] * X[m][k])
+ * in float32 with one rounding to Y's type. Rows that are not listed keep their Y.
+ *   dtype: f16 or bf16, the type of X, A and B. X: [M][ldx], A: [L][R][K], B: [L][N][R].
+ *   rank int32 [L]: adapter l's rank, held to [0, R] (NULL: R); what A and B hold past it is not used.
+ *   scale float32 [L], or NULL for 1.
+ *   Y: [M][ldy] in y_dtype (f32, f16 or bf16), the projection's output, or N columns of a joined one: 16-byte
+ *     aligned, any ldy >= N (rows that start 16-byte aligned are faster). It must not overlap the inputs.
+ *   row [M], offsets [L + 1]: as qgemm_lora_group writes them. Entries of offsets are held to [0, M] and to the
+ *     largest before them; an entry of row outside [0, M) is skipped; a row may be listed once.
+ * K % 64 == 0, R % 8 == 0, 8 <= R <= QGEMM_MAX_RANK, 1 <= L <= QGEMM_MAX_ADAPTERS, rows of X 16-byte aligned; M,
+ * K and N up to 2^30. */
+int qgemm_lora_run(int M, int K, int N, int L, int R, int dtype, const int32_t* row, const int32_t* offsets, const void* X,
+                   long long ldx, const void* A, const void* B, const int32_t* rank, const float* scale, void* Y,
+                   int y_dtype, long long ldy, void* stream);
+
+/* norm(v) over a row of K values, in float32 */
+#define QGEMM_NORM_RMS 1   /* v / sqrt(mean(v^2) + eps)                    */
+#define QGEMM_NORM_LAYER 2 /* (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) */
+#define QGEMM_MAX_NORM_K 32768
+
+/* The step between two blocks: the norm behind a block, its gate, the residual sum, and the norm in front of the
+ * next block. For each row m of the block's output X:
+ *   f = X[m], or norm(X[m]) * post_weight with post = 1
+ *   s = r_scale * residual[m] + x_scale * gate * f      (residual NULL: none; gate NULL: 1)
+ *   y = norm(s) * weight + bias                         (weight NULL: 1; bias NULL: 0)
+ * in float32, where y is formed from s before s is rounded; S and Y are rounded once.
+ *   kind: QGEMM_NORM_*, of both norms; eps >= 0, added as written above. Squares and their sums must fit float32.
+ *   X: [M][ldx] in x_dtype; gate in x_dtype: one of K values for all rows (ldg = 0), or row m's at m * ldg.
+ *   post_weight, weight, bias: float32 [K] or NULL. post_weight is NULL with post = 0.
+ *   residual, S: [M][K] in s_dtype; S may be residual itself, or NULL (s is then not stored).
+ *   Y: [M][K] in y_dtype, or NULL (no norm of s). It may be X itself where that has Y's type and ldx = K. S or Y must be given.
+ * Buffers must not overlap in any other way. K % 64 == 0, K <= QGEMM_MAX_NORM_K, rows of X and gate 16-byte
+ * aligned, M <= 2^30. */
+int qgemm_norm_run(int M, int K, int kind, float eps, const void* X, int x_dtype, long long ldx, float x_scale, int post,
+                   const float* post_weight, const void* gate, long long ldg, const void* residual, float r_scale, void* S,
+                   int s_dtype, const float* weight, const float* bias, void* Y, int y_dtype, void* stream);
+
+/* Log probabilities of softmax(scale * logits) over each of T rows of V logits:
+ *   logprob float32 [T]: of the row's given token (token int32 [T]); 0 for a token outside [0, V). Both or neither NULL.
+ *   entropy float32 [T], in nats, or NULL.
+ *   top int32 [T][k], top_logprob float32 [T][k]: the k likeliest tokens, the likeliest first (ties: the lowest
+ *     token), and their log probabilities; -1 and -inf where fewer than k have any probability. k = 0: NULL.
+ *   logits: [T][ld] in dtype, ld >= V. A logit of -inf or NaN has probability 0. Logits of +inf share the whole
+ *     probability. A row without any probability has logprob -inf and entropy 0.
+ *   scale: finite and above 0 (1 / temperature).
+ * k <= QGEMM_MAX_TOPK; T and V up to 2^30. */
+int qgemm_logprobs(int T, int V, const void* logits, int dtype, long long ld, float scale, const int32_t* token,
+                   float* logprob, float* entropy, int k, int32_t* top, float* top_logprob, void* stream);
+
 /* ---------------------------------------------------------------- no-allocation variant */
 
 /* Size of the library's own scratch buffer used by qgemm_run_noalloc (4 MiB). */
@@ -433,7 +501,7 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
 /* QGEMM_OPT_FAULT_INJECT (default 0, or the value of the environment variable QGEMM_FAULT_INJECT
  * when the library loads). Host-side fault injection: when n > 0, the n-th compute call from now
  * (qgemm_pack, qgemm_run, qgemm_run_fused, qgemm_run_noalloc, qgemm_act_quant, qgemm_w4a8_acc, the
- * qgemm_fp4_*, qgemm_grouped_run and qgemm_moe_* calls) passes its argument checks and then returns
+ * qgemm_fp4_*, qgemm_grouped_run, qgemm_moe_*, qgemm_lora_*, qgemm_norm_run and qgemm_logprobs calls) passes its argument checks and then returns
  * QGEMM_ERR_CUDA with the detail "simulated launch failure" instead of launching, as a failed launch
  * would; the count then stays 0. No GPU fault is involved. For testing callers' error handling. Process-wide. */
 #define QGEMM_OPT_FAULT_INJECT 6

@@ -19,6 +19,8 @@ __all__ = [
     "qgemm_fused_quant_workspace_bytes", "qgemm_run_w4a8_codes", "qgemm_w4a8_codes_workspace_bytes",
     "qgemm_fp4_codes_bytes", "qgemm_fp4_scales_bytes", "qgemm_fp4_quant", "qgemm_fp4_dequant", "qgemm_fp4_pack", "qgemm_fp4_run",
     "qgemm_moe_route", "qgemm_moe_route_workspace_bytes", "qgemm_grouped_run", "qgemm_moe_combine",
+    "qgemm_lora_group", "qgemm_lora_run", "qgemm_norm_run", "qgemm_logprobs",
+    "NORM_RMS", "NORM_LAYER", "MAX_NORM_K", "MAX_ADAPTERS", "MAX_RANK",
     "FMT_F16", "FMT_BF16", "FMT_MXFP4", "FMT_NVFP4", "SCALES_ROWS", "SCALES_TILED", "ACT_SWIGLU", "MAX_EXPERTS", "MAX_TOPK",
     "MODE_FLOAT", "MODE_INT4", "MODE_INT8", "MODE_W4A8", "F32", "F16", "BF16", "LIB_PATH",
 ]
@@ -37,6 +39,9 @@ FMT_F16, FMT_BF16, FMT_MXFP4, FMT_NVFP4 = 1, 2, 3, 4
 SCALES_ROWS, SCALES_TILED = 0, 1
 ACT_SWIGLU = 4
 MAX_EXPERTS, MAX_TOPK = 1024, 32
+NORM_RMS, NORM_LAYER = 1, 2
+MAX_NORM_K = 32768
+MAX_ADAPTERS, MAX_RANK = 1024, 256
 OK = 0
 ERRORS = {-1: "QGEMM_ERR_ARG", -2: "QGEMM_ERR_UNSUPPORTED", -3: "QGEMM_ERR_ALIGN", -4: "QGEMM_ERR_WORKSPACE",
           -5: "QGEMM_ERR_CUDA", -6: "QGEMM_ERR_TIMEOUT", -7: "QGEMM_ERR_IO"}
@@ -45,7 +50,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 _lib = None
 
 # exported symbol -> (argtypes, restype)
-_P, _I, _SZ, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+_P, _I, _SZ, _LL, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "qgemm_packed_bytes": ([_I, _I, _I, _I], _SZ),
     "qgemm_table_bytes": ([_I, _I, _I, _I], _SZ),
@@ -75,6 +80,10 @@ SIGNATURES = {
     "qgemm_moe_route_workspace_bytes": ([_I, _I, _I], _SZ),
     "qgemm_grouped_run": ([_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _P], _I),
     "qgemm_moe_combine": ([_I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _I, _P], _I),
+    "qgemm_lora_group": ([_I, _I, _P, _P, _P, _P], _I),
+    "qgemm_lora_run": ([_I, _I, _I, _I, _I, _I, _P, _P, _P, _LL, _P, _P, _P, _P, _P, _I, _LL, _P], _I),
+    "qgemm_norm_run": ([_I, _I, _I, _F, _P, _I, _LL, _F, _I, _P, _P, _LL, _P, _F, _P, _I, _P, _P, _P, _I, _P], _I),
+    "qgemm_logprobs": ([_I, _I, _P, _I, _LL, _F, _P, _P, _P, _I, _P, _P, _P], _I),
     "qgemm_set_option": ([_I, _I], _I),
     "qgemm_get_option": ([_I], _I),
     "qgemm_error_string": ([_I], ctypes.c_char_p),
@@ -324,6 +333,35 @@ def qgemm_moe_combine(T: int, k: int, N: int, R: int, Y, y_dtype: int, slot, wei
     """out[t] = sum_j weight[t][j] * Y[slot[t][j]] + residual[t] (see qgemm.h)."""
     _check(load().qgemm_moe_combine(T, k, N, R, _ptr(Y), y_dtype, _ptr(slot), _ptr(weight), _ptr(residual), _ptr(out),
                                     out_dtype, _stream(stream)), "qgemm_moe_combine")
+
+
+# ---------------------------------------------------------------- around the layer
+def qgemm_lora_group(M: int, L: int, adapter, row, offsets, stream=None) -> None:
+    """The rows of a batch in order of their adapter (see qgemm.h)."""
+    _check(load().qgemm_lora_group(M, L, _ptr(adapter), _ptr(row), _ptr(offsets), _stream(stream)), "qgemm_lora_group")
+
+
+def qgemm_lora_run(M: int, K: int, N: int, L: int, R: int, dtype: int, row, offsets, X, ldx: int, A, B, rank, scale, Y,
+                   y_dtype: int, ldy: int, stream=None) -> None:
+    """Y[m] += scale[l] * B[l] (A[l] X[m]) for the rows of each adapter l, in place (see qgemm.h)."""
+    _check(load().qgemm_lora_run(M, K, N, L, R, dtype, _ptr(row), _ptr(offsets), _ptr(X), ldx, _ptr(A), _ptr(B), _ptr(rank),
+                                 _ptr(scale), _ptr(Y), y_dtype, ldy, _stream(stream)), "qgemm_lora_run")
+
+
+def qgemm_norm_run(M: int, K: int, kind: int, eps: float, X, x_dtype: int, ldx: int, x_scale: float, post: int, post_weight,
+                   gate, ldg: int, residual, r_scale: float, S, s_dtype: int, weight, bias, Y, y_dtype: int,
+                   stream=None) -> None:
+    """S = r_scale * residual + x_scale * gate * (X or norm(X)), Y = norm(S) * weight + bias (see qgemm.h)."""
+    _check(load().qgemm_norm_run(M, K, kind, eps, _ptr(X), x_dtype, ldx, x_scale, post, _ptr(post_weight), _ptr(gate), ldg,
+                                 _ptr(residual), r_scale, _ptr(S), s_dtype, _ptr(weight), _ptr(bias), _ptr(Y), y_dtype,
+                                 _stream(stream)), "qgemm_norm_run")
+
+
+def qgemm_logprobs(T: int, V: int, logits, dtype: int, ld: int, scale: float, token, logprob, entropy, k: int, top,
+                   top_logprob, stream=None) -> None:
+    """Log probabilities of given tokens, entropy, and the k likeliest tokens of each row (see qgemm.h)."""
+    _check(load().qgemm_logprobs(T, V, _ptr(logits), dtype, ld, scale, _ptr(token), _ptr(logprob), _ptr(entropy), k,
+                                 _ptr(top), _ptr(top_logprob), _stream(stream)), "qgemm_logprobs")
 
 
 def qgemm_status(stream=None) -> int:

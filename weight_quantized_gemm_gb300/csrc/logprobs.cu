@@ -1,0 +1,424 @@
+// Log probabilities of given tokens, entropy and the likeliest tokens of rows of logits, in one pass over them.
+//
+// With z = scale * logit, M the row's largest z and S = sum exp(z - M):
+//   logprob[j] = z_j - M - ln S,   entropy = ln S - sum (z - M) exp(z - M) / S   (both terms are not negative)
+// A thread sums 2^t and t 2^t, t = (x - ref) scale log2(e), against a reference of its own, which moves only when a
+// value is more than kSlack doublings above it (each move rescales both sums; following the largest value itself
+// would take that branch in most steps, as some lane of a warp nearly always finds a larger one). t is held to
+// -200 from below, which makes both terms 0 and takes in -inf and NaN, too: the larger of NaN and -200 is -200.
+//
+// The k likeliest: each thread keeps its largest value and the place where it found it first. The k best of those
+// (by value, then place) belong to k threads that must hold the row's k best values: any other thread has k
+// values before its own best one. Only those threads' values are read again (from L2), and what is not below
+// the k-th best is put in order by warps, 32 keys at a time. A key is the value's order-preserving bits above the
+// complement of its index, so of equal values the lowest index comes first.
+//
+// A row is cut into equal runs of 16-byte pieces for the blocks of a cluster where the batch has few rows; their
+// sums and lists meet in the first block through distributed shared memory.
+#include <float.h>
+
+#include "serve.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kUnroll = 4;                 // 16-byte loads that a thread has in flight
+constexpr int kMaxCluster = 8;
+constexpr float kSlack = 3.f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+using Key = unsigned long long;
+
+struct Args {
+    int V;
+    const uint8_t* logits;
+    long long ld_bytes;
+    float scale, c;             // c = scale * log2(e)
+    const int32_t* token;
+    float* logprob;
+    float* entropy;
+    int k;
+    int32_t* top;
+    float* top_logprob;
+};
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
+__device__ __forceinline__ float pos_inf() { return __uint_as_float(0x7F800000u); }
+__device__ __forceinline__ float exp2_fast(float t) {      // 2^t, a few units in the last place; 0 below 2^-126
+    float p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+    return p;
+}
+
+// Grows with the value; 0 for -inf and NaN.
+__device__ __forceinline__ uint32_t to_key(float x) {
+    if (!(x > neg_inf())) return 0u;
+    const uint32_t b = __float_as_uint(x + 0.f);   // -0 and 0 are one value
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_key(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// ---------------------------------------------------------------- a warp's 32 keys in falling order
+__device__ __forceinline__ Key exchange(Key x, int o, bool larger) {
+    const Key y = __shfl_xor_sync(0xffffffffu, x, o);
+    return (x > y) == larger ? x : y;
+}
+__device__ __forceinline__ Key sorted(Key x, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size >> 1; o; o >>= 1) x = exchange(x, o, ((lane & o) == 0) == ((lane & size) == 0));
+    return x;
+}
+// The 32 largest of two lists in falling order.
+__device__ __forceinline__ Key merged(Key a, Key b, int lane) {
+    const Key y = __shfl_sync(0xffffffffu, b, 31 - lane);
+    Key x = a > y ? a : y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = exchange(x, o, (lane & o) == 0);
+    return x;
+}
+// The 32 largest of `count` (a power of two) warps' lists, in warp 0. Every thread of the block calls it.
+__device__ __forceinline__ Key merge_warps(Key key, int count, Key (*lists)[32], int warp, int lane) {
+    __syncthreads();
+    lists[warp][lane] = key;
+    for (int h = count >> 1; h; h >>= 1) {
+        __syncthreads();
+        if (warp < h) {
+            key = merged(key, lists[warp + h][lane], lane);
+            lists[warp][lane] = key;
+        }
+    }
+    return key;
+}
+
+// ---------------------------------------------------------------- a row
+template <int DT>
+struct Row {
+    static constexpr int kSize = DT == DT_F32 ? 4 : 2, kPer = 16 / kSize;
+    static constexpr uint32_t kNone = DT == DT_F32 ? 0xFF800000u : (DT == DT_F16 ? 0xFC00FC00u : 0xFF80FF80u);    // -inf
+    const uint8_t* from;        // 16-byte aligned, at or before the row's first value
+    int skip, end;              // the row is values skip .. end - 1 from there
+    __device__ __forceinline__ Row(const uint8_t* row, int V) {
+        const int over = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
+        from = row - over;
+        skip = over / kSize;
+        end = skip + V;         // (V <= 2^30)
+    }
+    __device__ __forceinline__ int pieces() const { return (end + kPer - 1) / kPer; }
+    // A piece at an end of the row: the values outside are neither read nor counted.
+    __device__ __noinline__ uint4 edge(int v) const {
+        uint32_t w[4] = {kNone, kNone, kNone, kNone};
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int i = v * kPer + j;
+            if (i < skip || i >= end) continue;
+            if constexpr (DT == DT_F32) w[j] = load(reinterpret_cast<const uint32_t*>(from) + i);
+            else {
+                const uint32_t h = load(reinterpret_cast<const uint16_t*>(from) + i);
+                w[j >> 1] = (j & 1) ? (w[j >> 1] & 0xFFFFu) | h << 16 : (w[j >> 1] & 0xFFFF0000u) | h;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ uint4 piece(int v) const {
+        if (v * kPer >= skip && (v + 1) * kPer <= end) return load(reinterpret_cast<const uint4*>(from) + v);
+        return edge(v);
+    }
+    __device__ __forceinline__ static void values(const uint4& raw, float (&x)[kPer]) {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            if constexpr (DT == DT_F32) x[j] = __uint_as_float(w[j]);
+            else if constexpr (DT == DT_BF16) x[j] = __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+            else x[j] = __half2float(__ushort_as_half((unsigned short)(w[j >> 1] >> (16 * (j & 1)))));
+        }
+    }
+};
+
+// Two float32 at once.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// sum of 2^t and of t 2^t against `ref`
+struct Sums {
+    float ref, s, e;
+    // the same against another reference, at or above this one
+    __device__ __forceinline__ void against(float to, float c) {
+        if (ref == neg_inf()) s = e = 0.f;
+        else {
+            const float d = (ref - to) * c, f = exp2_fast(d);
+            e = f * (f > 0.f ? fmaf(s, d, e) : 0.f);
+            s *= f;
+        }
+        ref = to;
+    }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
+    using R = Row<DT>;
+    constexpr int P = R::kPer;
+    __shared__ Key lists[kWarps][32];
+    __shared__ Key best[32];            // the block's threads with the largest values, then its largest values
+    __shared__ float s_top[kWarps];
+    __shared__ float3 s_sums[kWarps];
+    __shared__ float4 s_block;          // the block's largest logit and its sums against that; number of +inf
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t blocks = cluster_size(), rank = blocks > 1 ? cluster_rank() : 0u;
+    const size_t t = blockIdx.x / blocks;
+    grid_wait();
+    grid_release();
+    const R row(a.logits + (long long)t * a.ld_bytes, a.V);
+    const int pieces = row.pieces(), run = (pieces + (int)blocks - 1) / (int)blocks;
+    const int v0 = min((int)rank * run, pieces), v1 = min(v0 + run, pieces);
+
+    // ---- the pass
+    Sums sums{neg_inf(), 0.f, 0.f};
+    float most = neg_inf(), limit = neg_inf();
+    int place = 0;
+    uint64_t s2 = 0, e2 = 0, ref2 = 0;
+    const uint64_t c2 = pack2(a.c, a.c);
+    const float slack = kSlack / a.c;
+    for (int v = v0 + tid; v < v1; v += kUnroll * kThreads) {
+        uint4 raw[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int w = v + u * kThreads;
+            raw[u] = w < v1 ? row.piece(w) : make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float x[P];
+            R::values(raw[u], x);
+            float here = x[0];
+#pragma unroll
+            for (int j = 1; j < P; ++j) here = fmaxf(here, x[j]);
+            if (here > most) {
+                most = here;
+                place = v + u * kThreads;
+            }
+            if (here > limit) {
+                float s0, s1, e0, e1;
+                unpack2(s2, s0, s1);
+                unpack2(e2, e0, e1);
+                sums.s = s0 + s1;
+                sums.e = e0 + e1;
+                sums.against(here, a.c);
+                s2 = pack2(sums.s, 0.f);
+                e2 = pack2(sums.e, 0.f);
+                ref2 = pack2(-here, -here);
+                limit = here + slack;
+            }
+#pragma unroll
+            for (int j = 0; j < P; j += 2) {
+                float t0, t1;
+                unpack2(mul2(add2(pack2(x[j], x[j + 1]), ref2), c2), t0, t1);
+                t0 = fmaxf(t0, -200.f);
+                t1 = fmaxf(t1, -200.f);
+                const uint64_t p2 = pack2(exp2_fast(t0), exp2_fast(t1));
+                s2 = add2(s2, p2);
+                e2 = fma2(p2, pack2(t0, t1), e2);
+            }
+        }
+    }
+    {
+        float s0, s1, e0, e1;
+        unpack2(s2, s0, s1);
+        unpack2(e2, e0, e1);
+        sums.s = s0 + s1;
+        sums.e = e0 + e1;
+    }
+
+    // ---- the block's sums
+    float top = most;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
+    top = s_top[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_top[w]);
+    sums.against(top, a.c);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sums.s += __shfl_xor_sync(0xffffffffu, sums.s, o);
+        sums.e += __shfl_xor_sync(0xffffffffu, sums.e, o);
+    }
+    if (lane == 0) s_sums[warp] = make_float3(sums.s, sums.e, 0.f);
+    __syncthreads();
+    if (tid == 0) {
+        float s = 0.f, e = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            s += s_sums[w].x;
+            e += s_sums[w].y;
+        }
+        s_block = make_float4(top, s, e, 0.f);
+    }
+
+    // ---- the block's k largest values
+    if (a.k > 0) {
+        const uint32_t high = to_key(most);
+        Key key = high ? (Key)high << 32 | (uint32_t)~place : 0;
+        key = merge_warps(sorted(key, lane), kWarps, lists, warp, lane);
+        if (warp == 0) best[lane] = key;
+        __syncthreads();
+        const uint32_t least = (uint32_t)(best[a.k - 1] >> 32);     // 0: fewer than k threads hold any value
+        Key list = 0;
+        for (int j = warp; j < a.k; j += kWarps) {
+            if (best[j] == 0) break;
+            const int mine = ((int)~(uint32_t)best[j] - v0) % kThreads + v0;      // that thread's first piece
+            for (int v = mine + lane * kThreads; __any_sync(0xffffffffu, v < v1); v += 32 * kThreads) {
+                float x[P];
+                uint32_t left = 0;
+                if (v < v1) {
+                    R::values(row.piece(v), x);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const uint32_t h = to_key(x[i]);
+                        if (h != 0 && h >= least) left |= 1u << i;
+                    }
+                }
+                while (__any_sync(0xffffffffu, left != 0)) {
+                    Key cand = 0;
+                    if (left) {
+                        const int i = __ffs(left) - 1;
+                        left &= left - 1;
+                        float y = x[0];
+#pragma unroll
+                        for (int q = 1; q < P; ++q) y = i == q ? x[q] : y;
+                        cand = (Key)to_key(y) << 32 | (uint32_t)~(v * P + i - row.skip);
+                    }
+                    list = merged(list, sorted(cand, lane), lane);
+                }
+            }
+        }
+        int count = 1;
+        while (count < min(a.k, kWarps)) count <<= 1;
+        list = merge_warps(list, count, lists, warp, lane);
+        if (warp == 0) best[lane] = list;       // (merge_warps has synchronized since best was read)
+    }
+
+    // ---- the row's, by the cluster's first block
+    float4 all;
+    if (blocks > 1) {
+        cluster_sync();
+        float4 part[kMaxCluster];
+        top = neg_inf();
+#pragma unroll
+        for (int b = 0; b < kMaxCluster; ++b)
+            if (b < (int)blocks) {
+                part[b] = ld_cluster_f32x4(in_block(&s_block, b));
+                top = fmaxf(top, part[b].x);
+            }
+        all = make_float4(top, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int b = 0; b < kMaxCluster; ++b)
+            if (b < (int)blocks) {
+                Sums p{part[b].x, part[b].y, part[b].z};
+                p.against(top, a.c);
+                all.y += p.s;
+                all.z += p.e;
+            }
+    } else {
+        __syncthreads();
+        all = s_block;
+    }
+    float infinite = 0.f;
+    if (all.x == pos_inf()) {                   // the same for all threads of the cluster: count the row's +inf
+        float n = 0.f;
+        for (int v = v0 + tid; v < v1; v += kThreads) {
+            float x[P];
+            R::values(row.piece(v), x);
+#pragma unroll
+            for (int j = 0; j < P; ++j) n += x[j] == pos_inf() ? 1.f : 0.f;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        if (lane == 0) s_top[warp] = n;
+        __syncthreads();
+        n = 0.f;
+        for (int w = 0; w < kWarps; ++w) n += s_top[w];
+        if (tid == 0) s_block.w = n;
+        if (blocks > 1) cluster_sync();
+        else __syncthreads();
+        for (int b = 0; b < (int)blocks; ++b) infinite += blocks > 1 ? ld_cluster_f32(in_block(&s_block.w, b)) : s_block.w;
+    }
+    if (rank == 0) {
+        const float over = infinite > 0.f ? logf(infinite) : logf(all.y);      // ln S
+        auto log_p = [&](float x) {
+            if (infinite > 0.f) return x == pos_inf() ? -over : neg_inf();
+            return x > neg_inf() ? fminf((x - all.x) * a.scale - over, 0.f) : neg_inf();
+        };
+        if (tid == 0) {
+            if (a.logprob) {
+                const int token = load(a.token + t);
+                float lp = 0.f;
+                if (token >= 0 && token < a.V) lp = log_p(load_as_float<DT>(row.from, (size_t)row.skip + token));
+                a.logprob[t] = lp;
+            }
+            if (a.entropy) a.entropy[t] = infinite > 0.f ? over : (all.y > 0.f ? fmaxf(over - kLn2 * all.z / all.y, 0.f) : 0.f);
+        }
+        if (a.k > 0) {
+            if (blocks > 1) {
+                Key key = warp < (int)blocks ? ld_cluster_u64(in_block(&best[lane], warp)) : 0;
+                key = merge_warps(key, (int)blocks, lists, warp, lane);
+                if (warp == 0) best[lane] = key;
+            }
+            if (tid < a.k) {
+                const Key key = best[tid];
+                const float x = from_key((uint32_t)(key >> 32));
+                const bool any = key != 0 && (infinite == 0.f || x == pos_inf());
+                a.top[t * a.k + tid] = any ? (int)~(uint32_t)key : -1;
+                a.top_logprob[t * a.k + tid] = any ? log_p(x) : neg_inf();
+            }
+        }
+    }
+    if (blocks > 1) cluster_sync();     // no block leaves while the first reads its shared memory
+}
+
+template <int DT>
+cudaError_t launch_dt(const Args& a, int T, cudaStream_t s) {
+    const int pieces = (int)(((long long)a.V * (DT == DT_F32 ? 4 : 2) + 15) / 16);
+    int blocks = 1;
+    while (blocks < kMaxCluster && (long long)T * blocks < 2 * kTargetSms && pieces > 2 * blocks * kThreads) blocks *= 2;
+    return launch_behind(logprobs_kernel<DT>, dim3((unsigned)T * blocks), dim3(kThreads), 0, (unsigned)blocks, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(int T, int V, const void* logits, int dtype, long long ld, float scale, const int32_t* token,
+                            float* logprob, float* entropy, int k, int32_t* top, float* top_logprob, cudaStream_t s) {
+    const float c = scale * kLog2e;
+    const Args a{V, static_cast<const uint8_t*>(logits), ld * (long long)dt_size(dtype), scale, c < FLT_MAX ? c : FLT_MAX,
+                 token, logprob, entropy, k, top, top_logprob};
+    switch (dtype) {
+        case DT_F32: return launch_dt<DT_F32>(a, T, s);
+        case DT_F16: return launch_dt<DT_F16>(a, T, s);
+        default: return launch_dt<DT_BF16>(a, T, s);
+    }
+}
+
+}  // namespace qg
