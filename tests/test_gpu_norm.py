@@ -72,7 +72,7 @@ def test_types(M, K, x_dtype, s_dtype, y_dtype, kind):
 
 
 @pytest.mark.parametrize("kind", [qg.NORM_RMS, qg.NORM_LAYER])
-@pytest.mark.parametrize("M,K", [(1, 64), (9, 64), (1001, 192), (7, 256), (6, 320), (5, 2048), (3, 4096), (300, 4096), (2, 8192), (3, 8256), (2, 16384), (1, 16448), (2, 32768)])
+@pytest.mark.parametrize("M,K", [(1, 64), (9, 64), (1001, 192), (7, 256), (6, 320), (5, 2048), (3, 4096), (300, 4096), (305, 4096), (310, 320), (306, 1088), (306, 2240), (305, 9728), (305, 10304), (305, 64), (2, 8192), (3, 8256), (2, 16384), (1, 16448), (2, 32768)])
 def test_sizes(M, K, kind):
     check(make(M, K, kind, qg.BF16, qg.F32, qg.BF16, gate="row"))
 

@@ -42,8 +42,13 @@ struct NormArgs {
     const float* bias;          // [K] or none
     void* Y;                    // [M][K] or none
 };
-constexpr int kNormMaxK = 32768;
-cudaError_t launch_norm(const NormArgs& a, int x_dtype, int s_dtype, int y_dtype, cudaStream_t s);
+cudaError_t launch_norm_f32(const NormArgs& a, int s_dtype, int y_dtype, cudaStream_t s);
+cudaError_t launch_norm_f16(const NormArgs& a, int s_dtype, int y_dtype, cudaStream_t s);
+cudaError_t launch_norm_bf16(const NormArgs& a, int s_dtype, int y_dtype, cudaStream_t s);
+inline cudaError_t launch_norm(const NormArgs& a, int x_dtype, int s_dtype, int y_dtype, cudaStream_t s) {
+    return x_dtype == DT_F32 ? launch_norm_f32(a, s_dtype, y_dtype, s)
+                             : (x_dtype == DT_F16 ? launch_norm_f16(a, s_dtype, y_dtype, s) : launch_norm_bf16(a, s_dtype, y_dtype, s));
+}
 
 cudaError_t launch_logprobs(int T, int V, const void* logits, int dtype, long long ld, float scale, const int32_t* token,
                             float* logprob, float* entropy, int k, int32_t* top, float* top_logprob, cudaStream_t s);
