@@ -2,10 +2,12 @@
 //
 // With z = scale * logit, M the row's largest z and S = sum exp(z - M):
 //   logprob[j] = z_j - M - ln S,   entropy = ln S - sum (z - M) exp(z - M) / S   (both terms are not negative)
-// A thread sums 2^t and t 2^t, t = (x - ref) scale log2(e), against a reference of its own, which moves only when a
-// value is more than kSlack doublings above it (each move rescales both sums; following the largest value itself
-// would take that branch in most steps, as some lane of a warp nearly always finds a larger one). t is held to
-// -200 from below, which makes both terms 0 and takes in -inf and NaN, too: the larger of NaN and -200 is -200.
+// A thread sums 2^t and t 2^t, t = x c - ref with c = scale log2(e), against a reference of its own, which moves only
+// when a value is more than kSlack doublings above it (each move rescales both sums; following the largest value itself
+// would take that branch in most steps, as some lane of a warp nearly always finds a larger one). The reference is
+// a float32 in units of t, and the fused product and difference round once, so its own rounding costs nothing. t is
+// held to -200 from below, which makes both terms 0 and takes in -inf and NaN, too: the larger of NaN and -200 is -200.
+// Rows whose largest value times c is 2^22 or more are summed a second time, from differences of values.
 //
 // The k likeliest: each thread keeps its largest value and the place where it found it first. The k best of those
 // (by value, then place) belong to k threads that must hold the row's k best values: any other thread has k
@@ -22,10 +24,12 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kUnroll = 4;                 // 16-byte loads that a thread has in flight
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kUnroll = 8;                 // 16-byte loads that a thread has in flight
 constexpr int kMaxCluster = 8;
+static_assert(kMaxCluster <= kWarps, "a warp reads each block's list");
 constexpr float kSlack = 3.f;
+constexpr float kFar = 4194304.f;          // of a reference, whose own rounding is then a quarter or more
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 using Key = unsigned long long;
 
@@ -165,26 +169,42 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 struct Sums {
     float ref, s, e;
     // the same against another reference, at or above this one
-    __device__ __forceinline__ void against(float to, float c) {
-        if (ref == neg_inf()) s = e = 0.f;
-        else {
-            const float d = (ref - to) * c, f = exp2_fast(d);
-            e = f * (f > 0.f ? fmaf(s, d, e) : 0.f);
-            s *= f;
-        }
+    __device__ __forceinline__ void against(float to) {
+        const float d = ref - to, f = exp2_fast(d);
+        e = f > 0.f ? f * fmaf(s, d, e) : 0.f;      // (a reference of -inf has no sums, or none that can be told)
+        s = f > 0.f ? s * f : 0.f;
         ref = to;
     }
 };
+// Sums over the block, in thread 0; part: [kWarps] shared memory.
+__device__ __forceinline__ void block_sums(Sums& sums, float2* part, int warp, int lane) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sums.s += __shfl_xor_sync(0xffffffffu, sums.s, o);
+        sums.e += __shfl_xor_sync(0xffffffffu, sums.e, o);
+    }
+    if (lane == 0) part[warp] = make_float2(sums.s, sums.e);
+    __syncthreads();
+    if (warp == 0 && lane == 0) {
+        sums.s = sums.e = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            sums.s += part[w].x;
+            sums.e += part[w].y;
+        }
+    }
+}
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     using R = Row<DT>;
     constexpr int P = R::kPer;
     __shared__ Key lists[kWarps][32];
     __shared__ Key best[32];            // the block's threads with the largest values, then its largest values
     __shared__ float s_top[kWarps];
-    __shared__ float3 s_sums[kWarps];
-    __shared__ float4 s_block;          // the block's largest logit and its sums against that; number of +inf
+    __shared__ float2 s_sums[kWarps];
+    __shared__ float4 s_again;          // the sums from differences
+    __shared__ float4 s_block;          // the block's largest logit, and its sums against that
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t blocks = cluster_size(), rank = blocks > 1 ? cluster_rank() : 0u;
     const size_t t = blockIdx.x / blocks;
@@ -195,61 +215,73 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
     const int v0 = min((int)rank * run, pieces), v1 = min(v0 + run, pieces);
 
     // ---- the pass
-    Sums sums{neg_inf(), 0.f, 0.f};
-    float most = neg_inf(), limit = neg_inf();
+    float most = neg_inf(), limit = neg_inf(), ref = neg_inf();
     int place = 0;
-    uint64_t s2 = 0, e2 = 0, ref2 = 0;
+    uint64_t s2 = 0, e2 = 0, minus2 = 0;
     const uint64_t c2 = pack2(a.c, a.c);
     const float slack = kSlack / a.c;
-    for (int v = v0 + tid; v < v1; v += kUnroll * kThreads) {
-        uint4 raw[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int w = v + u * kThreads;
-            raw[u] = w < v1 ? row.piece(w) : make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float x[P];
-            R::values(raw[u], x);
-            float here = x[0];
-#pragma unroll
-            for (int j = 1; j < P; ++j) here = fmaxf(here, x[j]);
-            if (here > most) {
-                most = here;
-                place = v + u * kThreads;
-            }
-            if (here > limit) {
-                float s0, s1, e0, e1;
-                unpack2(s2, s0, s1);
-                unpack2(e2, e0, e1);
-                sums.s = s0 + s1;
-                sums.e = e0 + e1;
-                sums.against(here, a.c);
-                s2 = pack2(sums.s, 0.f);
-                e2 = pack2(sums.e, 0.f);
-                ref2 = pack2(-here, -here);
-                limit = here + slack;
-            }
-#pragma unroll
-            for (int j = 0; j < P; j += 2) {
-                float t0, t1;
-                unpack2(mul2(add2(pack2(x[j], x[j + 1]), ref2), c2), t0, t1);
-                t0 = fmaxf(t0, -200.f);
-                t1 = fmaxf(t1, -200.f);
-                const uint64_t p2 = pack2(exp2_fast(t0), exp2_fast(t1));
-                s2 = add2(s2, p2);
-                e2 = fma2(p2, pack2(t0, t1), e2);
-            }
-        }
-    }
-    {
+    // A logit in units of t, rounded: not to be fused with what follows, which would then see another reference.
+    auto in_units = [&](float x) { return __fmul_rn(x, a.c); };
+    auto sums_now = [&]() {
         float s0, s1, e0, e1;
         unpack2(s2, s0, s1);
         unpack2(e2, e0, e1);
-        sums.s = s0 + s1;
-        sums.e = e0 + e1;
+        return Sums{ref, s0 + s1, e0 + e1};
+    };
+    auto take = [&](const uint4& raw, int v) {
+        float x[P];
+        R::values(raw, x);
+        float here = x[0];
+#pragma unroll
+        for (int j = 1; j < P; ++j) here = fmaxf(here, x[j]);
+        if (here > most) {
+            most = here;
+            place = v;
+        }
+        if (here > limit) {
+            Sums sums = sums_now();
+            sums.against(in_units(here));
+            ref = sums.ref;
+            s2 = pack2(sums.s, 0.f);
+            e2 = pack2(sums.e, 0.f);
+            minus2 = pack2(-ref, -ref);
+            limit = here + slack;
+        }
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+            float t0, t1;
+            unpack2(fma2(pack2(x[j], x[j + 1]), c2, minus2), t0, t1);
+            t0 = fmaxf(t0, -200.f);
+            t1 = fmaxf(t1, -200.f);
+            const uint64_t p2 = pack2(exp2_fast(t0), exp2_fast(t1));
+            s2 = add2(s2, p2);
+            e2 = fma2(p2, pack2(t0, t1), e2);
+        }
+    };
+    // The row's first and last piece may be cut: by themselves, in their place in the order of each thread's pieces.
+    const int whole0 = max(v0, row.skip ? 1 : 0), whole1 = min(v1, row.end / P);
+    if (tid == 0 && v0 < min(whole0, v1)) take(row.edge(v0), v0);
+    for (int v = v0; v < whole1; v += kUnroll * kThreads) {
+        const uint4* from = reinterpret_cast<const uint4*>(row.from) + v + tid;
+        uint4 raw[kUnroll];
+        if (v >= whole0 && v + kUnroll * kThreads <= whole1) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) raw[u] = load(from + u * kThreads);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) take(raw[u], v + tid + u * kThreads);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int w = v + tid + u * kThreads;
+                raw[u] = make_uint4(R::kNone, R::kNone, R::kNone, R::kNone);
+                if (w >= whole0 && w < whole1) raw[u] = load(from + u * kThreads);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (v + u * kThreads < whole1) take(raw[u], v + tid + u * kThreads);
+        }
     }
+    if (const int last = max(whole1, v0); last < v1 && last >= whole0 && tid == (last - v0) % kThreads) take(row.edge(last), last);
 
     // ---- the block's sums
     float top = most;
@@ -260,23 +292,10 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
     top = s_top[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_top[w]);
-    sums.against(top, a.c);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        sums.s += __shfl_xor_sync(0xffffffffu, sums.s, o);
-        sums.e += __shfl_xor_sync(0xffffffffu, sums.e, o);
-    }
-    if (lane == 0) s_sums[warp] = make_float3(sums.s, sums.e, 0.f);
-    __syncthreads();
-    if (tid == 0) {
-        float s = 0.f, e = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            s += s_sums[w].x;
-            e += s_sums[w].y;
-        }
-        s_block = make_float4(top, s, e, 0.f);
-    }
+    Sums sums = sums_now();
+    sums.against(in_units(top));
+    block_sums(sums, s_sums, warp, lane);
+    if (tid == 0) s_block = make_float4(top, sums.s, sums.e, 0.f);
 
     // ---- the block's k largest values
     if (a.k > 0) {
@@ -337,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
 #pragma unroll
         for (int b = 0; b < kMaxCluster; ++b)
             if (b < (int)blocks) {
-                Sums p{part[b].x, part[b].y, part[b].z};
-                p.against(top, a.c);
+                Sums p{in_units(part[b].x), part[b].y, part[b].z};
+                p.against(in_units(top));
                 all.y += p.s;
                 all.z += p.e;
             }
@@ -346,30 +365,40 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
         __syncthreads();
         all = s_block;
     }
-    float infinite = 0.f;
-    if (all.x == pos_inf()) {                   // the same for all threads of the cluster: count the row's +inf
-        float n = 0.f;
+    // A reference too far away (the same for all threads of the cluster): with logits of +inf their number is the sum;
+    // else both sums once more, from differences.
+    const bool infinite = all.x == pos_inf();
+    if (infinite || (all.x > neg_inf() && fabsf(in_units(all.x)) >= kFar)) {
+        Sums again{0.f, 0.f, 0.f};
         for (int v = v0 + tid; v < v1; v += kThreads) {
             float x[P];
             R::values(row.piece(v), x);
 #pragma unroll
-            for (int j = 0; j < P; ++j) n += x[j] == pos_inf() ? 1.f : 0.f;
+            for (int j = 0; j < P; ++j) {
+                const float t = infinite ? (x[j] == pos_inf() ? 0.f : -200.f) : fmaxf((x[j] - all.x) * a.c, -200.f);
+                const float p = exp2_fast(t);
+                again.s += p;
+                again.e = fmaf(p, t, again.e);
+            }
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        if (lane == 0) s_top[warp] = n;
-        __syncthreads();
-        n = 0.f;
-        for (int w = 0; w < kWarps; ++w) n += s_top[w];
-        if (tid == 0) s_block.w = n;
+        block_sums(again, s_sums, warp, lane);
+        if (tid == 0) s_again = make_float4(all.x, again.s, again.e, 0.f);
         if (blocks > 1) cluster_sync();
         else __syncthreads();
-        for (int b = 0; b < (int)blocks; ++b) infinite += blocks > 1 ? ld_cluster_f32(in_block(&s_block.w, b)) : s_block.w;
+        all.y = all.z = 0.f;
+        for (int b = 0; b < (int)blocks; ++b) {
+            const float4 p = blocks > 1 ? ld_cluster_f32x4(in_block(&s_again, b)) : s_again;
+            all.y += p.y;
+            all.z += p.z;
+        }
+        all.w = 0.f;
+    } else {
+        all.w = all.x > neg_inf() ? fmaf(all.x, a.c, -in_units(all.x)) : 0.f;      // of the largest value, against the reference
     }
     if (rank == 0) {
-        const float over = infinite > 0.f ? logf(infinite) : logf(all.y);      // ln S
+        const float over = logf(all.y) - kLn2 * all.w;      // ln S
         auto log_p = [&](float x) {
-            if (infinite > 0.f) return x == pos_inf() ? -over : neg_inf();
+            if (infinite) return x == pos_inf() ? -over : neg_inf();
             return x > neg_inf() ? fminf((x - all.x) * a.scale - over, 0.f) : neg_inf();
         };
         if (tid == 0) {
@@ -379,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
                 if (token >= 0 && token < a.V) lp = log_p(load_as_float<DT>(row.from, (size_t)row.skip + token));
                 a.logprob[t] = lp;
             }
-            if (a.entropy) a.entropy[t] = infinite > 0.f ? over : (all.y > 0.f ? fmaxf(over - kLn2 * all.z / all.y, 0.f) : 0.f);
+            if (a.entropy) a.entropy[t] = all.y > 0.f ? fmaxf(logf(all.y) - kLn2 * all.z / all.y, 0.f) : 0.f;
         }
         if (a.k > 0) {
             if (blocks > 1) {
@@ -390,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Args a) {
             if (tid < a.k) {
                 const Key key = best[tid];
                 const float x = from_key((uint32_t)(key >> 32));
-                const bool any = key != 0 && (infinite == 0.f || x == pos_inf());
+                const bool any = key != 0 && (!infinite || x == pos_inf());
                 a.top[t * a.k + tid] = any ? (int)~(uint32_t)key : -1;
                 a.top_logprob[t * a.k + tid] = any ? log_p(x) : neg_inf();
             }
