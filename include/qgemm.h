@@ -481,8 +481,8 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
 #define QGEMM_OPT_SPLIT_K 3
 
 /* QGEMM_OPT_WAIT_LIMIT_US (default 1000000, range 1..1000000). The TMA-fed kernels (the decode
- * kernel for M <= 16, the tensor-core kernel and that of the 4-bit and grouped products) bound every
- * wait of their pipelines by this many microseconds of the GPU's global timer: a wait that runs out sets the status word that
+ * kernel for M <= 16, the tensor-core kernel and that of the 4-bit and grouped products), and the adapters'
+ * kernel for many rows, bound every wait of their pipelines by this many microseconds of the GPU's global timer: a wait that runs out sets the status word that
  * qgemm_status reports as QGEMM_ERR_TIMEOUT, every role of the thread block leaves its loop, the
  * copies and MMAs already issued are waited for (always with the full one-second bound; 20 ms for a
  * stage's copies in the 4-bit and grouped products, whose barrier may never complete then) and the

@@ -425,7 +425,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
             }
         }
     }
-    if (blocks > 1) cluster_sync();     // no block leaves while the first reads its shared memory
+    if (blocks > 1) {       // no block leaves while the first reads its shared memory
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 template <int DT>

@@ -1,11 +1,13 @@
 // Low-rank adapters beside a shared projection: Y[m] += scale_l B_l (A_l X[m]) for the rows of every adapter, in one
-// launch. Instantiated for f16 (lora_f16.cu) and bf16 (lora_bf16.cu).
+// launch. This file has the kernel for few rows, lora_many.cuh the one for many; instantiated for f16 (lora_f16.cu) and
+// bf16 (lora_bf16.cu).
 //
-// A cluster of thread blocks takes up to 16 WM rows of one adapter. Its blocks share K in the first product
-// (H = X A^T, R values a row), join their parts of H in distributed shared memory, each in the same order, and share
-// N in the second one (H B^T), so neither product needs scratch memory or a second launch. A call moves the rows of
-// X and Y once and each adapter once for every 16 WM of its rows; with R values between two wide sides there are few
-// operations to a byte, so the bytes bound long batches, and a chain of round trips to memory the short ones.
+// A cluster of thread blocks takes up to 16 rows of one adapter. Its blocks share K in the first product (H = X A^T,
+// R values a row), join their parts of H in distributed shared memory, each in the same order, and share N in the
+// second one (H B^T), so neither product needs scratch memory or a second launch. What bounds it is a chain of round
+// trips: the offsets, the rows' numbers, the first product's operands, the join, the store. 16 rows of 16 adapters,
+// 4096 x 4096 at rank 16: 5.9 us in a graph (the same with next to no K and N: 4.3); 77 rows of 24 adapters of ranks up
+// to 64, 9728 x 2560, float32 Y: 16 us.
 //
 // Both products run on 16x8x16 tensor-core steps from registers, without a copy through shared memory: the order of
 // the summed index is free as long as both operands keep to it, so a lane takes 16 neighbouring bytes of a row as its
@@ -28,8 +30,9 @@ constexpr int kMaxR = 256;
 
 struct Params {
     LoraArgs a;
-    int terms;
 };
+// 16-bit terms that stand for a value of H
+constexpr int terms_of(bool bf, int y_dtype) { return bf && y_dtype == DT_F32 ? 3 : 2; }
 
 // 16 x 8 += 16 x 16 * 16 x 8
 template <bool BF>
@@ -42,6 +45,18 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, 
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+// 16 x 8 = 16 x 16 * 16 x 8
+template <bool BF>
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    if constexpr (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
 }
 // The 16-bit value nearest to x, as bits; x becomes what is left of it (0 where the value is infinite or NaN).
 template <bool BF>
@@ -59,6 +74,86 @@ __device__ __forceinline__ uint32_t take_term(float& x) {
     }
     x = fabsf(y) < __uint_as_float(0x7F800000u) ? x - y : 0.f;
     return bits;
+}
+
+// f16 terms are of H over the power of two of the row's largest |H| (its bits): this is that power.
+__device__ __forceinline__ float row_unit(uint32_t top) {
+    const uint32_t e = top >> 23;
+    return e == 255u ? 1.f : __uint_as_float(min(max(e, 1u), 253u) << 23);
+}
+__device__ __forceinline__ float row_unit_inverse(uint32_t top) {
+    const uint32_t e = top >> 23;
+    return e == 255u ? 1.f : __uint_as_float((254u - min(max(e, 1u), 253u)) << 23);
+}
+
+// H of all of K from the blocks' parts h, added in rank order: [rows][pitch], 16 * chunks columns; top: the bits of each
+// row's largest |H| (f16; cleared before). Every thread of the block calls it.
+template <bool BF>
+__device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top, int pitch, int rows, int chunks, int blocks) {
+    const int width = chunks * 4;
+    for (int i = threadIdx.x; i < rows * width; i += kThreads) {
+        const int row = i / width, at = row * pitch + i % width * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (blocks > 1) {
+            for (int k0 = 0; k0 < blocks; k0 += 4) {
+                float4 o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k0 + k < blocks) o[k] = ld_cluster_f32x4(in_block(h + at, k0 + k));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k0 + k < blocks) {
+                        v.x += o[k].x; v.y += o[k].y; v.z += o[k].z; v.w += o[k].w;
+                    }
+            }
+        } else {
+            v = *reinterpret_cast<const float4*>(h + at);
+        }
+        *reinterpret_cast<float4*>(sum + at) = v;
+        if constexpr (!BF) {
+            const float t = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+            atomicMax(top + row, __float_as_uint(t));
+        }
+    }
+}
+// H's 16-bit terms, in the order in which the lanes take them: frag [tiles of 16 rows][chunks][terms][32].
+template <bool BF, int TERMS>
+__device__ __forceinline__ void make_terms(const float* sum, const uint32_t* top, uint4* frag, int pitch, int tiles, int chunks) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    for (int f = warp; f < tiles * chunks; f += kWarps) {
+        float v[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = f / chunks * 16 + g + 8 * i;
+            const float4 o = *reinterpret_cast<const float4*>(sum + row * pitch + f % chunks * 16 + q * 4);
+            const float by = BF ? 1.f : row_unit_inverse(top[row]);
+            v[i][0] = o.x * by; v[i][1] = o.y * by; v[i][2] = o.z * by; v[i][3] = o.w * by;
+        }
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+            uint32_t w[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t lo = take_term<BF>(v[i][2 * k]), hi = take_term<BF>(v[i][2 * k + 1]);
+                    w[i][k] = lo | hi << 16;
+                }
+            frag[(f * TERMS + t) * 32 + lane] = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
+        }
+    }
+}
+// y[k] += scale * d[k] for the first `n` of 8 values, one at a time.
+template <int YDT>
+__device__ __forceinline__ void add_edge(void* y, const float (&d)[8], float scale, int n) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k >= n) break;
+        const float v = fmaf(scale, d[k], load_as_float<YDT>(y, k));
+        if constexpr (YDT == DT_F32) static_cast<float*>(y)[k] = v;
+        else if constexpr (YDT == DT_F16) static_cast<__half*>(y)[k] = __float2half_rn(v);
+        else static_cast<__nv_bfloat16*>(y)[k] = __float2bfloat16_rn(v);
+    }
 }
 
 // The q-th tile of `rows` rows over the adapters: its adapter, first position in `row`, and rows. Every warp looks by
@@ -101,15 +196,15 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& a, int q, int rows, in
 }
 
 // Sixteen ranks at a time are a chunk; JT of them are in registers together.
-template <int JT, int WM>
+template <int JT>
 struct Shape {
-    static constexpr int kRows = 16 * WM, kWK = kWarps / WM;
+    static constexpr int kRows = 16, kWK = kWarps;    // warps along K, and later along N
     static constexpr int kRC = 16 * JT;               // ranks of a pass over K
     static constexpr int kPartPitch = kRC + 8;        // floats; 8 mod 32 spreads 4 rows' pairs over all banks
     static constexpr int kStep = JT <= 2 ? 64 : 32;   // of K at a time
     __host__ __device__ static int ranks(int R) { return (R + 15) / 16 * 16; }
     static size_t smem(int R, int terms) {
-        return shared_floats(R) * 4 + (size_t)kRows * (ranks(R) + 8) * 4 + (size_t)WM * (ranks(R) / 16) * terms * 512 + kRows * 4;
+        return shared_floats(R) * 4 + (size_t)kRows * (ranks(R) + 8) * 4 + (size_t)(ranks(R) / 16) * terms * 512 + kRows * 4;
     }
     // the warps' parts of H, and later, when those have been added up, H of all of K
     __host__ __device__ static int shared_floats(int R) {
@@ -118,21 +213,21 @@ struct Shape {
     }
 };
 
-template <bool BF, int YDT, int JT, int WM>
+template <bool BF, int YDT, int JT>
 __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
-    using S = Shape<JT, WM>;
-    constexpr int kNT = 2 * JT, kXV = S::kStep / 32;
+    using S = Shape<JT>;
+    constexpr int kNT = 2 * JT, kXV = S::kStep / 32, kTerms = terms_of(BF, YDT);
     extern __shared__ __align__(16) uint8_t smem[];
     const LoraArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-    const int wm = warp % WM, wk = warp / WM;
+    const int wk = warp;
     const int blocks = (int)cluster_size(), rank_in = blocks > 1 ? (int)cluster_rank() : 0;
     const int pitch = S::ranks(a.R) + 8;
     float* part = reinterpret_cast<float*>(smem);                           // [kWK][kRows][kPartPitch]
     float* sum = part;                                                      // [kRows][pitch], all of K
     float* h = part + S::shared_floats(a.R);                                // [kRows][pitch], this block's part of K
-    uint4* frag = reinterpret_cast<uint4*>(h + S::kRows * pitch);           // [WM][ranks / 16][terms][32]
-    uint32_t* top = reinterpret_cast<uint32_t*>(frag + WM * (S::ranks(a.R) / 16) * p.terms * 32);   // [kRows]
+    uint4* frag = reinterpret_cast<uint4*>(h + S::kRows * pitch);           // [ranks / 16][terms][32]
+    uint32_t* top = reinterpret_cast<uint32_t*>(frag + (S::ranks(a.R) / 16) * kTerms * 32);   // [kRows]
     grid_wait();
     grid_release();
     int l, from, count;
@@ -145,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     int m[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int at = wm * 16 + g + 8 * i;
+        const int at = g + 8 * i;
         m[i] = at < count ? load(a.row + from + at) : -1;
         if (m[i] >= a.M) m[i] = -1;
     }
@@ -170,11 +265,11 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
 #pragma unroll
                 for (int v = 0; v < kXV; ++v) {
                     const size_t k = (size_t)s * S::kStep + v * 32 + q * 8;
-                    x[0][v] = m[0] >= 0 ? load(reinterpret_cast<const uint4*>(x0 + k)) : zero;
-                    x[1][v] = m[1] >= 0 ? load(reinterpret_cast<const uint4*>(x1 + k)) : zero;
 #pragma unroll
                     for (int n = 0; n < kNT; ++n)
                         w[n][v] = r0 + n * 8 + g < rank ? load(reinterpret_cast<const uint4*>(A + (size_t)n * 8 * a.K + k)) : zero;
+                    x[0][v] = m[0] >= 0 ? load(reinterpret_cast<const uint4*>(x0 + k)) : zero;
+                    x[1][v] = m[1] >= 0 ? load(reinterpret_cast<const uint4*>(x1 + k)) : zero;
                 }
             };
             if (s0 + wk < s1) fetch(s0 + wk);
@@ -197,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
                     }
             }
             if (r0 > 0) __syncthreads();        // the pass before has been read
-            float* mine = part + (wk * S::kRows + wm * 16 + g) * S::kPartPitch + 2 * q;
+            float* mine = part + (wk * S::kRows + g) * S::kPartPitch + 2 * q;
 #pragma unroll
             for (int n = 0; n < kNT; ++n) {
                 *reinterpret_cast<float2*>(mine + n * 8) = make_float2(acc[n][0], acc[n][1]);
@@ -257,67 +352,16 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     // ---- H of all of K, in the same order in every block, and its terms
     if (blocks > 1) cluster_sync();
     else __syncthreads();
-    {
-        const int width = chunks * 4;
-        for (int i = tid; i < S::kRows * width; i += kThreads) {
-            const int row = i / width, c = i % width * 4;
-            float4 v = *reinterpret_cast<const float4*>(h + row * pitch + c);
-            if (blocks > 1) {
-                v = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k = 0; k < blocks; ++k) {
-                    const float4 o = ld_cluster_f32x4(in_block(h + row * pitch + c, k));
-                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-                }
-            }
-            *reinterpret_cast<float4*>(sum + row * pitch + c) = v;
-            if constexpr (!BF) {
-                const float t = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-                atomicMax(top + row, __float_as_uint(t));
-            }
-        }
-    }
+    join_h<BF>(h, sum, top, pitch, S::kRows, chunks, blocks);
     if (blocks > 1) cluster_arrive();       // waited for at the end
     __syncthreads();
-    for (int f = warp; f < WM * chunks; f += kWarps) {
-        const int tile = f / chunks, j = f % chunks;
-        float v[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = tile * 16 + g + 8 * i;
-            const float4 o = *reinterpret_cast<const float4*>(sum + row * pitch + j * 16 + q * 4);
-            v[i][0] = o.x; v[i][1] = o.y; v[i][2] = o.z; v[i][3] = o.w;
-            if constexpr (!BF) {
-                const uint32_t e = min(max(top[row] >> 23, 1u), 253u);
-                const float mul = top[row] >> 23 == 255u ? 1.f : __uint_as_float((254u - e) << 23);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[i][k] *= mul;
-            }
-        }
-        for (int t = 0; t < p.terms; ++t) {
-            uint32_t w[2][2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t lo = take_term<BF>(v[i][2 * k]), hi = take_term<BF>(v[i][2 * k + 1]);
-                    w[i][k] = lo | hi << 16;
-                }
-            frag[((tile * chunks + j) * p.terms + t) * 32 + lane] = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
-        }
-    }
+    make_terms<BF, kTerms>(sum, top, frag, pitch, 1, chunks);
     __syncthreads();
 
     // ---- Y += scale H B^T
     float mul[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        mul[i] = scale;
-        if constexpr (!BF) {
-            const uint32_t bits = top[wm * 16 + g + 8 * i], e = min(max(bits >> 23, 1u), 253u);
-            if (bits >> 23 != 255u) mul[i] = __uint_as_float(e << 23);      // (scale follows below)
-            else mul[i] = 1.f;
-        }
-    }
+    for (int i = 0; i < 2; ++i) mul[i] = BF ? 1.f : row_unit(top[g + 8 * i]);
     for (int u = u0 + wk; u < u1; u += S::kWK) {
         float acc[4][4];
 #pragma unroll
@@ -340,8 +384,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
 #pragma unroll
             for (int j = 0; j < JT; ++j) {
                 if (c0 + j >= chunks) break;
-                const uint4* f = frag + (wm * chunks + c0 + j) * p.terms * 32 + lane;
-                for (int k = 0; k < p.terms; ++k) {
+                const uint4* f = frag + (c0 + j) * kTerms * 32 + lane;
+#pragma unroll
+                for (int k = 0; k < kTerms; ++k) {
                     const uint4 w = f[k * 32];
 #pragma unroll
                     for (int t = 0; t < 4; ++t) mma<BF>(acc[t], w, cb[j][t].x, cb[j][t].y);
@@ -357,63 +402,33 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
             for (int t = 0; t < 4; ++t) {
                 d[2 * t] = acc[t][2 * i] * mul[i];
                 d[2 * t + 1] = acc[t][2 * i + 1] * mul[i];
-                if constexpr (!BF) {
-                    d[2 * t] *= scale;
-                    d[2 * t + 1] *= scale;
-                }
             }
-            const size_t at = (size_t)((long long)m[i] * a.ldy) + n;
+            uint8_t* out = static_cast<uint8_t*>(a.Y) + ((long long)m[i] * a.ldy + n) * (YDT == DT_F32 ? 4 : 2);
             if (wide && n + 8 <= a.N) {
                 float v[8];
                 cy[i].values(v);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] += d[k];
+                for (int k = 0; k < 8; ++k) v[k] = fmaf(scale, d[k], v[k]);
                 cy[i].round_from(v);
-                cy[i].store(a.Y, at);
+                cy[i].store(out, 0);
             } else {
-                for (int k = 0; k < 8 && n + k < a.N; ++k) {
-                    float v = load_as_float<YDT>(a.Y, at + k);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v += j == k ? d[j] : 0.f;
-                    if constexpr (YDT == DT_F32) static_cast<float*>(a.Y)[at + k] = v;
-                    else if constexpr (YDT == DT_F16) static_cast<__half*>(a.Y)[at + k] = __float2half_rn(v);
-                    else static_cast<__nv_bfloat16*>(a.Y)[at + k] = __float2bfloat16_rn(v);
-                }
+                add_edge<YDT>(out, d, scale, a.N - n);
             }
         }
     }
     if (blocks > 1) cluster_wait();         // no block leaves while its H is read
 }
 
-template <bool BF, int YDT, int JT, int WM>
+template <bool BF, int YDT, int JT>
 cudaError_t launch(const LoraArgs& a, int blocks, cudaStream_t s) {
-    const Params p{a, BF && YDT == DT_F32 ? 3 : 2};
-    const size_t smem = Shape<JT, WM>::smem(a.R, p.terms);
-    auto kern = lora_kernel<BF, YDT, JT, WM>;
+    const Params p{a};
+    const size_t smem = Shape<JT>::smem(a.R, terms_of(BF, YDT));
+    auto kern = lora_kernel<BF, YDT, JT>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // at most one tile that is not full for each adapter that has rows
-    const long long tiles = (long long)a.M / Shape<JT, WM>::kRows + (a.L < a.M ? a.L : a.M);
+    const long long tiles = (long long)a.M / Shape<JT>::kRows + (a.L < a.M ? a.L : a.M);
     return launch_behind(kern, dim3((unsigned)(tiles * blocks)), dim3(kThreads), smem, (unsigned)blocks, s, p);
-}
-
-template <bool BF, int YDT>
-cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
-    const bool many = a.M >= 1024;
-    const int blocks = many ? 2 : 8;
-    if (a.R <= 16) return many ? launch<BF, YDT, 1, 4>(a, blocks, s) : launch<BF, YDT, 1, 1>(a, blocks, s);
-    if (a.R <= 32) return many ? launch<BF, YDT, 2, 4>(a, blocks, s) : launch<BF, YDT, 2, 1>(a, blocks, s);
-    if (a.R > 128 && many) return launch<BF, YDT, 4, 2>(a, blocks, s);       // (64 rows of H and its terms exceed shared memory)
-    return many ? launch<BF, YDT, 4, 4>(a, blocks, s) : launch<BF, YDT, 4, 1>(a, blocks, s);
-}
-
-template <bool BF>
-cudaError_t launch_form(const LoraArgs& a, int y_dtype, cudaStream_t s) {
-    switch (y_dtype) {
-        case DT_F32: return launch_y<BF, DT_F32>(a, s);
-        case DT_F16: return launch_y<BF, DT_F16>(a, s);
-        default: return launch_y<BF, DT_BF16>(a, s);
-    }
 }
 
 }  // namespace lora

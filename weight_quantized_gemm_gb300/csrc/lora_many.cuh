@@ -1,0 +1,508 @@
+// The adapters' products for batches of many rows, on the tensor cores' asynchronous path (lora.cuh has the few rows, and
+// the mathematics): Y[m] += scale_l B_l (A_l X[m]), a cluster of blocks to a tile of 128 rows of one adapter.
+//
+//   first product   D1 = X A^T (128 x RP) in tensor memory, a ring of stages of 64 of K (rows of 128 bytes in the
+//                   128-byte swizzle) filled by asynchronous copies of all threads, since the rows of a tile lie
+//                   anywhere in X. The cluster's blocks share K;
+//   join            each block adds 128 / C rows of the blocks' parts, in rank order, splits them into 16-bit terms and
+//                   writes these, as the second product's operand, into every block's shared memory;
+//   second product  D2 = H B^T, 64 columns a turn (32 for float32 Y) in two buffers of tensor memory: while the tensor cores work on a turn,
+//                   all warps add the one before to Y. Y passes through shared memory, copied in and stored by whole
+//                   128-byte runs. The blocks share N.
+// RP: the ranks rounded up to a power of two; what lies past an adapter's rank is filled with zeros.
+//
+// There are few operations to a byte, so HBM's bytes are the floor: X, Y and Y again. The products were first on
+// 16x8x16 steps from registers, as in lora.cuh: 8192 x 4096 x 14336 at rank 16 took 109 us with 12 instructions a value
+// of Y, and 4099 x 2560 x 2560 at rank 128 61 us, for the loads that feed such steps.
+//
+// Every wait is bounded (see ptx.cuh). After a wait that ran out the blocks still meet at the cluster's barriers, wait
+// for the MMAs in flight and release their tensor memory.
+#pragma once
+
+#include "group_gemm.cuh"
+#include "lora.cuh"
+
+namespace qg {
+namespace lora {
+
+constexpr int kManyRows = 128;
+constexpr int kMaxBlocks = 8;           // of a cluster
+
+template <int YDT, int RP, int TERMS>
+struct Many {
+    static constexpr int kYSize = YDT == DT_F32 ? 4 : 2;
+    static constexpr int kCols = 128 / kYSize;                                         // of a turn: 128 bytes of a row of Y
+    static constexpr int kX = kManyRows * 128, kStage = kX + RP * 128;                  // a stage: X's rows, A's ranks
+    static constexpr int kBPitch = RP < 64 ? RP * 2 : 128, kBAtoms = (RP + 63) / 64;    // bytes of a column of B, 64 ranks at a time
+    static constexpr int kY = kManyRows * 128, kB = kBAtoms * kCols * kBPitch, kTurn = kY + kB;
+    static constexpr int kHAtoms = (TERMS * RP + 63) / 64, kH = kHAtoms * kManyRows * 128;
+    static constexpr int kRoom = (RP <= 64 ? 112 << 10 : 225 << 10) - kH - 2048;        // two blocks an SM where they fit
+    static constexpr int kTurns = kRoom / kTurn < 5 ? kRoom / kTurn : 5;                // ring of turns
+    static constexpr int kStages = kTurns * kTurn / kStage < 5 ? kTurns * kTurn / kStage : 5;
+    // the first product's stages go to kSums accumulators in turn: the tensor cores cut sums off, and shorter chains lose less
+    static constexpr int kSums = RP <= 64 ? 128 / RP : 2, kD2 = kSums * RP, kTmem = RP <= 64 ? 256 : 512;
+    static constexpr int kPartPitch = RP + 4;                                          // floats: 16-byte writes of 8 rows meet no bank twice
+    static constexpr int kRing = kTurns * kTurn;
+    static constexpr size_t kSmem = 1024 + kRing + kH;
+    static_assert(kTurns >= 3 && kStages >= 2 && kTurn % 1024 == 0 && kStage % 1024 == 0, "rings");
+    static_assert(kManyRows * kPartPitch * 4 <= (kTurns - 1) * kTurn, "the parts of H take the ring's place but for one turn's");
+    static_assert(3 * kSmem > (228 << 10), "at most two blocks an SM, whose tensor memory is there");
+};
+
+struct ManyParams {
+    LoraArgs a;
+    unsigned int* status;
+    long long wait_ns;
+    int stall;
+};
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool any) {     // zeros where there is nothing to copy
+    const int bytes = any ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 read16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void write16(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Shared memory written by threads, of this block or another of the cluster, before the tensor cores read it.
+__device__ __forceinline__ void to_tensor_cores() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// Where 16-byte piece c of row r is, rows of PITCH bytes in the swizzle of that width: the piece's number is combined
+// with the bits of the address three places above it.
+template <int PITCH>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+    constexpr int kShift = PITCH == 128 ? 0 : (PITCH == 64 ? 1 : 2);
+    return r * PITCH + ((c ^ ((r >> kShift) & (PITCH / 16 - 1))) << 4);
+}
+// The high word of such rows' matrix descriptor (K-major, eight rows 8 PITCH bytes apart; swizzles of 128, 64 and 32
+// bytes are numbers 2, 4 and 6).
+template <int PITCH>
+constexpr uint32_t kDescHi = (8u * PITCH >> 4) | (1u << 14) | ((PITCH == 128 ? 2u : (PITCH == 64 ? 4u : 6u)) << 29);
+// D (+)= A B^T over 16 of K, issued by one lane of the (whole) warp: A's rows of 128 bytes, B's of PITCH. a, b: the
+// descriptors' low words.
+template <int PITCH>
+__device__ __forceinline__ void mma_async(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %6};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kDescHi<128>), "n"(kDescHi<PITCH>)
+        : "memory");
+}
+
+template <bool BF, int YDT, int RP>
+__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(const ManyParams p) {
+    constexpr int kTerms = terms_of(BF, YDT);
+    using S = Many<YDT, RP, kTerms>;
+    constexpr int kYSize = S::kYSize, kTurnCols = S::kCols, kHalf = kTurnCols / 2;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) unsigned long long s_bar[S::kStages + 3];      // stages, the two buffers of D2, one that never completes
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    __shared__ int s_row[kManyRows];
+    __shared__ float s_unit[kManyRows];         // f16: the power of two that a row of H was divided by
+    const LoraArgs& a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int blocks = (int)cluster_size(), rank_in = blocks > 1 ? (int)cluster_rank() : 0;
+    const uint32_t ring = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;       // (the same offset in every block)
+    const uint32_t H = ring + S::kRing;
+    const uint32_t bar = ptx::smem_u32(s_bar);
+    volatile int* abort_flag = &s_abort;
+    if (tid == 0) {
+#pragma unroll
+        for (int i = 0; i < S::kStages + 3; ++i) ptx::mbar_init(bar + 8 * i, 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        // (before the next kernel may come up, and at most two blocks an SM: the columns are free, or will be)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_u32(&s_tmem)), "r"(S::kTmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    gg::tc_fence_before();
+    __syncthreads();
+    gg::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    grid_wait();
+    grid_release();
+    int l = 0, from = 0, count = 0;
+    const bool any = find_tile(a, blockIdx.x / blocks, kManyRows, l, from, count);
+    const int rank = !any ? 0 : (a.rank ? min(max(load(a.rank + l), 0), a.R) : a.R);
+    if (rank > 0) {             // (the same for the whole cluster)
+        const float scale = a.scale ? load(a.scale + l) : 1.f;
+        if (tid < kManyRows) {
+            const int m = tid < count ? load(a.row + from + tid) : -1;
+            s_row[tid] = m < a.M ? m : -1;
+            s_unit[tid] = 1.f;
+        }
+        __syncthreads();
+        bool fail = false;
+        auto wait = [&](int i, uint32_t parity) { return ptx::mbar_wait(bar + 8 * i, parity, abort_flag, p.status, p.wait_ns); };
+        if (p.stall) fail = !wait(S::kStages + 2, 0);
+        const int c8 = tid & 7, r8 = tid >> 3;      // 8 threads copy a row's 128 bytes, 32 rows at a time
+
+        // ---- D1 = X A^T over this block's part of K
+        const int steps = a.K / 64;
+        const int s0 = (int)((long long)steps * rank_in / blocks), n1 = (int)((long long)steps * (rank_in + 1) / blocks) - s0;
+        {
+            constexpr int kXC = kManyRows / 32, kAC = (RP + 31) / 32;
+            const uint8_t* x[kXC];
+            uint32_t live = 0;
+#pragma unroll
+            for (int i = 0; i < kXC; ++i) {
+                const int m = s_row[r8 + 32 * i];
+                live |= (m >= 0 ? 1u : 0u) << i;
+                x[i] = static_cast<const uint8_t*>(a.X) + ((long long)max(m, 0) * a.ldx + (size_t)s0 * 64 + c8 * 8) * 2;
+            }
+            const uint8_t* A = static_cast<const uint8_t*>(a.A) + (((size_t)l * a.R + r8) * a.K + (size_t)s0 * 64 + c8 * 8) * 2;
+            const uint32_t to = ring + swizzled<128>(r8, c8);        // (rows 32 apart have the same swizzle)
+            auto fetch = [&](int i, int slot) {
+                if (i < n1) {
+                    const uint32_t at = to + slot * S::kStage;
+#pragma unroll
+                    for (int j = 0; j < kXC; ++j) copy16(at + j * 32 * 128, x[j] + (size_t)i * 128, live >> j & 1u);
+#pragma unroll
+                    for (int j = 0; j < kAC; ++j)
+                        if (RP >= 32 || r8 < RP) {
+                            const bool in = r8 + 32 * j < rank;
+                            copy16(at + S::kX + j * 32 * 128, in ? A + ((size_t)j * 32 * a.K + (size_t)i * 64) * 2 : a.A, in);
+                        }
+                }
+                copies_end();
+            };
+            const uint32_t idesc = gg::inst_desc<gg::HALF>(kManyRows, RP, BF);
+#pragma unroll
+            for (int d = 0; d < S::kStages - 1; ++d) fetch(d, d);
+            int slot = 0, before = S::kStages - 1;
+            uint32_t parity = 1;        // of the slot before this one
+            for (int i = 0; i < n1; ++i) {
+                copies_wait<S::kStages - 2>();
+                ptx::fence_proxy_async_smem();
+                if (__syncthreads_or(fail)) {
+                    fail = true;
+                    break;
+                }
+                if (warp == 0) {
+                    gg::tc_fence_after();
+                    const uint32_t at = ring + slot * S::kStage;
+                    uint32_t xa = gg::rows_lo(at), wa = gg::rows_lo(at + S::kX);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_async<128>(tmem + i % S::kSums * RP, xa + 2 * k, wa + 2 * k, idesc, i >= S::kSums || k > 0);
+                    gg::mma_commit<gg::SOLO>(bar + 8 * slot);
+                }
+                if (i > 0) fail = fail || !wait(before, parity);       // the stage before has been read
+                fetch(i + S::kStages - 1, before);
+                before = slot;
+                if (++slot == S::kStages) slot = 0;
+                parity = (uint32_t)(i / S::kStages) & 1u;
+            }
+            // MMAs in flight end before anything else happens to what they read and write
+            copies_wait<0>();
+            if (n1 > 0 && !fail) fail = !wait(before, parity);
+            fail = __syncthreads_or(fail);
+        }
+
+        // ---- the second product's first turn comes while the blocks join their parts of H (behind which it has room)
+        const int turns = (a.N + kTurnCols - 1) / kTurnCols;
+        const int t0 = (int)((long long)turns * rank_in / blocks), n2 = (int)((long long)turns * (rank_in + 1) / blocks) - t0;
+        const bool wide = a.ldy % (16 / kYSize) == 0;
+        constexpr int kPer = 16 / kYSize, kYC = kManyRows / 32;        // values of a 16-byte piece; pieces of a thread
+        const uint32_t y_to = swizzled<128>(r8, c8);
+        // A turn is whole where all of its columns are there and rows of Y start 16-byte aligned. This thread's pieces of the
+        // turn that is stored; those of the turn that is fetched lie kAhead turns further on. Rows that are not there
+        // have nothing to copy (`full`: none is missing).
+        constexpr int kAhead = S::kTurns - 1, kTurnBytes = kTurnCols * kYSize;
+        uint8_t* y_at[kYC];
+        uint32_t there = 0;
+#pragma unroll
+        for (int i = 0; i < kYC; ++i) {
+            const int m = s_row[r8 + 32 * i];
+            there |= (m >= 0 ? 1u : 0u) << i;
+            y_at[i] = static_cast<uint8_t*>(a.Y) + ((long long)max(m, 0) * a.ldy + (size_t)t0 * kTurnCols + c8 * kPer) * kYSize;
+        }
+        if (!wide) there = 0;
+        const bool full = there == (1u << kYC) - 1;
+        auto whole = [&](int u) { return (t0 + u + 1) * kTurnCols <= a.N; };
+        // (8 columns belong together: they are copied, or at the row's end added one by one)
+        auto copied = [&](int u) { return whole(u) || (t0 + u) * kTurnCols + (c8 * kPer / 8 + 1) * 8 <= a.N; };
+        constexpr int kBPieces = (RP < 64 ? RP : 64) / 8 * S::kBAtoms;      // 16-byte pieces of a column of B
+        constexpr int kBC = (kTurnCols * kBPieces + kThreads - 1) / kThreads, kBApart = kThreads / kBPieces;
+        const int bn = tid / kBPieces, bc = tid % kBPieces;
+        const uint8_t* b_at = static_cast<const uint8_t*>(a.B) + (((size_t)l * a.N + (size_t)t0 * kTurnCols + bn) * a.R + bc * 8) * 2;
+        const uint32_t b_to = S::kY + (bc >> 3) * (kTurnCols * S::kBPitch) + swizzled<S::kBPitch>(bn, bc & 7);     // (kBApart is a multiple of 8)
+        static_assert(kBApart % 8 == 0, "columns a thread copies have one order of pieces");
+        const int b_bytes = min(max(rank - bc * 8, 0), 8) * 2;              // a piece's values past the adapter's rank become zeros
+        // fetches turn u; y_at is kAhead - `back` turns before it
+        auto fetch = [&](int u, int slot, int back) {
+            if (u < n2) {
+                const uint32_t at = ring + slot * S::kTurn;
+                if (copied(u)) {
+#pragma unroll
+                    for (int i = 0; i < kYC; ++i)
+                        if (full || (there >> i & 1u)) copy16(at + y_to + i * 32 * 128, y_at[i] + (kAhead - back) * kTurnBytes, true);
+                }
+#pragma unroll
+                for (int i = 0; i < kBC; ++i) {
+                    const int n = bn + i * kBApart;
+                    if (kTurnCols * kBPieces % kThreads != 0 && n >= kTurnCols) break;
+                    const int bytes = whole(u) || (t0 + u) * kTurnCols + n < a.N ? b_bytes : 0;
+                    const uint8_t* src = bytes ? b_at + ((size_t)u * kTurnCols + i * kBApart) * a.R * 2 : static_cast<const uint8_t*>(a.B);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + b_to + i * kBApart * S::kBPitch), "l"(src), "r"(bytes) : "memory");
+                }
+            }
+            copies_end();
+        };
+        const uint32_t idesc = gg::inst_desc<gg::HALF>(kManyRows, kTurnCols, BF);
+        if (!fail) fetch(0, S::kTurns - 1, kAhead);
+
+        // ---- the block's part of H, where the stages were
+        float* part = reinterpret_cast<float*>(smem_raw + (ring - ptx::smem_u32(smem_raw)));      // [128][kPartPitch]
+        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;      // a warp reads its quarter's lanes
+        const uint32_t lanes = tmem + ((uint32_t)quarter * 32 << 16);
+        gg::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < RP; c += 32) {
+            float v[16];
+            if (c + half * 16 < RP) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                for (int d = 0; d < min(n1, S::kSums); ++d) {
+                    float w[16];
+                    gg::tmem_ld(lanes + d * RP + c + half * 16, w);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] += w[j];
+                }
+                float4* to = reinterpret_cast<float4*>(part + row * S::kPartPitch + c + half * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+        }
+        gg::tc_fence_before();
+        if (blocks > 1) cluster_sync();
+        else __syncthreads();
+
+        // ---- this block's share of the rows: summed, and their terms to every block
+        {
+            constexpr int kLanes = RP / 4;      // of a row, 4 values each
+            const int rows = kManyRows / blocks;
+            for (int i = tid; i < rows * kLanes; i += kThreads) {
+                const int r = rank_in * rows + i / kLanes, c = i % kLanes * 4;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int b0 = 0; b0 < blocks; b0 += 4) {
+                    float4 o[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if (b0 + b < blocks) o[b] = ld_cluster_f32x4(in_block(part + r * S::kPartPitch + c, b0 + b));
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if (b0 + b < blocks) {
+                            v.x += o[b].x; v.y += o[b].y; v.z += o[b].z; v.w += o[b].w;
+                        }
+                }
+                float x[4] = {v.x, v.y, v.z, v.w};
+                if constexpr (!BF) {
+                    float t = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+#pragma unroll
+                    for (int o = 1; o < kLanes; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));      // (whole warps are in the loop)
+                    const uint32_t bits = __float_as_uint(t);
+                    const float by = row_unit_inverse(bits);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] *= by;
+                    if (c == 0)
+                        for (int b = 0; b < blocks; ++b)
+                            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_block(&s_unit[r], b)), "f"(row_unit(bits)) : "memory");
+                }
+#pragma unroll
+                for (int t = 0; t < kTerms; ++t) {
+                    uint32_t w[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t lo = take_term<BF>(x[2 * k]), hi = take_term<BF>(x[2 * k + 1]);
+                        w[k] = lo | hi << 16;
+                    }
+                    const int col = t * RP + c;
+                    const uint32_t at = H + (col >> 6) * (kManyRows * 128) + swizzled<128>(r, (col & 63) >> 3) + (col & 7) * 2;
+                    for (int b = 0; b < blocks; ++b) {
+                        uint32_t to;
+                        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(b));
+                        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(w[0]), "r"(w[1]) : "memory");
+                    }
+                }
+            }
+        }
+        to_tensor_cores();
+        if (blocks > 1) cluster_sync_all();     // (from here on no block reads another's shared memory)
+        else __syncthreads();
+        to_tensor_cores();
+
+        // ---- Y += scale H B^T, a turn's columns at a time
+        const int chunks = (rank + 15) / 16;
+        const float by = scale * s_unit[row];       // exact: a power of two
+        const int my_row = s_row[row];
+        const uint32_t y_cell = swizzled<128>(row, 0);      // (a row's pieces differ in the same three bits)
+#pragma unroll
+        for (int d = 1; d < S::kTurns - 2; ++d) fetch(d, d - 1, kAhead - d);
+        int slot = S::kTurns - 1, before = S::kTurns - 2, next = S::kTurns - 3;        // this turn's, the last turn's, and the one to fill
+        // one turn more than there are: each adds the turn before to Y
+        for (int u = 0; u <= n2 && n2 > 0; ++u) {
+            copies_wait<S::kTurns - 3>();
+            ptx::fence_proxy_async_smem();
+            gg::tc_fence_before();
+            if (__syncthreads_or(fail)) {       // this turn is in; the one before the last is stored, and its accumulator read
+                fail = true;
+                break;
+            }
+            if (warp == 0 && u < n2) {
+                gg::tc_fence_after();
+                const uint32_t d = tmem + S::kD2 + (u & 1) * kTurnCols, bt = ring + slot * S::kTurn + S::kY;
+                for (int t = 0; t < kTerms; ++t)
+                    for (int k = 0; k < chunks; ++k) {
+                        const int col = t * RP + k * 16;
+                        const uint32_t ha = gg::rows_lo(H + (col >> 6) * (kManyRows * 128)) + ((col & 63) >> 3);
+                        const uint32_t ba = gg::rows_lo(bt + (k >> 2) * (kTurnCols * 128)) + 2 * (k & 3);
+                        mma_async<S::kBPitch>(d, ha, ba, idesc, t > 0 || k > 0);
+                    }
+                gg::mma_commit<gg::SOLO>(bar + 8 * (S::kStages + (u & 1)));
+            }
+            fetch(u + S::kTurns - 2, next, u > 0 ? 0 : 1);
+            if (u > 0) {
+                const int v = u - 1, n = (t0 + v) * kTurnCols + half * kHalf;
+                const uint32_t tile = ring + before * S::kTurn;
+                fail = fail || !wait(S::kStages + (v & 1), (uint32_t)(v >> 1) & 1u);
+                gg::tc_fence_after();
+                float acc[kHalf];
+                gg::tmem_ld(lanes + S::kD2 + (v & 1) * kTurnCols + half * kHalf, acc);
+                constexpr int kV = Eight<YDT>::kVecs;
+                // (what rows that are not there hold in shared memory goes nowhere; all is read before the first is written,
+                // as the compiler keeps the order of these accesses)
+                Eight<YDT> y[kHalf / 8];
+                const bool fast = wide && whole(v);
+#pragma unroll
+                for (int j = 0; j < kHalf / 8; ++j)
+                    if (fast || (wide && n + 8 * j + 8 <= a.N))
+#pragma unroll
+                        for (int k = 0; k < kV; ++k) y[j].v[k] = read16(tile + (y_cell ^ ((half * 4 + j * kV + k) << 4)));
+#pragma unroll
+                for (int j = 0; j < kHalf / 8; ++j) {
+                    if (fast || (wide && n + 8 * j + 8 <= a.N)) {
+                        float x[8];
+                        y[j].values(x);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = fmaf(by, acc[8 * j + k], x[k]);
+                        y[j].round_from(x);
+#pragma unroll
+                        for (int k = 0; k < kV; ++k) write16(tile + (y_cell ^ ((half * 4 + j * kV + k) << 4)), y[j].v[k]);
+                    } else if (n + 8 * j < a.N && my_row >= 0 && !fail) {
+                        float d[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) d[k] = acc[8 * j + k];
+                        add_edge<YDT>(static_cast<uint8_t*>(a.Y) + ((long long)my_row * a.ldy + n + 8 * j) * kYSize, d, by, a.N - n - 8 * j);
+                    }
+                }
+                if (__syncthreads_or(fail)) {       // the tile is summed
+                    fail = true;
+                    break;
+                }
+                if (copied(v)) {
+                    uint4 out[kYC];
+#pragma unroll
+                    for (int i = 0; i < kYC; ++i) out[i] = read16(tile + y_to + i * 32 * 128);
+#pragma unroll
+                    for (int i = 0; i < kYC; ++i)
+                        if (full || (there >> i & 1u)) *reinterpret_cast<uint4*>(y_at[i]) = out[i];
+                }
+#pragma unroll
+                for (int i = 0; i < kYC; ++i) y_at[i] += kTurnBytes;
+            }
+            before = slot;
+            if (++slot == S::kTurns) slot = 0;
+            if (++next == S::kTurns) next = 0;
+        }
+        copies_wait<0>();
+        if (fail) {
+            // the MMAs issued end before the tensor memory is released: one that reports later than the ones before it
+            volatile int never = 0;
+            __syncthreads();
+            if (warp == 0) {
+                gg::mma_commit<gg::SOLO>(bar + 8 * (S::kStages + 2));
+                ptx::mbar_wait(bar + 8 * (S::kStages + 2), 0, &never, p.status);
+            }
+        }
+    }
+    gg::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        gg::tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem) : "memory");
+    }
+}
+
+template <bool BF, int YDT, int RP>
+cudaError_t launch_many(const LoraArgs& a, int blocks, cudaStream_t s) {
+    using S = Many<YDT, RP, terms_of(BF, YDT)>;
+    const ManyParams p{a, status_word_address(), option_wait_ns(), option_stall()};
+    if (!p.status) return cudaErrorUnknown;
+    auto kern = lora_many_kernel<BF, YDT, RP>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e != cudaSuccess) return e;
+    // at most one tile that is not full for each adapter that has rows
+    const long long tiles = (long long)a.M / kManyRows + (a.L < a.M ? a.L : a.M);
+    return launch_behind(kern, dim3((unsigned)(tiles * blocks)), dim3(kThreads), S::kSmem, (unsigned)blocks, s, p);
+}
+
+// Largest power of two up to 8 of which `tiles` clusters make at most `most` blocks (1 at least).
+inline int blocks_of(long long tiles, int most) {
+    int blocks = 1;
+    while (blocks < 8 && tiles * blocks * 2 <= most) blocks *= 2;
+    return blocks;
+}
+
+template <bool BF, int YDT>
+cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
+    // Tiles of 128 rows where there are many rows; from how many on depends on the rank, as the few rows' kernel reads each
+    // adapter once for every 16 rows (4096 x 14336, us, few / many: rank 16 2048 rows 47 / 52, 2900 rows 69 / 54; rank 32
+    // 1500 rows 46 / 45; rank 64 1024 rows 40 / 49, 1500 rows 70 / 50; rank 128, 2560 x 2560, 512 rows 20 / 19, 1024 rows
+    // 24 / 21, and 4096 x 14336, 512 rows 38 / 55). The cluster's size fills the SMs once (two blocks an SM, one at rank
+    // 128), with the number of tiles guessed from M and L, since the host does not see the offsets: 8192 rows 102 us with 4
+    // blocks, 117 with 8, 142 with 2.
+    const int rank = a.R <= 16 ? 16 : (a.R <= 32 ? 32 : (a.R <= 64 ? 64 : 128));
+    const int from = rank == 16 ? 2304 : (rank == 32 ? 1536 : (rank == 64 ? 1280 : 768));
+    if (a.R <= 128 && a.M >= from) {
+        const int tiles = a.M / kManyRows;
+        const int blocks = blocks_of(tiles + (a.L < tiles ? a.L : tiles), rank == 128 ? kTargetSms : 2 * kTargetSms);
+        switch (rank) {
+            case 16: return launch_many<BF, YDT, 16>(a, blocks, s);
+            case 32: return launch_many<BF, YDT, 32>(a, blocks, s);
+            case 64: return launch_many<BF, YDT, 64>(a, blocks, s);
+            default: return launch_many<BF, YDT, 128>(a, blocks, s);
+        }
+    }
+    // 8 blocks for a few rows (16 rows of 16 adapters 5.9 us; 4 blocks 6.9), fewer where the tiles alone fill the GPU
+    // (1024 rows 25 us with 4, 29 with 8).
+    const int blocks = blocks_of(a.M / 16 + (a.L < a.M ? a.L : a.M) / 2, kTargetSms * 9 / 4);
+    switch (rank) {
+        case 16: return launch<BF, YDT, 1>(a, blocks, s);
+        case 32: return launch<BF, YDT, 2>(a, blocks, s);
+        default: return launch<BF, YDT, 4>(a, blocks, s);
+    }
+}
+
+template <bool BF>
+cudaError_t launch_form(const LoraArgs& a, int y_dtype, cudaStream_t s) {
+    switch (y_dtype) {
+        case DT_F32: return launch_y<BF, DT_F32>(a, s);
+        case DT_F16: return launch_y<BF, DT_F16>(a, s);
+        default: return launch_y<BF, DT_BF16>(a, s);
+    }
+}
+
+}  // namespace lora
+}  // namespace qg

@@ -20,12 +20,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
     return r;
 }
-// Every thread of every block of the cluster arrives and waits; what any of them wrote to shared memory before
-// is seen by all of them after.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// Barriers of the cluster's blocks, each thread arriving and waiting. The plain one orders lifetimes. With
+// cluster_sync what any thread wrote to its own block's shared memory before is seen by all blocks after: its release
+// is restricted to that memory, as one of all memory waits for the thread's loads in flight (a microsecond, where the
+// next step's operands are on the way). cluster_sync_all also covers what was written to other blocks' shared memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
     cluster_arrive();
+    cluster_wait();
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     cluster_wait();
 }
 // Address of the same shared-memory variable in block `rank` of the cluster.
