@@ -11,9 +11,13 @@
 //
 // The k likeliest: each thread keeps its largest value and the place where it found it first. The k best of those
 // (by value, then place) belong to k threads that must hold the row's k best values: any other thread has k
-// values before its own best one. Only those threads' values are read again (from L2), and what is not below
-// the k-th best is put in order by warps, 32 keys at a time. A key is the value's order-preserving bits above the
-// complement of its index, so of equal values the lowest index comes first.
+// values before its own best one. Of these, what is not below the k-th best is read again and put in order; the largest
+// value of each thread's every kUnroll pieces is kept beside, so that few pieces are read (with all of these threads'
+// pieces, from HBM where the rows in flight exceed L2, 4096 rows of 131072 in bf16 took 185 us with k = 5, and 253 with
+// 32). A key is the value's order-preserving bits above the complement of its index, so of
+// equal values the lowest index comes first. The usual row is quick: few runs of pieces reach the k-th best value, ties
+// and all, and few of their values; these are collected and sorted once. Where equal values make them many (a row of
+// zeros), exactly k threads are chosen, and all their values go through the warps' lists 32 at a time.
 //
 // A row is cut into equal runs of 16-byte pieces for the blocks of a cluster where the batch has few rows; their
 // sums and lists meet in the first block through distributed shared memory.
@@ -26,6 +30,8 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kUnroll = 8;                 // 16-byte loads that a thread has in flight
+constexpr int kRuns = 16;                  // largest values that a thread keeps
+constexpr int kQuickRuns = kThreads, kQuickKeys = kThreads;
 constexpr int kMaxCluster = 8;
 static_assert(kMaxCluster <= kWarps, "a warp reads each block's list");
 constexpr float kSlack = 3.f;
@@ -65,11 +71,13 @@ __device__ __forceinline__ float from_key(uint32_t k) {
 }
 
 // ---------------------------------------------------------------- a warp's 32 keys in falling order
-__device__ __forceinline__ Key exchange(Key x, int o, bool larger) {
-    const Key y = __shfl_xor_sync(0xffffffffu, x, o);
+template <class T>
+__device__ __forceinline__ T exchange(T x, int o, bool larger) {
+    const T y = __shfl_xor_sync(0xffffffffu, x, o);
     return (x > y) == larger ? x : y;
 }
-__device__ __forceinline__ Key sorted(Key x, int lane) {
+template <class T>
+__device__ __forceinline__ T sorted(T x, int lane) {
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
@@ -77,15 +85,17 @@ __device__ __forceinline__ Key sorted(Key x, int lane) {
     return x;
 }
 // The 32 largest of two lists in falling order.
-__device__ __forceinline__ Key merged(Key a, Key b, int lane) {
-    const Key y = __shfl_sync(0xffffffffu, b, 31 - lane);
-    Key x = a > y ? a : y;
+template <class T>
+__device__ __forceinline__ T merged(T a, T b, int lane) {
+    const T y = __shfl_sync(0xffffffffu, b, 31 - lane);
+    T x = a > y ? a : y;
 #pragma unroll
     for (int o = 16; o; o >>= 1) x = exchange(x, o, (lane & o) == 0);
     return x;
 }
 // The 32 largest of `count` (a power of two) warps' lists, in warp 0. Every thread of the block calls it.
-__device__ __forceinline__ Key merge_warps(Key key, int count, Key (*lists)[32], int warp, int lane) {
+template <class T>
+__device__ __forceinline__ T merge_warps(T key, int count, T (*lists)[32], int warp, int lane) {
     __syncthreads();
     lists[warp][lane] = key;
     for (int h = count >> 1; h; h >>= 1) {
@@ -201,6 +211,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     constexpr int P = R::kPer;
     __shared__ Key lists[kWarps][32];
     __shared__ Key best[32];            // the block's threads with the largest values, then its largest values
+    __shared__ Key found[kQuickKeys];
+    __shared__ float runs[kRuns][kThreads];        // each thread's, the largest values of its runs of pieces
+    __shared__ int which[kQuickRuns], s_which, s_found;
+    __shared__ uint32_t s_least;
     __shared__ float s_top[kWarps];
     __shared__ float2 s_sums[kWarps];
     __shared__ float4 s_again;          // the sums from differences
@@ -211,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     grid_wait();
     grid_release();
     const R row(a.logits + (long long)t * a.ld_bytes, a.V);
-    const int pieces = row.pieces(), run = (pieces + (int)blocks - 1) / (int)blocks;
-    const int v0 = min((int)rank * run, pieces), v1 = min(v0 + run, pieces);
+    const int pieces = row.pieces(), share = (pieces + (int)blocks - 1) / (int)blocks;
+    const int v0 = min((int)rank * share, pieces), v1 = min(v0 + share, pieces);
 
     // ---- the pass
     float most = neg_inf(), limit = neg_inf(), ref = neg_inf();
@@ -228,12 +242,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
         unpack2(e2, e0, e1);
         return Sums{ref, s0 + s1, e0 + e1};
     };
+    // a run is `per` turns of kUnroll pieces of a thread
+    const int turns = (v1 - v0 + kUnroll * kThreads - 1) / (kUnroll * kThreads), per = (turns + kRuns - 1) / kRuns;
+    float run_most = neg_inf();
     auto take = [&](const uint4& raw, int v) {
         float x[P];
         R::values(raw, x);
         float here = x[0];
 #pragma unroll
         for (int j = 1; j < P; ++j) here = fmaxf(here, x[j]);
+        run_most = fmaxf(run_most, here);
         if (here > most) {
             most = here;
             place = v;
@@ -261,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     // The row's first and last piece may be cut: by themselves, in their place in the order of each thread's pieces.
     const int whole0 = max(v0, row.skip ? 1 : 0), whole1 = min(v1, row.end / P);
     if (tid == 0 && v0 < min(whole0, v1)) take(row.edge(v0), v0);
+    int turn = 0, run = 0;          // turns of the run at hand
     for (int v = v0; v < whole1; v += kUnroll * kThreads) {
         const uint4* from = reinterpret_cast<const uint4*>(row.from) + v + tid;
         uint4 raw[kUnroll];
@@ -280,8 +299,23 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
             for (int u = 0; u < kUnroll; ++u)
                 if (v + u * kThreads < whole1) take(raw[u], v + tid + u * kThreads);
         }
+        if (++turn == per) {
+            runs[run++][tid] = run_most;
+            run_most = neg_inf();
+            turn = 0;
+        }
     }
-    if (const int last = max(whole1, v0); last < v1 && last >= whole0 && tid == (last - v0) % kThreads) take(row.edge(last), last);
+    // the cut last piece belongs to the last run, which may be written already
+    if (const int last = max(whole1, v0); last < v1 && last >= whole0 && tid == (last - v0) % kThreads) {
+        const bool again = turn == 0 && run > 0 && (last - v0) / (kUnroll * kThreads * per) < run;
+        if (again) run_most = runs[run - 1][tid];
+        take(row.edge(last), last);
+        if (again) runs[run - 1][tid] = run_most;
+    }
+    for (; run * per < turns; ++run) {
+        runs[run][tid] = run_most;
+        run_most = neg_inf();
+    }
 
     // ---- the block's sums
     float top = most;
@@ -300,44 +334,94 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     // ---- the block's k largest values
     if (a.k > 0) {
         const uint32_t high = to_key(most);
-        Key key = high ? (Key)high << 32 | (uint32_t)~place : 0;
-        key = merge_warps(sorted(key, lane), kWarps, lists, warp, lane);
-        if (warp == 0) best[lane] = key;
+        // piece v's values that are not below `least`, one bit each
+        auto reach = [&](int v, uint32_t least, float (&x)[P]) {
+            uint32_t left = 0;
+            R::values(row.piece(v), x);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const uint32_t h = to_key(x[i]);
+                if (h != 0 && h >= least) left |= 1u << i;
+            }
+            return left;
+        };
+        auto key_of = [&](float x, int v, int i) { return (Key)to_key(x) << 32 | (uint32_t)~(v * P + i - row.skip); };
+        if (tid == 0) s_which = s_found = 0;
+        const uint32_t kth = merge_warps(sorted(high, lane), kWarps, reinterpret_cast<uint32_t(*)[32]>(lists), warp, lane);
+        if (tid == a.k - 1) s_least = kth;
         __syncthreads();
-        const uint32_t least = (uint32_t)(best[a.k - 1] >> 32);     // 0: fewer than k threads hold any value
-        Key list = 0;
-        for (int j = warp; j < a.k; j += kWarps) {
-            if (best[j] == 0) break;
-            const int mine = ((int)~(uint32_t)best[j] - v0) % kThreads + v0;      // that thread's first piece
-            for (int v = mine + lane * kThreads; __any_sync(0xffffffffu, v < v1); v += 32 * kThreads) {
-                float x[P];
-                uint32_t left = 0;
-                if (v < v1) {
-                    R::values(row.piece(v), x);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        const uint32_t h = to_key(x[i]);
-                        if (h != 0 && h >= least) left |= 1u << i;
-                    }
-                }
-                while (__any_sync(0xffffffffu, left != 0)) {
-                    Key cand = 0;
-                    if (left) {
-                        const int i = __ffs(left) - 1;
-                        left &= left - 1;
-                        float y = x[0];
-#pragma unroll
-                        for (int q = 1; q < P; ++q) y = i == q ? x[q] : y;
-                        cand = (Key)to_key(y) << 32 | (uint32_t)~(v * P + i - row.skip);
-                    }
-                    list = merged(list, sorted(cand, lane), lane);
+        uint32_t least = s_least;       // 0: fewer than k threads hold any value
+        if (high != 0 && high >= least)
+            for (int r = 0; r * per < turns; ++r) {
+                const uint32_t h = to_key(runs[r][tid]);
+                if (h != 0 && h >= least) {
+                    const int at = atomicAdd(&s_which, 1);      // (the order does not matter)
+                    if (at < kQuickRuns) which[at] = r * kThreads + tid;
                 }
             }
+        __syncthreads();
+        const int reached = s_which;
+        bool quick = reached <= kQuickRuns;
+        if (quick) {
+            const int each = per * kUnroll;     // pieces of a run
+            for (long long i = tid; i < (long long)reached * each; i += kThreads) {
+                const int j = (int)(i / each), at = which[j];
+                const int v = v0 + at % kThreads + (at / kThreads * each + (int)(i % each)) * kThreads;
+                if (v >= v1) continue;
+                float x[P];
+                const uint32_t left = reach(v, least, x);
+                if (left)
+#pragma unroll
+                    for (int q = 0; q < P; ++q)
+                        if (left >> q & 1u) {
+                            const int to = atomicAdd(&s_found, 1);      // (nor here: keys differ)
+                            if (to < kQuickKeys) found[to] = key_of(x[q], v, q);
+                        }
+            }
+            __syncthreads();
+            const int n = s_found;
+            quick = n <= kQuickKeys;
+            if (quick) {
+                int count = 1;
+                while (count * 32 < n) count <<= 1;
+                Key key = tid < n ? found[tid] : 0;
+                if (warp < count) key = sorted(key, lane);
+                key = merge_warps(key, count, lists, warp, lane);
+                if (warp == 0) best[lane] = key;
+            }
         }
-        int count = 1;
-        while (count < min(a.k, kWarps)) count <<= 1;
-        list = merge_warps(list, count, lists, warp, lane);
-        if (warp == 0) best[lane] = list;       // (merge_warps has synchronized since best was read)
+        if (!quick) {
+            Key key = high ? (Key)high << 32 | (uint32_t)~place : 0;
+            key = merge_warps(sorted(key, lane), kWarps, lists, warp, lane);
+            if (warp == 0) best[lane] = key;
+            __syncthreads();
+            least = (uint32_t)(best[a.k - 1] >> 32);
+            Key list = 0;
+            for (int j = warp; j < a.k; j += kWarps) {
+                if (best[j] == 0) break;
+                const int mine = ((int)~(uint32_t)best[j] - v0) % kThreads + v0;      // that thread's first piece
+                for (int v = mine + lane * kThreads; __any_sync(0xffffffffu, v < v1); v += 32 * kThreads) {
+                    float x[P];
+                    uint32_t left = v < v1 ? reach(v, least, x) : 0u;
+                    while (__any_sync(0xffffffffu, left != 0)) {
+                        Key cand = 0;
+                        if (left) {
+                            const int i = __ffs(left) - 1;
+                            left &= left - 1;
+                            float y = x[0];
+#pragma unroll
+                            for (int q = 1; q < P; ++q) y = i == q ? x[q] : y;
+                            cand = key_of(y, v, i);
+                        }
+                        list = merged(list, sorted(cand, lane), lane);
+                    }
+                }
+            }
+            int count = 1;
+            while (count < min(a.k, kWarps)) count <<= 1;
+            list = merge_warps(list, count, lists, warp, lane);
+            if (warp == 0) best[lane] = list;       // (merge_warps has synchronized since best was read)
+        }
     }
 
     // ---- the row's, by the cluster's first block
@@ -435,7 +519,7 @@ template <int DT>
 cudaError_t launch_dt(const Args& a, int T, cudaStream_t s) {
     const int pieces = (int)(((long long)a.V * (DT == DT_F32 ? 4 : 2) + 15) / 16);
     int blocks = 1;
-    while (blocks < kMaxCluster && (long long)T * blocks < 2 * kTargetSms && pieces > 2 * blocks * kThreads) blocks *= 2;
+    while (blocks < kMaxCluster && (long long)T * blocks < kTargetSms && pieces > 2 * blocks * kThreads) blocks *= 2;
     return launch_behind(logprobs_kernel<DT>, dim3((unsigned)T * blocks), dim3(kThreads), 0, (unsigned)blocks, s, a);
 }
 
