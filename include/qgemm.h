@@ -334,8 +334,9 @@ int qgemm_moe_combine(int T, int k, int N, int R, const void* Y, int y_dtype, co
 
 /* What stands directly before, beside and behind the layers of a served model: the norms that make a layer's
  * input, the low-rank adapters of the requests in a batch, and the log probabilities behind the last layer.
- * Buffers are on the current device; as the calls above, these are launched with a programmatic dependency and
- * need no workspace. Results depend on the shape and the inputs alone. */
+ * As the calls above, these are launched with a programmatic dependency; they need no workspace. Results depend on the
+ * shape and the inputs alone (a row's do not depend on the other rows of its batch, but for which of the adapters'
+ * two kernels the batch's size takes). They are forward operators. */
 
 #define QGEMM_MAX_ADAPTERS 1024
 #define QGEMM_MAX_RANK 256
@@ -344,7 +345,7 @@ int qgemm_moe_combine(int T, int k, int N, int R, const void* Y, int y_dtype, co
  *   adapter int32 [M]: each row's adapter; a row whose entry is outside [0, L) has none.
  *   row int32 [M]: the rows in order of adapter, then row; -1 past the last one that has an adapter.
  *   offsets int32 [L + 1]: adapter l's rows are row[offsets[l]] .. row[offsets[l + 1] - 1].
- * M <= 2^30, 1 <= L <= QGEMM_MAX_ADAPTERS. */
+ * The buffers must not overlap. M <= 2^30, 1 <= L <= QGEMM_MAX_ADAPTERS. */
 int qgemm_lora_group(int M, int L, const int32_t* adapter, int32_t* row, int32_t* offsets, void* stream);
 
 /* Low-rank adapters beside a shared projection, each row by its own: for every row m that `row` lists under

@@ -170,8 +170,10 @@ cudaError_t launch_ch(const NormArgs& a, cudaStream_t s) {
 template <int XDT, int SDT, int YDT>
 cudaError_t launch_y(const NormArgs& a, cudaStream_t s) {
     const int pieces = a.K / 8;
-    // One piece a thread where the rows fill no more than two blocks an SM, or are too short for more.
-    if (pieces < 32 || (a.M <= 2 * kTargetSms && pieces <= 1024)) return launch_ch<XDT, SDT, YDT, 1, 1024>(a, s);
+    // One piece a thread in rows too short for more, or where an SM takes its share of the rows at once (K = 4096: 304 rows
+    // 4.7 us, 400 rows 5.1; with four pieces 400 rows take 7.6).
+    const int one = threads_of(pieces, 1), at_once = one < 1536 ? 1536 / one : 0;
+    if (pieces < 32 || (pieces <= 1024 && a.M <= kTargetSms * at_once)) return launch_ch<XDT, SDT, YDT, 1, 1024>(a, s);
     // Only a thread's last piece may lie past the row's end: from 32 pieces on with 2 a thread, and with 4 but where a
     // row is little longer than a whole number of its warps' pieces.
     if (3 * threads_of(pieces, 4) > pieces) return launch_ch<XDT, SDT, YDT, 2, 192>(a, s);
