@@ -11,9 +11,14 @@
 //                   128-byte runs. The blocks share N.
 // RP: the ranks rounded up to a power of two; what lies past an adapter's rank is filled with zeros.
 //
-// There are few operations to a byte, so HBM's bytes are the floor: X, Y and Y again. The products were first on
-// 16x8x16 steps from registers, as in lora.cuh: 8192 x 4096 x 14336 at rank 16 took 109 us with 12 instructions a value
-// of Y, and 4099 x 2560 x 2560 at rank 128 61 us, for the loads that feed such steps.
+// There are few operations to a byte, so HBM's bytes are the floor: X, Y and Y again. 8192 x 4096 x 14336 at rank 16 in
+// bf16 takes 102 us (5.3 TB/s; a kernel that does nothing but add 1 to that Y in 128-byte runs takes 80 for its 470 MB,
+// and 67 MB of X come on top), at rank 64 133; 4099 x 2560 x 2560 at rank 128 29 us, of which 11 are the launch (one block
+// an SM, so that the next call's blocks wait for this one's), the join and the chain to the first store. With 16x8x16
+// steps from registers, as in lora.cuh, these took 109, 189 and 61 us: 12 instructions a value of Y, and the loads that feed
+// such steps. Waiting for all memory before each turn's products, and not for shared memory alone, made 102 us 151.
+// One block an SM whose warps add to Y without block barriers (a warp its own rows, groups of warps in turns) took the
+// same 103 us at rank 16, and 159 and 40 us at ranks 64 and 128, where the one warp that fed the products fell behind.
 //
 // Every wait is bounded (see ptx.cuh). After a wait that ran out the blocks still meet at the cluster's barriers, wait
 // for the MMAs in flight and release their tensor memory.
@@ -31,6 +36,9 @@ constexpr int kMaxBlocks = 8;           // of a cluster
 template <int YDT, int RP, int TERMS>
 struct Many {
     static constexpr int kYSize = YDT == DT_F32 ? 4 : 2;
+    // The warp that issues the products: one of the eight, or where a turn has 16 of them or more one of its own (4099 x 2560 x
+    // 2560 at rank 128: 31 -> 29 us; at ranks up to 64 two blocks an SM lose more by it than they gain).
+    static constexpr int kIssuer = RP > 64 ? kWarps : 0, kAll = RP > 64 ? kThreads + 32 : kThreads;
     static constexpr int kCols = 128 / kYSize;                                         // of a turn: 128 bytes of a row of Y
     static constexpr int kX = kManyRows * 128, kStage = kX + RP * 128;                  // a stage: X's rows, A's ranks
     static constexpr int kBPitch = RP < 64 ? RP * 2 : 128, kBAtoms = (RP + 63) / 64;    // bytes of a column of B, 64 ranks at a time
@@ -98,7 +106,7 @@ __device__ __forceinline__ void mma_async(uint32_t d, uint32_t a, uint32_t b, ui
 }
 
 template <bool BF, int YDT, int RP>
-__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(const ManyParams p) {
+__global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(const ManyParams p) {
     constexpr int kTerms = terms_of(BF, YDT);
     using S = Many<YDT, RP, kTerms>;
     constexpr int kYSize = S::kYSize, kTurnCols = S::kCols, kHalf = kTurnCols / 2;
@@ -147,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(c
         auto wait = [&](int i, uint32_t parity) { return ptx::mbar_wait(bar + 8 * i, parity, abort_flag, p.status, p.wait_ns); };
         if (p.stall) fail = !wait(S::kStages + 2, 0);
         const int c8 = tid & 7, r8 = tid >> 3;      // 8 threads copy a row's 128 bytes, 32 rows at a time
+        const bool copier = RP <= 64 || warp != S::kIssuer;
 
         // ---- D1 = X A^T over this block's part of K
         const int steps = a.K / 64;
@@ -157,14 +166,14 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(c
             uint32_t live = 0;
 #pragma unroll
             for (int i = 0; i < kXC; ++i) {
-                const int m = s_row[r8 + 32 * i];
+                const int m = copier ? s_row[r8 + 32 * i] : -1;
                 live |= (m >= 0 ? 1u : 0u) << i;
                 x[i] = static_cast<const uint8_t*>(a.X) + ((long long)max(m, 0) * a.ldx + (size_t)s0 * 64 + c8 * 8) * 2;
             }
             const uint8_t* A = static_cast<const uint8_t*>(a.A) + (((size_t)l * a.R + r8) * a.K + (size_t)s0 * 64 + c8 * 8) * 2;
             const uint32_t to = ring + swizzled<128>(r8, c8);        // (rows 32 apart have the same swizzle)
             auto fetch = [&](int i, int slot) {
-                if (i < n1) {
+                if (copier && i < n1) {
                     const uint32_t at = to + slot * S::kStage;
 #pragma unroll
                     for (int j = 0; j < kXC; ++j) copy16(at + j * 32 * 128, x[j] + (size_t)i * 128, live >> j & 1u);
@@ -189,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(c
                     fail = true;
                     break;
                 }
-                if (warp == 0) {
+                if (warp == S::kIssuer) {
                     gg::tc_fence_after();
                     const uint32_t at = ring + slot * S::kStage;
                     uint32_t xa = gg::rows_lo(at), wa = gg::rows_lo(at + S::kX);
@@ -224,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(c
         uint32_t there = 0;
 #pragma unroll
         for (int i = 0; i < kYC; ++i) {
-            const int m = s_row[r8 + 32 * i];
+            const int m = copier ? s_row[r8 + 32 * i] : -1;
             there |= (m >= 0 ? 1u : 0u) << i;
             y_at[i] = static_cast<uint8_t*>(a.Y) + ((long long)max(m, 0) * a.ldy + (size_t)t0 * kTurnCols + c8 * kPer) * kYSize;
         }
@@ -242,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(c
         const int b_bytes = min(max(rank - bc * 8, 0), 8) * 2;              // a piece's values past the adapter's rank become zeros
         // fetches turn u; y_at is kAhead - `back` turns before it
         auto fetch = [&](int u, int slot, int back) {
-            if (u < n2) {
+            if (copier && u < n2) {
                 const uint32_t at = ring + slot * S::kTurn;
                 if (copied(u)) {
 #pragma unroll
@@ -265,13 +274,13 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(c
 
         // ---- the block's part of H, where the stages were
         float* part = reinterpret_cast<float*>(smem_raw + (ring - ptx::smem_u32(smem_raw)));      // [128][kPartPitch]
-        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;      // a warp reads its quarter's lanes
+        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;      // a warp reads its quarter's lanes (the issuer none)
         const uint32_t lanes = tmem + ((uint32_t)quarter * 32 << 16);
         gg::tc_fence_after();
 #pragma unroll
         for (int c = 0; c < RP; c += 32) {
             float v[16];
-            if (c + half * 16 < RP) {
+            if (copier && c + half * 16 < RP) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = 0.f;
                 for (int d = 0; d < min(n1, S::kSums); ++d) {
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(c
         {
             constexpr int kLanes = RP / 4;      // of a row, 4 values each
             const int rows = kManyRows / blocks;
-            for (int i = tid; i < rows * kLanes; i += kThreads) {
+            for (int i = tid; i < rows * kLanes; i += S::kAll) {
                 const int r = rank_in * rows + i / kLanes, c = i % kLanes * 4;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int b0 = 0; b0 < blocks; b0 += 4) {
@@ -360,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(c
                 fail = true;
                 break;
             }
-            if (warp == 0 && u < n2) {
+            if (warp == S::kIssuer && u < n2) {
                 gg::tc_fence_after();
                 const uint32_t d = tmem + S::kD2 + (u & 1) * kTurnCols, bt = ring + slot * S::kTurn + S::kY;
                 for (int t = 0; t < kTerms; ++t)
@@ -373,7 +382,12 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(c
                 gg::mma_commit<gg::SOLO>(bar + 8 * (S::kStages + (u & 1)));
             }
             fetch(u + S::kTurns - 2, next, u > 0 ? 0 : 1);
-            if (u > 0) {
+            if (u > 0 && !copier) {
+                if (__syncthreads_or(fail)) {
+                    fail = true;
+                    break;
+                }
+            } else if (u > 0) {
                 const int v = u - 1, n = (t0 + v) * kTurnCols + half * kHalf;
                 const uint32_t tile = ring + before * S::kTurn;
                 fail = fail || !wait(S::kStages + (v & 1), (uint32_t)(v >> 1) & 1u);
@@ -455,7 +469,7 @@ cudaError_t launch_many(const LoraArgs& a, int blocks, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // at most one tile that is not full for each adapter that has rows
     const long long tiles = (long long)a.M / kManyRows + (a.L < a.M ? a.L : a.M);
-    return launch_behind(kern, dim3((unsigned)(tiles * blocks)), dim3(kThreads), S::kSmem, (unsigned)blocks, s, p);
+    return launch_behind(kern, dim3((unsigned)(tiles * blocks)), dim3(S::kAll), S::kSmem, (unsigned)blocks, s, p);
 }
 
 // Largest power of two up to 8 of which `tiles` clusters make at most `most` blocks (1 at least).
