@@ -228,6 +228,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     const int pieces = row.pieces(), share = (pieces + (int)blocks - 1) / (int)blocks;
     const int v0 = min((int)rank * share, pieces), v1 = min(v0 + share, pieces);
 
+    // the given token's logit, which the end would else wait for
+    int token = -1;
+    float given = 0.f;
+    if (a.logprob && rank == 0 && tid == 0) {
+        token = load(a.token + t);
+        if (token >= 0 && token < a.V) given = load_as_float<DT>(row.from, (size_t)row.skip + token);
+    }
+
     // ---- the pass
     float most = neg_inf(), limit = neg_inf(), ref = neg_inf();
     int place = 0;
@@ -486,12 +494,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
             return x > neg_inf() ? fminf((x - all.x) * a.scale - over, 0.f) : neg_inf();
         };
         if (tid == 0) {
-            if (a.logprob) {
-                const int token = load(a.token + t);
-                float lp = 0.f;
-                if (token >= 0 && token < a.V) lp = log_p(load_as_float<DT>(row.from, (size_t)row.skip + token));
-                a.logprob[t] = lp;
-            }
+            if (a.logprob) a.logprob[t] = token >= 0 && token < a.V ? log_p(given) : 0.f;
             if (a.entropy) a.entropy[t] = all.y > 0.f ? fmaxf(logf(all.y) - kLn2 * all.z / all.y, 0.f) : 0.f;
         }
         if (a.k > 0) {
