@@ -156,6 +156,34 @@ def test_offsets_that_are_not_in_order():
     ref.check(c["Y"], want, allow)
 
 
+@pytest.mark.parametrize("M,L,none", [(1, 1024, 0.0), (40, 33, 0.2), (200, 255, 0.0), (300, 256, 0.5), (333, 257, 0.1), (700, 513, 0.0), (500, 1000, 0.3),
+                                      (1100, 1024, 0.0), (2400, 1000, 0.1)])
+def test_many_adapters(M, L, none):
+    check(make(M, 128, 40, L, 16, qg.BF16, qg.F32, mixed(M, L, M, none=none), seed=L))
+
+
+@pytest.mark.parametrize("L", [31, 90, 256, 600, 1024])
+@pytest.mark.parametrize("M", [57, 2500])
+def test_many_offsets_that_are_not_in_order(M, L):
+    r = random.Random(L + M)
+    c = make(M, 64, 24, L, 16, qg.BF16, qg.F32, [0] * M)
+    given = sorted(r.randrange(M + 1) for _ in range(L + 1))
+    for _ in range(L // 3):
+        given[r.randrange(L + 1)] = r.choice((-9, -(1 << 31), 0, r.randrange(M + 1)))
+    owner, row = [-1] * M, list(range(M))
+    r.shuffle(row)
+    held = min(max(given[0], 0), M)
+    for l in range(L):
+        end = max(min(max(given[l + 1], 0), M), held)
+        for i in range(held, end):
+            owner[row[i]] = l
+        held = end
+    want, allow = ref.lora(c["Y"], c["X"], c["A"], c["B"], owner, None, c["scale"])
+    to = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    qg.qgemm_lora_run(M, 64, 24, L, 16, c["dtype"], to(row), to(given), c["X"], 64, c["A"], c["B"], None, c["scale"], c["Y"], qg.F32, 24)
+    ref.check(c["Y"], want, allow)
+
+
 def test_same_bits_every_time_and_on_another_stream():
     c = make(77, 1024, 333, 6, 64, qg.BF16, qg.F32, mixed(77, 6))
     before = c["Y"].clone()

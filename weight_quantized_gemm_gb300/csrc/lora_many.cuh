@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
     __shared__ __align__(8) unsigned long long s_bar[S::kStages + 3];      // stages, the two buffers of D2, one that never completes
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ TileSearch s_tile;
     __shared__ int s_row[kManyRows];
     __shared__ float s_unit[kManyRows];         // f16: the power of two that a row of H was divided by
     const LoraArgs& a = p.a;
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
     grid_wait();
     grid_release();
     int l = 0, from = 0, count = 0;
-    const bool any = find_tile(a, blockIdx.x / blocks, kManyRows, l, from, count);
+    const bool any = find_tile(a, blockIdx.x / blocks, kManyRows, s_tile, l, from, count);
     const int rank = !any ? 0 : (a.rank ? min(max(load(a.rank + l), 0), a.R) : a.R);
     if (rank > 0) {             // (the same for the whole cluster)
         const float scale = a.scale ? load(a.scale + l) : 1.f;
@@ -500,8 +501,10 @@ cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
         }
     }
     // 8 blocks for a few rows (16 rows of 16 adapters 5.9 us; 4 blocks 6.9), fewer where the tiles alone fill the GPU
-    // (1024 rows 25 us with 4, 29 with 8).
-    const int blocks = blocks_of(a.M / 16 + (a.L < a.M ? a.L : a.M) / 2, kTargetSms * 9 / 4);
+    // (1024 rows 25 us with 4, 29 with 8). As many rows as adapters, each row's drawn at random, leave 5/8 of the
+    // adapters with rows, a tile each (4096 x 4096, rank 16, us with 2 / 4 / 8 blocks: 48 of each 15.2 / 10.3 / 7.9, 64
+    // of each 16.9 / 11.5 / 15.3, 512 rows of 8 adapters 17.0 / 11.1 / 10.2).
+    const int blocks = blocks_of(a.M / 16 + (long long)(a.L < a.M ? a.L : a.M) * 5 / 8, kTargetSms * 9 / 4);
     switch (rank) {
         case 16: return launch<BF, YDT, 1>(a, blocks, s);
         case 32: return launch<BF, YDT, 2>(a, blocks, s);

@@ -6,6 +6,8 @@
 
 namespace qg {
 
+constexpr int kMaxLoraAdapters = 1024;
+
 enum NormKind { NORM_RMS = 1, NORM_LAYER = 2 };
 
 struct LoraArgs {

@@ -29,6 +29,7 @@ bool all_aligned16(P... p) {
     return (aligned16(p) && ...);
 }
 bool valid_dtype(int d) { return d == QGEMM_F32 || d == QGEMM_F16 || d == QGEMM_BF16; }
+static_assert(QGEMM_MAX_ADAPTERS == qg::kMaxLoraAdapters, "how many the search for a tile takes");
 constexpr int kMax = 1 << 30;      // rows and columns of one call, so that rounding up to a tile stays an int
 // rows `ld` values apart start 16-byte aligned (of any size: the product is not formed)
 bool row_aligned(long long ld, int dtype) { return ld % (16 / (long long)qg::dt_size(dtype)) == 0; }
