@@ -334,9 +334,10 @@ int qgemm_moe_combine(int T, int k, int N, int R, const void* Y, int y_dtype, co
 
 /* What stands directly before, beside and behind the layers of a served model: the norms that make a layer's
  * input, the low-rank adapters of the requests in a batch, and the log probabilities behind the last layer.
- * As the calls above, these are launched with a programmatic dependency; they need no workspace. Results depend on the
- * shape and the inputs alone (a row's do not depend on the other rows of its batch, but for which of the adapters'
- * two kernels the batch's size takes). They are forward operators. */
+ * As the calls above, these are launched with a programmatic dependency; they need no workspace. Results depend on
+ * the shape and the inputs alone. A row's do not depend on what the other rows of its batch hold; how many rows there
+ * are (and adapters) decides how its sums are split, so that in batches of different sizes it may differ in the last
+ * bits. They are forward operators. */
 
 #define QGEMM_MAX_ADAPTERS 1024
 #define QGEMM_MAX_RANK 256
@@ -482,8 +483,9 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
 #define QGEMM_OPT_SPLIT_K 3
 
 /* QGEMM_OPT_WAIT_LIMIT_US (default 1000000, range 1..1000000). The TMA-fed kernels (the decode
- * kernel for M <= 16, the tensor-core kernel and that of the 4-bit and grouped products), and the adapters'
- * kernel for many rows, bound every wait of their pipelines by this many microseconds of the GPU's global timer: a wait that runs out sets the status word that
+ * kernel for M <= 16, the tensor-core kernel and that of the 4-bit and grouped products), and the
+ * adapters' kernel for many rows, bound every wait of their pipelines by this many microseconds of
+ * the GPU's global timer: a wait that runs out sets the status word that
  * qgemm_status reports as QGEMM_ERR_TIMEOUT, every role of the thread block leaves its loop, the
  * copies and MMAs already issued are waited for (always with the full one-second bound; 20 ms for a
  * stage's copies in the 4-bit and grouped products, whose barrier may never complete then) and the
@@ -493,8 +495,9 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
 #define QGEMM_OPT_WAIT_LIMIT_US 4
 
 /* QGEMM_OPT_DEBUG_STALL (default 0). Diagnostic: when 1, every following launch of the TMA-fed
- * kernels has one role (the MMA issuer of the tensor-core kernel, the first consumer warp of the
- * decode kernel) wait first on a barrier that nothing arrives at, so that the wait runs out after
+ * kernels, and of the adapters' kernel for many rows, has one role (the MMA issuer of the tensor-core
+ * kernel, the first consumer warp of the decode kernel, all threads of the adapters' kernel) wait
+ * first on a barrier that nothing arrives at, so that the wait runs out after
  * QGEMM_OPT_WAIT_LIMIT_US and the call ends with QGEMM_ERR_TIMEOUT as described above. It makes
  * the timeout path testable without a hang; production code keeps 0. Process-wide. */
 #define QGEMM_OPT_DEBUG_STALL 5
@@ -502,9 +505,10 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
 /* QGEMM_OPT_FAULT_INJECT (default 0, or the value of the environment variable QGEMM_FAULT_INJECT
  * when the library loads). Host-side fault injection: when n > 0, the n-th compute call from now
  * (qgemm_pack, qgemm_run, qgemm_run_fused, qgemm_run_noalloc, qgemm_act_quant, qgemm_w4a8_acc, the
- * qgemm_fp4_*, qgemm_grouped_run, qgemm_moe_*, qgemm_lora_*, qgemm_norm_run and qgemm_logprobs calls) passes its argument checks and then returns
- * QGEMM_ERR_CUDA with the detail "simulated launch failure" instead of launching, as a failed launch
- * would; the count then stays 0. No GPU fault is involved. For testing callers' error handling. Process-wide. */
+ * qgemm_fp4_*, qgemm_grouped_run, qgemm_moe_*, qgemm_lora_*, qgemm_norm_run and qgemm_logprobs calls)
+ * passes its argument checks and then returns QGEMM_ERR_CUDA with the detail "simulated launch
+ * failure" instead of launching, as a failed launch would; the count then stays 0. No GPU fault is
+ * involved. For testing callers' error handling. Process-wide. */
 #define QGEMM_OPT_FAULT_INJECT 6
 
 /* Set an option; returns its previous value, or QGEMM_ERR_ARG for an unknown option or value. */
