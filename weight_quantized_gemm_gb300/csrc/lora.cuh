@@ -5,9 +5,11 @@
 // A cluster of thread blocks takes up to 16 rows of one adapter. Its blocks share K in the first product (H = X A^T,
 // R values a row), join their parts of H in distributed shared memory, each in the same order, and share N in the
 // second one (H B^T), so neither product needs scratch memory or a second launch. What bounds it is a chain of round
-// trips: the offsets, the rows' numbers, the first product's operands, the join, the store. 16 rows of 16 adapters,
-// 4096 x 4096 at rank 16: 5.9 us in a graph (the same with next to no K and N: 4.3); 77 rows of 24 adapters of ranks up
-// to 64, 9728 x 2560, float32 Y: 16 us.
+// trips: the offsets, the first product's operands, the join, the second one's, the store. 16 rows of 16 adapters,
+// 4096 x 4096 at rank 16: 4.6 us in a graph, in which the parts take some 1700 cycles (tile and rows), 1250 (the first
+// product, one step a warp), 600 (its warps' sums), 700 (asking for B and Y), 1400 (the join) and 1500 (the second
+// product). 77 rows of 24 adapters of ranks up to 64, 9728 x 2560, float32 Y: 13.9 us, of which the first product's five
+// steps a warp take 4 (15 MB, most of which HBM needs 2.3 for).
 //
 // Both products run on 16x8x16 tensor-core steps from registers, without a copy through shared memory: the order of
 // the summed index is free as long as both operands keep to it, so a lane takes 16 neighbouring bytes of a row as its
@@ -85,46 +87,53 @@ __device__ __forceinline__ float row_unit_inverse(uint32_t top) {
     return e == 255u ? 1.f : __uint_as_float((254u - min(max(e, 1u), 253u)) << 23);
 }
 
-// H of all of K from the blocks' parts h, added in rank order: [rows][pitch], 16 * chunks columns; top: the bits of each
-// row's largest |H| (f16; cleared before). Every thread of the block calls it.
-template <bool BF>
-__device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top, int pitch, int rows, int chunks, int blocks) {
-    const int width = chunks * 4;
-    for (int i = threadIdx.x; i < rows * width; i += kThreads) {
-        const int row = i / width, at = row * pitch + i % width * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (blocks > 1) {
-            for (int k0 = 0; k0 < blocks; k0 += 4) {
-                float4 o[4];
+// 4 values at h of all blocks, added in rank order, AT_ONCE of them asked for together: a round trip to another block takes
+// some 700 cycles (16 rows, 16 adapters, with 8 together 4.5 us, with 4 4.8; of ranks up to 64 registers allow 4).
+template <int AT_ONCE>
+__device__ __forceinline__ float4 sum_of_blocks(const float* h, int blocks) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < blocks; k0 += AT_ONCE) {
+        float4 o[AT_ONCE];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k0 + k < blocks) o[k] = ld_cluster_f32x4(in_block(h + at, k0 + k));
+        for (int k = 0; k < AT_ONCE; ++k)
+            if (k0 + k < blocks) o[k] = ld_cluster_f32x4(in_block(h, k0 + k));
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k0 + k < blocks) {
-                        v.x += o[k].x; v.y += o[k].y; v.z += o[k].z; v.w += o[k].w;
-                    }
+        for (int k = 0; k < AT_ONCE; ++k)
+            if (k0 + k < blocks) {
+                v.x += o[k].x; v.y += o[k].y; v.z += o[k].z; v.w += o[k].w;
             }
-        } else {
-            v = *reinterpret_cast<const float4*>(h + at);
-        }
-        *reinterpret_cast<float4*>(sum + at) = v;
-        if constexpr (!BF) {
-            const float t = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-            atomicMax(top + row, __float_as_uint(t));
-        }
     }
+    return v;
 }
-// H's 16-bit terms, in the order in which the lanes take them: frag [tiles of 16 rows][chunks][terms][32].
+// H of all of K from the blocks' parts h: [rows][pitch], 16 * chunks columns, WIDTH pieces of 4 at a time; top: the bits
+// of each row's largest |H| (f16; cleared before). Every thread of the block calls it.
+template <bool BF, int WIDTH>
+__device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top, int pitch, int rows, int chunks, int blocks) {
+    for (int c0 = 0; c0 < chunks * 4; c0 += WIDTH)
+        for (int i = threadIdx.x; i < rows * WIDTH; i += kThreads) {
+            const int row = i / WIDTH, c = c0 + i % WIDTH, at = row * pitch + c * 4;
+            if (c >= chunks * 4) continue;
+            float4 v;
+            if (blocks == 1) v = *reinterpret_cast<const float4*>(h + at);
+            else if (WIDTH <= 8 && blocks == 8) v = sum_of_blocks<8>(h + at, 8);
+            else v = sum_of_blocks<4>(h + at, blocks);
+            *reinterpret_cast<float4*>(sum + at) = v;
+            if constexpr (!BF) {
+                const float t = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+                atomicMax(top + row, __float_as_uint(t));
+            }
+        }
+}
+// H's 16-bit terms, in the order in which the lanes take them: frag [chunks][terms][32].
 template <bool BF, int TERMS>
-__device__ __forceinline__ void make_terms(const float* sum, const uint32_t* top, uint4* frag, int pitch, int tiles, int chunks) {
+__device__ __forceinline__ void make_terms(const float* sum, const uint32_t* top, uint4* frag, int pitch, int chunks) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    for (int f = warp; f < tiles * chunks; f += kWarps) {
+    for (int f = warp; f < chunks; f += kWarps) {
         float v[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int row = f / chunks * 16 + g + 8 * i;
-            const float4 o = *reinterpret_cast<const float4*>(sum + row * pitch + f % chunks * 16 + q * 4);
+            const int row = g + 8 * i;
+            const float4 o = *reinterpret_cast<const float4*>(sum + row * pitch + f * 16 + q * 4);
             const float by = BF ? 1.f : row_unit_inverse(top[row]);
             v[i][0] = o.x * by; v[i][1] = o.y * by; v[i][2] = o.z * by; v[i][3] = o.w * by;
         }
@@ -250,6 +259,21 @@ __device__ __forceinline__ bool find_tile(const LoraArgs& a, int q, int rows, Ti
     return true;
 }
 
+// 16 or 8 bytes, zeros where `any` is not set: one instruction under a predicate, where a branch around each of a step's
+// loads takes longer than the loads (77 rows of ranks up to 64: 15.4 -> 14.4 us).
+__device__ __forceinline__ void load_if(uint4& v, const void* p, bool any) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((int)any));
+}
+__device__ __forceinline__ void load_if(uint2& v, const void* p, bool any) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t@p ld.global.v2.b32 {%0, %1}, [%2];\n\t}"
+                 : "=&r"(v.x), "=&r"(v.y)
+                 : "l"(p), "r"((int)any));
+}
+
 // Sixteen ranks at a time are a chunk; JT of them are in registers together.
 template <int JT>
 struct Shape {
@@ -274,10 +298,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     constexpr int kNT = 2 * JT, kXV = S::kStep / 32, kTerms = terms_of(BF, YDT);
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ TileSearch s_tile;
+    __shared__ int s_row[kThreads], s_rank[kThreads];
+    __shared__ float s_scale[kThreads];
     const LoraArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
     const int wk = warp;
-    const int blocks = (int)cluster_size(), rank_in = blocks > 1 ? (int)cluster_rank() : 0;
+    // (blocks is a power of two, of 8 at most: shifts, as a 64-bit division takes 330 cycles)
+    const int blocks = (int)cluster_size(), shift = __ffs(blocks) - 1, rank_in = blocks > 1 ? (int)cluster_rank() : 0;
     const int pitch = S::ranks(a.R) + 8;
     float* part = reinterpret_cast<float*>(smem);                           // [kWK][kRows][kPartPitch]
     float* sum = part;                                                      // [kRows][pitch], all of K
@@ -286,21 +313,36 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     uint32_t* top = reinterpret_cast<uint32_t*>(frag + (S::ranks(a.R) / 16) * kTerms * 32);   // [kRows]
     grid_wait();
     grid_release();
-    int l, from, count;
-    if (!find_tile(a, blockIdx.x / blocks, S::kRows, s_tile, l, from, count)) return;      // the whole cluster
-    const int rank = a.rank ? min(max(load(a.rank + l), 0), a.R) : a.R;
-    if (rank == 0) return;
-    const float scale = a.scale ? load(a.scale + l) : 1.f;
-
-    // this lane's two rows
-    int m[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = g + 8 * i;
-        m[i] = at < count ? load(a.row + from + at) : -1;
-        if (m[i] >= a.M) m[i] = -1;
+    // A batch of a row a thread at most has its rows' numbers on the way while it looks for the tile.
+    // So have the ranks and scales of as many adapters.
+    const bool few = a.M <= kThreads && a.L <= kThreads;
+    if (few) {
+        s_row[tid] = tid < a.M ? load(a.row + tid) : -1;
+        s_rank[tid] = a.rank && tid < a.L ? load(a.rank + tid) : a.R;
+        s_scale[tid] = a.scale && tid < a.L ? load(a.scale + tid) : 1.f;
     }
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    int l, from, count;
+    if (!find_tile(a, blockIdx.x >> shift, S::kRows, s_tile, l, from, count)) return;      // the whole cluster
+    // this lane's two rows
+    int m[2], rank;
+    float scale;
+    if (few) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) m[i] = g + 8 * i < count ? s_row[from + g + 8 * i] : -1;
+        scale = s_scale[l];
+        rank = s_rank[l];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) m[i] = g + 8 * i < count ? load(a.row + from + g + 8 * i) : -1;
+        scale = a.scale ? load(a.scale + l) : 1.f;
+        rank = a.rank ? load(a.rank + l) : a.R;
+    }
+    rank = min(max(rank, 0), a.R);
+    if (rank == 0) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (m[i] >= a.M) m[i] = -1;
 
     // ---- H = X A^T, kRC ranks a pass; the block's part of K, its warps' parts of that
     {
@@ -308,45 +350,49 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
         const uint16_t* x0 = X + (long long)max(m[0], 0) * a.ldx;
         const uint16_t* x1 = X + (long long)max(m[1], 0) * a.ldx;
         const int steps = a.K / S::kStep;
-        const int s0 = (int)((long long)steps * rank_in / blocks), s1 = (int)((long long)steps * (rank_in + 1) / blocks);
-        for (int r0 = 0; r0 < rank; r0 += S::kRC) {
+        const int s0 = steps * rank_in >> shift, s1 = steps * (rank_in + 1) >> shift;     // (K <= 2^30)
+        // Two steps are in flight, each in registers of its own: with one set, copied before the next step's loads, each
+        // step waited for its own (64 rows of 64 adapters 11.8 -> 10 us).
+        uint4 x[2][2][kXV], w[2][kNT][kXV];
+        auto fetch = [&](int r0, int s, uint4 (&x)[2][kXV], uint4 (&w)[kNT][kXV]) {
+            if (r0 >= rank || s >= s1) return;
             const uint16_t* A = static_cast<const uint16_t*>(a.A) + ((size_t)l * a.R + r0 + g) * a.K;
+#pragma unroll
+            for (int v = 0; v < kXV; ++v) {
+                const size_t k = (size_t)s * S::kStep + v * 32 + q * 8;
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+                    load_if(w[n][v], A + (size_t)n * 8 * a.K + k, r0 + n * 8 + g < rank);
+                load_if(x[0][v], x0 + k, m[0] >= 0);
+                load_if(x[1][v], x1 + k, m[1] >= 0);
+            }
+        };
+        fetch(0, s0 + wk, x[0], w[0]);
+        fetch(0, s0 + wk + S::kWK, x[1], w[1]);
+        for (int r0 = 0; r0 < rank; r0 += S::kRC) {
             float acc[kNT][4];
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-            uint4 x[2][kXV], w[kNT][kXV];
-            auto fetch = [&](int s) {
-#pragma unroll
-                for (int v = 0; v < kXV; ++v) {
-                    const size_t k = (size_t)s * S::kStep + v * 32 + q * 8;
-#pragma unroll
-                    for (int n = 0; n < kNT; ++n)
-                        w[n][v] = r0 + n * 8 + g < rank ? load(reinterpret_cast<const uint4*>(A + (size_t)n * 8 * a.K + k)) : zero;
-                    x[0][v] = m[0] >= 0 ? load(reinterpret_cast<const uint4*>(x0 + k)) : zero;
-                    x[1][v] = m[1] >= 0 ? load(reinterpret_cast<const uint4*>(x1 + k)) : zero;
-                }
-            };
-            if (s0 + wk < s1) fetch(s0 + wk);
-            for (int s = s0 + wk; s < s1; s += S::kWK) {
-                uint4 cx[2][kXV], cw[kNT][kXV];
-#pragma unroll
-                for (int v = 0; v < kXV; ++v) {
-                    cx[0][v] = x[0][v];
-                    cx[1][v] = x[1][v];
-#pragma unroll
-                    for (int n = 0; n < kNT; ++n) cw[n][v] = w[n][v];
-                }
-                if (s + S::kWK < s1) fetch(s + S::kWK);
+            auto step = [&](const uint4 (&x)[2][kXV], const uint4 (&w)[kNT][kXV]) {
 #pragma unroll
                 for (int v = 0; v < kXV; ++v)
 #pragma unroll
                     for (int n = 0; n < kNT; ++n) {
-                        mma<BF>(acc[n], make_uint4(cx[0][v].x, cx[1][v].x, cx[0][v].y, cx[1][v].y), cw[n][v].x, cw[n][v].y);
-                        mma<BF>(acc[n], make_uint4(cx[0][v].z, cx[1][v].z, cx[0][v].w, cx[1][v].w), cw[n][v].z, cw[n][v].w);
+                        mma<BF>(acc[n], make_uint4(x[0][v].x, x[1][v].x, x[0][v].y, x[1][v].y), w[n][v].x, w[n][v].y);
+                        mma<BF>(acc[n], make_uint4(x[0][v].z, x[1][v].z, x[0][v].w, x[1][v].w), w[n][v].z, w[n][v].w);
                     }
+            };
+            for (int s = s0 + wk; s < s1; s += 2 * S::kWK) {
+                step(x[0], w[0]);
+                fetch(r0, s + 2 * S::kWK, x[0], w[0]);
+                if (s + S::kWK >= s1) break;
+                step(x[1], w[1]);
+                fetch(r0, s + 3 * S::kWK, x[1], w[1]);
             }
+            fetch(r0 + S::kRC, s0 + wk, x[0], w[0]);
+            fetch(r0 + S::kRC, s0 + wk + S::kWK, x[1], w[1]);
             if (r0 > 0) __syncthreads();        // the pass before has been read
             float* mine = part + (wk * S::kRows + g) * S::kPartPitch + 2 * q;
 #pragma unroll
@@ -355,9 +401,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
                 *reinterpret_cast<float2*>(mine + 8 * S::kPartPitch + n * 8) = make_float2(acc[n][2], acc[n][3]);
             }
             __syncthreads();
-            const int width = min(S::kRC, pitch - 8 - r0) / 4;
-            for (int i = tid; i < S::kRows * width; i += kThreads) {
-                const int row = i / width, c = i % width * 4;
+            constexpr int kWidth = S::kRC / 4;
+            for (int i = tid; i < S::kRows * kWidth; i += kThreads) {
+                const int row = i / kWidth, c = i % kWidth * 4;
+                if (r0 + c >= pitch - 8) continue;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < S::kWK; ++k) {
@@ -372,83 +419,90 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
 
     // ---- the second product's first operands come while the blocks meet
     const int units = (a.N + 31) / 32;
-    const int u0 = (int)((long long)units * rank_in / blocks), u1 = (int)((long long)units * (rank_in + 1) / blocks);
+    const int u0 = units * rank_in >> shift, u1 = units * (rank_in + 1) >> shift;         // (N <= 2^30)
     const int chunks = (rank + 15) / 16;
     const uint16_t* B = static_cast<const uint16_t*>(a.B) + (size_t)l * a.N * a.R;
     const bool wide = a.ldy % (YDT == DT_F32 ? 4 : 8) == 0;
-    uint2 b[JT][4];
-    Eight<YDT> y[2];
-    // ranks 16 (c0 + j) + 4 q .. + 3 of the columns of unit u: bits past the adapter's rank are cleared
-    auto fetch_b = [&](int u, int c0) {
+    // Items of JT chunks of a unit of 32 columns, two in flight in registers of their own (Y's rows of the second where
+    // registers allow it).
+    constexpr int kYSets = JT == 4 && YDT == DT_F32 ? 1 : 2;
+    uint2 b[2][JT][4];
+    Eight<YDT> y[kYSets][2];
+    // ranks 16 (c0 + j) + 4 q .. + 3 of the columns of unit u
+    auto fetch_b = [&](int u, int c0, uint2 (&b)[JT][4]) {
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
-            const int r = (c0 + j) * 16 + q * 4, left = rank - r;
+            const int r = (c0 + j) * 16 + q * 4;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int n = u * 32 + (g >> 1) * 8 + t * 2 + (g & 1);
-                b[j][t] = left > 0 && n < a.N ? load(reinterpret_cast<const uint2*>(B + (size_t)n * a.R + r)) : make_uint2(0, 0);
-                if (left < 4) {
-                    b[j][t].x &= left >= 2 ? ~0u : (left == 1 ? 0xFFFFu : 0u);
-                    b[j][t].y &= left == 3 ? 0xFFFFu : 0u;
-                }
+                load_if(b[j][t], B + (size_t)n * a.R + r, r < rank && n < a.N);
             }
         }
     };
-    auto fetch_y = [&](int u) {
+    auto fetch_y = [&](int u, Eight<YDT> (&y)[2]) {
         if (!wide || u * 32 + q * 8 + 8 > a.N) return;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (m[i] >= 0) y[i].fetch(a.Y, (size_t)((long long)m[i] * a.ldy) + u * 32 + q * 8);
     };
-    if (u0 + wk < u1) {
-        fetch_b(u0 + wk, 0);
-        fetch_y(u0 + wk);
-    }
+    int next_u = u0 + wk, next_c = 0;       // the item to fetch
+    auto fetch_item = [&](uint2 (&b)[JT][4], Eight<YDT> (&y)[2]) {
+        if (next_u >= u1) return;
+        fetch_b(next_u, next_c, b);
+        next_c += JT;
+        if (next_c >= chunks) {             // the unit's last
+            if (kYSets == 2) fetch_y(next_u, y);
+            next_c = 0;
+            next_u += S::kWK;
+        }
+    };
+    if (kYSets == 1 && u0 + wk < u1) fetch_y(u0 + wk, y[0]);
+    fetch_item(b[0], y[0]);
+    fetch_item(b[1], y[kYSets - 1]);
 
     // ---- H of all of K, in the same order in every block, and its terms
     if (blocks > 1) cluster_sync();
     else __syncthreads();
-    join_h<BF>(h, sum, top, pitch, S::kRows, chunks, blocks);
+    join_h<BF, S::kRC / 4>(h, sum, top, pitch, S::kRows, chunks, blocks);
     if (blocks > 1) cluster_arrive();       // waited for at the end
     __syncthreads();
-    make_terms<BF, kTerms>(sum, top, frag, pitch, 1, chunks);
+    make_terms<BF, kTerms>(sum, top, frag, pitch, chunks);
     __syncthreads();
 
     // ---- Y += scale H B^T
     float mul[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) mul[i] = BF ? 1.f : row_unit(top[g + 8 * i]);
-    for (int u = u0 + wk; u < u1; u += S::kWK) {
-        float acc[4][4];
+    float acc[4][4];
+    int u = u0 + wk, c0 = 0;
+    auto item = [&](uint2 (&b)[JT][4], Eight<YDT> (&y)[2]) {
+        if (c0 == 0)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
-        Eight<YDT> cy[2] = {y[0], y[1]};
-        for (int c0 = 0; c0 < chunks; c0 += JT) {
-            uint2 cb[JT][4];
+                for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
 #pragma unroll
-            for (int j = 0; j < JT; ++j)
+        for (int j = 0; j < JT; ++j) {
+            if (c0 + j >= chunks) break;
+            const int left = rank - (c0 + j) * 16 - q * 4;
+            if (left < 4)                   // values past the adapter's rank are cleared
 #pragma unroll
-                for (int t = 0; t < 4; ++t) cb[j][t] = b[j][t];
-            if (c0 + JT < chunks) {
-                fetch_b(u, c0 + JT);
-            } else if (u + S::kWK < u1) {
-                fetch_b(u + S::kWK, 0);
-                fetch_y(u + S::kWK);
-            }
-#pragma unroll
-            for (int j = 0; j < JT; ++j) {
-                if (c0 + j >= chunks) break;
-                const uint4* f = frag + (c0 + j) * kTerms * 32 + lane;
-#pragma unroll
-                for (int k = 0; k < kTerms; ++k) {
-                    const uint4 w = f[k * 32];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) mma<BF>(acc[t], w, cb[j][t].x, cb[j][t].y);
+                for (int t = 0; t < 4; ++t) {
+                    b[j][t].x &= left >= 2 ? ~0u : (left == 1 ? 0xFFFFu : 0u);
+                    b[j][t].y &= left == 3 ? 0xFFFFu : 0u;
                 }
+            const uint4* f = frag + (c0 + j) * kTerms * 32 + lane;
+#pragma unroll
+            for (int k = 0; k < kTerms; ++k) {
+                const uint4 h = f[k * 32];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) mma<BF>(acc[t], h, b[j][t].x, b[j][t].y);
             }
         }
+        c0 += JT;
+        if (c0 < chunks) return;
+        c0 = 0;
         const int n = u * 32 + q * 8;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -462,15 +516,24 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
             uint8_t* out = static_cast<uint8_t*>(a.Y) + ((long long)m[i] * a.ldy + n) * (YDT == DT_F32 ? 4 : 2);
             if (wide && n + 8 <= a.N) {
                 float v[8];
-                cy[i].values(v);
+                y[i].values(v);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = fmaf(scale, d[k], v[k]);
-                cy[i].round_from(v);
-                cy[i].store(out, 0);
+                y[i].round_from(v);
+                y[i].store(out, 0);
             } else {
                 add_edge<YDT>(out, d, scale, a.N - n);
             }
         }
+        u += S::kWK;
+        if (kYSets == 1 && u < u1) fetch_y(u, y);
+    };
+    while (u < u1) {
+        item(b[0], y[0]);
+        fetch_item(b[0], y[0]);
+        if (u >= u1) break;
+        item(b[1], y[kYSets - 1]);
+        fetch_item(b[1], y[kYSets - 1]);
     }
     if (blocks > 1) cluster_wait();         // no block leaves while its H is read
 }

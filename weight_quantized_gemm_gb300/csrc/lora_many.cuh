@@ -483,11 +483,11 @@ inline int blocks_of(long long tiles, int most) {
 template <bool BF, int YDT>
 cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
     // Tiles of 128 rows where there are many rows; from how many on depends on the rank, as the few rows' kernel reads each
-    // adapter once for every 16 rows (4096 x 14336, us, few / many: rank 16 2048 rows 47 / 52, 2900 rows 69 / 54; rank 32
-    // 1500 rows 46 / 45; rank 64 1024 rows 40 / 49, 1500 rows 70 / 50; rank 128, 2560 x 2560, 512 rows 20 / 19, 1024 rows
-    // 24 / 21, and 4096 x 14336, 512 rows 38 / 55). The cluster's size fills the SMs once (two blocks an SM, one at rank
-    // 128), with the number of tiles guessed from M and L, since the host does not see the offsets: 8192 rows 102 us with 4
-    // blocks, 117 with 8, 142 with 2.
+    // adapter once for every 16 rows, and from where on it needs a second round of blocks (4096 x 14336, us, few / many:
+    // rank 16 2048 rows 42 / 51, 2900 rows 74 / 53; rank 32 1500 rows 46 / 45; rank 64 1024 rows 37 / 48, 1300 rows 65 / 49;
+    // rank 128 512 rows 45 / 47, 900 rows 60 / 49, and 2560 x 2560 768 rows 20 / 19, 1024 rows 21 / 19). The cluster's size
+    // fills the SMs once (two blocks an SM, one at rank 128), with the number of tiles guessed from M and L, since the host
+    // does not see the offsets: 8192 rows 102 us with 4 blocks, 117 with 8, 142 with 2.
     const int rank = a.R <= 16 ? 16 : (a.R <= 32 ? 32 : (a.R <= 64 ? 64 : 128));
     const int from = rank == 16 ? 2304 : (rank == 32 ? 1536 : (rank == 64 ? 1280 : 768));
     if (a.R <= 128 && a.M >= from) {
@@ -500,10 +500,10 @@ cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
             default: return launch_many<BF, YDT, 128>(a, blocks, s);
         }
     }
-    // 8 blocks for a few rows (16 rows of 16 adapters 5.9 us; 4 blocks 6.9), fewer where the tiles alone fill the GPU
-    // (1024 rows 25 us with 4, 29 with 8). As many rows as adapters, each row's drawn at random, leave 5/8 of the
-    // adapters with rows, a tile each (4096 x 4096, rank 16, us with 2 / 4 / 8 blocks: 48 of each 15.2 / 10.3 / 7.9, 64
-    // of each 16.9 / 11.5 / 15.3, 512 rows of 8 adapters 17.0 / 11.1 / 10.2).
+    // 8 blocks for a few rows (16 rows of 16 adapters 4.6 us; 4 blocks 5.4), fewer where the tiles alone fill the GPU
+    // (1024 rows 23 us with 4, 28 with 8). As many rows as adapters, each row's drawn at random, leave 5/8 of the
+    // adapters with rows, a tile each (4096 x 4096, rank 16, us with 2 / 4 / 8 blocks: 48 of each 11.7 / 8.2 / 6.5, 64
+    // of each 12.8 / 9.2 / 11.7, 512 rows of 8 adapters 13.9 / 9.0 / 9.3).
     const int blocks = blocks_of(a.M / 16 + (long long)(a.L < a.M ? a.L : a.M) * 5 / 8, kTargetSms * 9 / 4);
     switch (rank) {
         case 16: return launch<BF, YDT, 1>(a, blocks, s);
