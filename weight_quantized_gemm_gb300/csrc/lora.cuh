@@ -168,7 +168,7 @@ __device__ __forceinline__ void add_edge(void* y, const float (&d)[8], float sca
 // [0, M] and to the largest before them. Every thread of the block calls it.
 //
 // Up to 32 adapters each warp looks by itself; more are shared between the block's threads, neighbouring adapters a
-// thread (128 rows of 1000 adapters 21 us; with 32 at a time in every warp 34).
+// thread (96 rows of 1000 adapters, 4096 x 4096, 22 us; with 32 at a time in every warp 36).
 struct TileSearch {
     int most[kWarps], tiles[kWarps], l, from, count;
 };

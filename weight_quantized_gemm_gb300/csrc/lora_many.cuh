@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
     __shared__ float s_unit[kManyRows];         // f16: the power of two that a row of H was divided by
     const LoraArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int blocks = (int)cluster_size(), rank_in = blocks > 1 ? (int)cluster_rank() : 0;
+    const int blocks = (int)cluster_size(), shift = __ffs(blocks) - 1, rank_in = blocks > 1 ? (int)cluster_rank() : 0;      // (a power of two, of 8 at most)
     const uint32_t ring = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;       // (the same offset in every block)
     const uint32_t H = ring + S::kRing;
     const uint32_t bar = ptx::smem_u32(s_bar);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
     grid_wait();
     grid_release();
     int l = 0, from = 0, count = 0;
-    const bool any = find_tile(a, blockIdx.x / blocks, kManyRows, s_tile, l, from, count);
+    const bool any = find_tile(a, blockIdx.x >> shift, kManyRows, s_tile, l, from, count);
     const int rank = !any ? 0 : (a.rank ? min(max(load(a.rank + l), 0), a.R) : a.R);
     if (rank > 0) {             // (the same for the whole cluster)
         const float scale = a.scale ? load(a.scale + l) : 1.f;
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
 
         // ---- D1 = X A^T over this block's part of K
         const int steps = a.K / 64;
-        const int s0 = (int)((long long)steps * rank_in / blocks), n1 = (int)((long long)steps * (rank_in + 1) / blocks) - s0;
+        const int s0 = steps * rank_in >> shift, n1 = (steps * (rank_in + 1) >> shift) - s0;        // (K <= 2^30)
         {
             constexpr int kXC = kManyRows / 32, kAC = (RP + 31) / 32;
             const uint8_t* x[kXC];
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
 
         // ---- the second product's first turn comes while the blocks join their parts of H (behind which it has room)
         const int turns = (a.N + kTurnCols - 1) / kTurnCols;
-        const int t0 = (int)((long long)turns * rank_in / blocks), n2 = (int)((long long)turns * (rank_in + 1) / blocks) - t0;
+        const int t0 = turns * rank_in >> shift, n2 = (turns * (rank_in + 1) >> shift) - t0;        // (N <= 2^30)
         const bool wide = a.ldy % (16 / kYSize) == 0;
         constexpr int kPer = 16 / kYSize, kYC = kManyRows / 32;        // values of a 16-byte piece; pieces of a thread
         const uint32_t y_to = swizzled<128>(r8, c8);
