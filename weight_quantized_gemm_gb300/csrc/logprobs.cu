@@ -9,7 +9,7 @@
 // held to -200 from below, which makes both terms 0 and takes in -inf and NaN, too: the larger of NaN and -200 is -200.
 // Rows whose largest value times c is 2^22 or more are summed a second time, from differences of values.
 //
-// The k likeliest: each thread keeps its largest value and the place where it found it first. The k best of those
+// The k likeliest: each thread keeps its largest value and the pieces in which it found it first. The k best of those
 // (by value, then place) belong to k threads that must hold the row's k best values: any other thread has k
 // values before its own best one. Of these, what is not below the k-th best is read again and put in order; the largest
 // value of each thread's every kUnroll pieces is kept beside, so that few pieces are read (with all of these threads'
@@ -23,6 +23,8 @@
 // sums and lists meet in the first block through distributed shared memory.
 #include <float.h>
 
+#include <type_traits>
+
 #include "serve.cuh"
 
 namespace qg {
@@ -30,6 +32,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kUnroll = 8;                 // 16-byte loads that a thread has in flight
+constexpr int kTogether = 4;               // pieces that are summed between two looks at the largest value
 constexpr int kRuns = 16;                  // largest values that a thread keeps
 constexpr int kQuickRuns = kThreads, kQuickKeys = kThreads;
 constexpr int kMaxCluster = 8;
@@ -141,6 +144,25 @@ struct Row {
         if (v * kPer >= skip && (v + 1) * kPer <= end) return load(reinterpret_cast<const uint4*>(from) + v);
         return edge(v);
     }
+    // The largest of N pieces' values, NaN left out.
+    template <int N>
+    __device__ __forceinline__ static float largest(const uint4* raw) {
+        if constexpr (DT == DT_F32) {
+            float m = __uint_as_float(raw[0].x);
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(raw[u].x)), __uint_as_float(raw[u].y)), fmaxf(__uint_as_float(raw[u].z), __uint_as_float(raw[u].w)));
+            return m;
+        } else {        // two at a time
+            using T = std::conditional_t<DT == DT_F16, __half2, __nv_bfloat162>;
+            const T* p = reinterpret_cast<const T*>(raw);
+            T m[4] = {p[0], p[1], p[2], p[3]};
+#pragma unroll
+            for (int i = 4; i < 4 * N; ++i) m[i & 3] = __hmax2(m[i & 3], p[i]);
+            const T all = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+            return fmaxf(__low2float(all), __high2float(all));
+        }
+    }
     __device__ __forceinline__ static void values(const uint4& raw, float (&x)[kPer]) {
         const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
@@ -209,7 +231,7 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     using R = Row<DT>;
     constexpr int P = R::kPer;
-    __shared__ Key lists[kWarps][32];
+    __shared__ __align__(16) Key lists[kWarps][32];
     __shared__ Key best[32];            // the block's threads with the largest values, then its largest values
     __shared__ Key found[kQuickKeys];
     __shared__ float runs[kRuns][kThreads];        // each thread's, the largest values of its runs of pieces
@@ -253,12 +275,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     // a run is `per` turns of kUnroll pieces of a thread
     const int turns = (v1 - v0 + kUnroll * kThreads - 1) / (kUnroll * kThreads), per = (turns + kRuns - 1) / kRuns;
     float run_most = neg_inf();
-    auto take = [&](const uint4& raw, int v) {
-        float x[P];
-        R::values(raw, x);
-        float here = x[0];
-#pragma unroll
-        for (int j = 1; j < P; ++j) here = fmaxf(here, x[j]);
+    // N pieces, the first of which is piece v: one look at their largest value, then sums without branches.
+    auto take = [&](auto count, const uint4* raw, int v) {
+        constexpr int N = decltype(count)::value;
+        const float here = R::template largest<N>(raw);
         run_most = fmaxf(run_most, here);
         if (here > most) {
             most = here;
@@ -274,19 +294,29 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
             limit = here + slack;
         }
 #pragma unroll
-        for (int j = 0; j < P; j += 2) {
-            float t0, t1;
-            unpack2(fma2(pack2(x[j], x[j + 1]), c2, minus2), t0, t1);
-            t0 = fmaxf(t0, -200.f);
-            t1 = fmaxf(t1, -200.f);
-            const uint64_t p2 = pack2(exp2_fast(t0), exp2_fast(t1));
-            s2 = add2(s2, p2);
-            e2 = fma2(p2, pack2(t0, t1), e2);
+        for (int u = 0; u < N; ++u) {
+            float x[P];
+            R::values(raw[u], x);
+#pragma unroll
+            for (int j = 0; j < P; j += 2) {
+                float t0, t1;
+                unpack2(fma2(pack2(x[j], x[j + 1]), c2, minus2), t0, t1);
+                t0 = fmaxf(t0, -200.f);
+                t1 = fmaxf(t1, -200.f);
+                const uint64_t p2 = pack2(exp2_fast(t0), exp2_fast(t1));
+                s2 = add2(s2, p2);
+                e2 = fma2(p2, pack2(t0, t1), e2);
+            }
         }
     };
+    using One = std::integral_constant<int, 1>;
+    using Some = std::integral_constant<int, kTogether>;
     // The row's first and last piece may be cut: by themselves, in their place in the order of each thread's pieces.
     const int whole0 = max(v0, row.skip ? 1 : 0), whole1 = min(v1, row.end / P);
-    if (tid == 0 && v0 < min(whole0, v1)) take(row.edge(v0), v0);
+    if (tid == 0 && v0 < min(whole0, v1)) {
+        const uint4 raw = row.edge(v0);
+        take(One(), &raw, v0);
+    }
     int turn = 0, run = 0;          // turns of the run at hand
     for (int v = v0; v < whole1; v += kUnroll * kThreads) {
         const uint4* from = reinterpret_cast<const uint4*>(row.from) + v + tid;
@@ -295,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) raw[u] = load(from + u * kThreads);
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) take(raw[u], v + tid + u * kThreads);
+            for (int u = 0; u < kUnroll; u += kTogether) take(Some(), raw + u, v + tid + u * kThreads);
         } else {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
@@ -304,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
                 if (w >= whole0 && w < whole1) raw[u] = load(from + u * kThreads);
             }
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (v + u * kThreads < whole1) take(raw[u], v + tid + u * kThreads);
+            for (int u = 0; u < kUnroll; u += kTogether)
+                if (v + u * kThreads < whole1) take(Some(), raw + u, v + tid + u * kThreads);
         }
         if (++turn == per) {
             runs[run++][tid] = run_most;
@@ -317,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     if (const int last = max(whole1, v0); last < v1 && last >= whole0 && tid == (last - v0) % kThreads) {
         const bool again = turn == 0 && run > 0 && (last - v0) / (kUnroll * kThreads * per) < run;
         if (again) run_most = runs[run - 1][tid];
-        take(row.edge(last), last);
+        const uint4 raw = row.edge(last);
+        take(One(), &raw, last);
         if (again) runs[run - 1][tid] = run_most;
     }
     for (; run * per < turns; ++run) {
@@ -355,7 +386,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
         };
         auto key_of = [&](float x, int v, int i) { return (Key)to_key(x) << 32 | (uint32_t)~(v * P + i - row.skip); };
         if (tid == 0) s_which = s_found = 0;
-        const uint32_t kth = merge_warps(sorted(high, lane), kWarps, reinterpret_cast<uint32_t(*)[32]>(lists), warp, lane);
+        if (warp == 0) best[lane] = 0;
+        auto rows = reinterpret_cast<uint32_t(*)[32]>(lists);
+        const uint32_t kth = merge_warps(sorted(high, lane), kWarps, rows, warp, lane);
         if (tid == a.k - 1) s_least = kth;
         __syncthreads();
         uint32_t least = s_least;       // 0: fewer than k threads hold any value
@@ -390,15 +423,22 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
             const int n = s_found;
             quick = n <= kQuickKeys;
             if (quick) {
-                int count = 1;
-                while (count * 32 < n) count <<= 1;
-                Key key = tid < n ? found[tid] : 0;
-                if (warp < count) key = sorted(key, lane);
-                key = merge_warps(key, count, lists, warp, lane);
-                if (warp == 0) best[lane] = key;
+                if (tid < n) {          // keys differ: a key's place is the number of those above it
+                    const Key key = found[tid];
+                    int place = 0;
+#pragma unroll 4
+                    for (int j = 0; j < n; ++j) place += found[j] > key;
+                    if (place < 32) best[place] = key;
+                }
             }
         }
         if (!quick) {
+            // the first piece that holds the largest value is among those taken together
+            if (high != 0)
+                for (int u = 0; u < kTogether && place < v1; ++u, place += kThreads) {
+                    const uint4 raw = row.piece(place);
+                    if (R::template largest<1>(&raw) == most) break;
+                }
             Key key = high ? (Key)high << 32 | (uint32_t)~place : 0;
             key = merge_warps(sorted(key, lane), kWarps, lists, warp, lane);
             if (warp == 0) best[lane] = key;
@@ -434,8 +474,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
 
     // ---- the row's, by the cluster's first block
     float4 all;
+    Key theirs = 0;         // of the warp's block
     if (blocks > 1) {
         cluster_sync();
+        if (rank == 0 && a.k > 0 && warp < (int)blocks) theirs = ld_cluster_u64(in_block(&best[lane], warp));
         float4 part[kMaxCluster];
         top = neg_inf();
 #pragma unroll
@@ -499,8 +541,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
         }
         if (a.k > 0) {
             if (blocks > 1) {
-                Key key = warp < (int)blocks ? ld_cluster_u64(in_block(&best[lane], warp)) : 0;
-                key = merge_warps(key, (int)blocks, lists, warp, lane);
+                const Key key = merge_warps(theirs, (int)blocks, lists, warp, lane);
                 if (warp == 0) best[lane] = key;
             }
             if (tid < a.k) {
