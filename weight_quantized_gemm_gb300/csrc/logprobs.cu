@@ -405,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
         bool quick = reached <= kQuickRuns;
         if (quick) {
             const int each = per * kUnroll;     // pieces of a run
-            for (long long i = tid; i < (long long)reached * each; i += kThreads) {
-                const int j = (int)(i / each), at = which[j];
-                const int v = v0 + at % kThreads + (at / kThreads * each + (int)(i % each)) * kThreads;
+            for (uint32_t i = tid; i < (uint32_t)(reached * each); i += kThreads) {       // (V <= 2^30: below 2^24)
+                const int j = (int)(i / (uint32_t)each), at = which[j];
+                const int v = v0 + at % kThreads + (at / kThreads * each + (int)i - j * each) * kThreads;
                 if (v >= v1) continue;
                 float x[P];
                 const uint32_t left = reach(v, least, x);
