@@ -64,9 +64,11 @@ struct ManyParams {
     int stall;
 };
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool any) {     // zeros where there is nothing to copy
+// 16 bytes, zeros where there is nothing to copy. L2 fetches 256 bytes from HBM at a time, the next stage's or turn's 128 with
+// this one's (8192 x 4096 x 14336 at rank 16 100.9 -> 98.3 us, at rank 64 131.9 -> 125.2).
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool any) {
     const int bytes = any ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -143,12 +145,13 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
     grid_release();
     int l = 0, from = 0, count = 0;
     const bool any = find_tile(a, blockIdx.x >> shift, kManyRows, s_tile, l, from, count);
+    // (the rows, the rank and the scale are asked for together)
+    const int m_here = any && tid < count ? load(a.row + from + tid) : -1;
+    const float scale = any && a.scale ? load(a.scale + l) : 1.f;
     const int rank = !any ? 0 : (a.rank ? min(max(load(a.rank + l), 0), a.R) : a.R);
     if (rank > 0) {             // (the same for the whole cluster)
-        const float scale = a.scale ? load(a.scale + l) : 1.f;
         if (tid < kManyRows) {
-            const int m = tid < count ? load(a.row + from + tid) : -1;
-            s_row[tid] = m < a.M ? m : -1;
+            s_row[tid] = m_here < a.M ? m_here : -1;
             s_unit[tid] = 1.f;
         }
         __syncthreads();
