@@ -106,6 +106,19 @@ def test_in_place(K):
 
 
 @pytest.mark.parametrize("kind", [qg.NORM_RMS, qg.NORM_LAYER])
+@pytest.mark.parametrize("x_dtype,s_dtype", [(qg.BF16, qg.F32), (qg.F16, qg.F16), (qg.F32, qg.BF16)])
+@pytest.mark.parametrize("M,K", [(4000, 256), (4000, 320), (1500, 1088), (1000, 2240), (500, 4096), (460, 4160), (310, 5120), (310, 5184), (310, 6144), (310, 6208),
+                                 (310, 8192)])
+def test_more_rows_than_the_gpu_takes_at_once(M, K, x_dtype, s_dtype, kind):
+    """Several pieces of a row to a thread; S over the residual."""
+    c = make(M, K, kind, x_dtype, s_dtype, x_dtype, gate="row")
+    s, es, y, ey = want(c)
+    S, Y = run(c, S=c["residual"])
+    ref.check(S, s, es)
+    ref.check(Y, y, ey)
+
+
+@pytest.mark.parametrize("kind", [qg.NORM_RMS, qg.NORM_LAYER])
 def test_a_large_mean(kind):
     """Values 1000 +- 1: the variance is not the difference of two sums."""
     check(make(4, 4096, kind, qg.F32, qg.F32, qg.F32, post=0, gate="none", residual=False, mean=1000.0))

@@ -20,12 +20,16 @@
 namespace qg {
 namespace norm {
 
-// Threads of a block at most, and blocks an SM at least (which bounds the registers).
-template <int MAXT>
-constexpr int kBlocks = MAXT <= 128 ? 6 : (MAXT <= 192 ? 4 : (MAXT <= 320 ? 2 : 1));
+// Threads of a block at most, and blocks an SM at least (which bounds the registers): of rows above 5120 and up to 8192
+// values three blocks or more (16384 x 8192 in bf16, 80 registers a thread, 195 -> 170 us; x 6144 138 -> 126). Longer rows would lose
+// more to the stack than they gain (x 9728 222 us with two blocks, 241 with three), but with a residual in float32 that
+// is asked for only where it is added (kLate): 1023 x 9728 36.4 -> 34.4 us, x 8192 32.9 -> 26.6, x 6144 25.8 -> 21.1; rows
+// up to 5120 lose by that (20.8 -> 22.2).
+template <int SDT, int MAXT>
+constexpr int kBlocks = MAXT <= 128 ? 6 : (MAXT <= 192 ? 4 : (MAXT <= 256 ? 3 : (MAXT <= 320 ? (SDT == DT_F32 ? 3 : 2) : 1)));
 
 template <int XDT, int SDT, int YDT, int CH, int MAXT>
-__global__ void __launch_bounds__(MAXT, kBlocks<MAXT>) norm_kernel(const NormArgs a, const float per) {
+__global__ void __launch_bounds__(MAXT, kBlocks<SDT, MAXT>) norm_kernel(const NormArgs a, const float per) {
     // a slot for each reduction, so that one barrier each is enough
     __shared__ __align__(16) float part[4][32];
     const int t = threadIdx.x, threads = blockDim.x, warps = threads >> 5, pieces = a.K >> 3;
@@ -40,7 +44,8 @@ __global__ void __launch_bounds__(MAXT, kBlocks<MAXT>) norm_kernel(const NormArg
     grid_release();
     float f[CH][8];
     Eight<XDT> x[CH], gate[CH];
-    Eight<SDT> res[CH];
+    constexpr bool kLate = SDT == DT_F32 && MAXT > 192 && MAXT <= 320;
+    Eight<SDT> res[kLate ? 1 : CH];
     bool live[CH];
     {
         const size_t x0 = (size_t)(m * a.ldx), r0 = (size_t)(m * a.K), g0 = (size_t)(m * a.ldg);
@@ -51,10 +56,10 @@ __global__ void __launch_bounds__(MAXT, kBlocks<MAXT>) norm_kernel(const NormArg
             if (live[c]) x[c].fetch(a.X, x0 + p * 8);
             else x[c] = Eight<XDT>{};           // adds nothing to the sums
         }
-        if (a.residual)
+        if (!kLate && a.residual)
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-                if (live[c]) res[c].fetch(a.residual, r0 + (c * threads + t) * 8);
+                if (live[c]) res[kLate ? 0 : c].fetch(a.residual, r0 + (c * threads + t) * 8);
         if (a.gate)
 #pragma unroll
             for (int c = 0; c < CH; ++c)
@@ -121,7 +126,8 @@ __global__ void __launch_bounds__(MAXT, kBlocks<MAXT>) norm_kernel(const NormArg
             for (int j = 0; j < 8; ++j) f[c][j] *= v[j];
         }
         if (a.residual) {
-            res[c].values(v);
+            if (kLate) res[0].fetch(a.residual, row + p * 8);
+            res[kLate ? 0 : c].values(v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[c][j] = fmaf(a.r_scale, v[j], f[c][j]);
         }
@@ -178,6 +184,8 @@ cudaError_t launch_y(const NormArgs& a, cudaStream_t s) {
     // row is little longer than a whole number of its warps' pieces.
     if (3 * threads_of(pieces, 4) > pieces) return launch_ch<XDT, SDT, YDT, 2, 192>(a, s);
     if (pieces <= 4 * 128) return launch_ch<XDT, SDT, YDT, 4, 128>(a, s);
+    if (pieces <= 4 * 160) return launch_ch<XDT, SDT, YDT, 4, 160>(a, s);
+    if (pieces <= 4 * (SDT == DT_F32 ? 192 : 256)) return launch_ch<XDT, SDT, YDT, 4, 256>(a, s);
     if (pieces <= 4 * 320) return launch_ch<XDT, SDT, YDT, 4, 320>(a, s);
     return launch_ch<XDT, SDT, YDT, 4, 1024>(a, s);
 }
