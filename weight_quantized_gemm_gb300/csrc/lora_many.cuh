@@ -12,13 +12,14 @@
 // RP: the ranks rounded up to a power of two; what lies past an adapter's rank is filled with zeros.
 //
 // There are few operations to a byte, so HBM's bytes are the floor: X, Y and Y again. 8192 x 4096 x 14336 at rank 16 in
-// bf16 takes 102 us (5.3 TB/s; a kernel that does nothing but add 1 to that Y in 128-byte runs takes 80 for its 470 MB,
-// and 67 MB of X come on top), at rank 64 133; 4099 x 2560 x 2560 at rank 128 29 us, of which 11 are the launch (one block
-// an SM, so that the next call's blocks wait for this one's), the join and the chain to the first store. With 16x8x16
-// steps from registers, as in lora.cuh, these took 109, 189 and 61 us: 12 instructions a value of Y, and the loads that feed
+// bf16 takes 98 us (5.5 TB/s; a kernel that does nothing but add 1 to that Y in 128-byte runs takes 80 for its 470 MB,
+// and 67 MB of X come on top), at rank 64 125; 4099 x 2560 x 2560 at rank 128 28 us, with one block an SM, in which the first
+// product takes 6.6 (1260 cycles a stage of 32 KB), the join 4 and a turn 1.1. With 16x8x16 steps from registers, as in
+// lora.cuh, these took 109, 189 and 61 us: 12 instructions a value of Y, and the loads that feed
 // such steps. Waiting for all memory before each turn's products, and not for shared memory alone, made 102 us 151.
 // One block an SM whose warps add to Y without block barriers (a warp its own rows, groups of warps in turns) took the
-// same 103 us at rank 16, and 159 and 40 us at ranks 64 and 128, where the one warp that fed the products fell behind.
+// same time at rank 16, and 159 and 40 us at ranks 64 and 128, where the one warp that fed the products fell behind. A and B by
+// tiled copies of one thread, with the ranks past the adapter's masked, changed nothing (28.1 -> 29.2 us at rank 128).
 //
 // Every wait is bounded (see ptx.cuh). After a wait that ran out the blocks still meet at the cluster's barriers, wait
 // for the MMAs in flight and release their tensor memory.
@@ -490,7 +491,7 @@ cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
     // rank 16 2048 rows 42 / 51, 2900 rows 74 / 53; rank 32 1500 rows 46 / 45; rank 64 1024 rows 37 / 48, 1300 rows 65 / 49;
     // rank 128 512 rows 45 / 47, 900 rows 60 / 49, and 2560 x 2560 768 rows 20 / 19, 1024 rows 21 / 19). The cluster's size
     // fills the SMs once (two blocks an SM, one at rank 128), with the number of tiles guessed from M and L, since the host
-    // does not see the offsets: 8192 rows 102 us with 4 blocks, 117 with 8, 142 with 2.
+    // does not see the offsets: of 8192 rows, 4 blocks take 102 us, 8 117 and 2 142 (before L2 fetched 256 bytes).
     const int rank = a.R <= 16 ? 16 : (a.R <= 32 ? 32 : (a.R <= 64 ? 64 : 128));
     const int from = rank == 16 ? 2304 : (rank == 32 ? 1536 : (rank == 64 ? 1280 : 768));
     if (a.R <= 128 && a.M >= from) {

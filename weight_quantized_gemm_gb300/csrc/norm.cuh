@@ -23,8 +23,8 @@ namespace norm {
 // Threads of a block at most, and blocks an SM at least (which bounds the registers): of rows above 5120 and up to 8192
 // values three blocks or more (16384 x 8192 in bf16, 80 registers a thread, 195 -> 170 us; x 6144 138 -> 126). Longer rows would lose
 // more to the stack than they gain (x 9728 222 us with two blocks, 241 with three), but with a residual in float32 that
-// is asked for only where it is added (kLate): 1023 x 9728 36.4 -> 34.4 us, x 8192 32.9 -> 26.6, x 6144 25.8 -> 21.1; rows
-// up to 5120 lose by that (20.8 -> 22.2).
+// is asked for only where it is added (kLate): 1023 x 9728 36.4 -> 34.4 us, x 8192 32.9 -> 26.6, x 6144 25.8 -> 21.1,
+// 2000 x 16384 119 -> 92; rows up to 5120 lose by that (20.8 -> 22.2).
 template <int SDT, int MAXT>
 constexpr int kBlocks = MAXT <= 128 ? 6 : (MAXT <= 192 ? 4 : (MAXT <= 256 ? 3 : (MAXT <= 320 ? (SDT == DT_F32 ? 3 : 2) : 1)));
 
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(MAXT, kBlocks<SDT, MAXT>) norm_kernel(const No
     grid_release();
     float f[CH][8];
     Eight<XDT> x[CH], gate[CH];
-    constexpr bool kLate = SDT == DT_F32 && MAXT > 192 && MAXT <= 320;
+    constexpr bool kLate = SDT == DT_F32 && MAXT > 192 && CH > 1;
     Eight<SDT> res[kLate ? 1 : CH];
     bool live[CH];
     {
