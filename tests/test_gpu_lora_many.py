@@ -23,6 +23,15 @@ def test_many_rows(M, K, N, L, R, dtype, y_dtype):
     check(make(M, K, N, L, R, dtype, y_dtype, mixed(M, L, M), seed=M + R, ragged=M % 100 == 0))
 
 
+@pytest.mark.parametrize("dtype", [qg.F16, qg.BF16])
+@pytest.mark.parametrize("y_dtype", [qg.F32, qg.BF16])
+@pytest.mark.parametrize("M,K,N,L,R", [(1000, 320, 136, 3, 136), (900, 1024, 72, 2, 200), (1500, 512, 200, 4, 256), (256, 64, 33, 1, 256),
+                                       (257, 2560, 264, 70, 144)])
+def test_ranks_above_128(M, K, N, L, R, dtype, y_dtype):
+    check(make(M, K, N, L, R, dtype, y_dtype, mixed(M, L, M), seed=M + R, ragged=True))
+    check(make(M, K, N, L, R, dtype, y_dtype, mixed(M, L, M), seed=M + R + 1))
+
+
 @pytest.mark.parametrize("pad_x,pad_y", [(0, 1), (8, 3), (64, 8), (0, 4)])
 @pytest.mark.parametrize("y_dtype", [qg.F32, qg.BF16])
 def test_strides(pad_x, pad_y, y_dtype):
@@ -116,7 +125,7 @@ def test_two_at_once_and_in_a_graph():
         assert torch.equal(c["Y"], w)
 
 
-@pytest.mark.parametrize("M,R", [(2304, 16), (1300, 64), (900, 128)])
+@pytest.mark.parametrize("M,R", [(2304, 16), (1300, 64), (900, 128), (300, 256)])
 def test_waits_that_run_out(M, R):
     """One wait runs out on purpose: the call returns, the status says so, and the next calls give their bits."""
     c = make(M, 512, 200, 3, R, qg.BF16, qg.BF16, mixed(M, 3))

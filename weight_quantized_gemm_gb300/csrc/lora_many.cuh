@@ -1,5 +1,6 @@
 // The adapters' products for batches of many rows, on the tensor cores' asynchronous path (lora.cuh has the few rows, and
-// the mathematics): Y[m] += scale_l B_l (A_l X[m]), a cluster of blocks to a tile of 128 rows of one adapter.
+// the mathematics): Y[m] += scale_l B_l (A_l X[m]), a cluster of blocks to a tile of 128 rows of one adapter (64 at ranks
+// above 128).
 //
 //   first product   D1 = X A^T (128 x RP) in tensor memory, a ring of stages of 64 of K (rows of 128 bytes in the
 //                   128-byte swizzle) filled by asynchronous copies of all threads, since the rows of a tile lie
@@ -31,30 +32,33 @@
 namespace qg {
 namespace lora {
 
-constexpr int kManyRows = 128;
+constexpr int kManyRows = 128;          // of a tile, and of the tensor cores' products
 constexpr int kMaxBlocks = 8;           // of a cluster
 
 template <int YDT, int RP, int TERMS>
 struct Many {
     static constexpr int kYSize = YDT == DT_F32 ? 4 : 2;
+    // Rows of a tile: with 256 ranks H of 128 would not fit. The products are formed of 128 all the same; what they read
+    // behind a tile's rows is other operands' memory, and what comes of it is not used.
+    static constexpr int kRows = RP > 128 ? 64 : kManyRows;
     // The warp that issues the products: one of the eight, or where a turn has 16 of them or more one of its own (4099 x 2560 x
     // 2560 at rank 128: 31 -> 29 us; at ranks up to 64 two blocks an SM lose more by it than they gain).
     static constexpr int kIssuer = RP > 64 ? kWarps : 0, kAll = RP > 64 ? kThreads + 32 : kThreads;
     static constexpr int kCols = 128 / kYSize;                                         // of a turn: 128 bytes of a row of Y
-    static constexpr int kX = kManyRows * 128, kStage = kX + RP * 128;                  // a stage: X's rows, A's ranks
+    static constexpr int kX = kRows * 128, kStage = kX + RP * 128;                  // a stage: X's rows, A's ranks
     static constexpr int kBPitch = RP < 64 ? RP * 2 : 128, kBAtoms = (RP + 63) / 64;    // bytes of a column of B, 64 ranks at a time
-    static constexpr int kY = kManyRows * 128, kB = kBAtoms * kCols * kBPitch, kTurn = kY + kB;
-    static constexpr int kHAtoms = (TERMS * RP + 63) / 64, kH = kHAtoms * kManyRows * 128;
+    static constexpr int kY = kRows * 128, kB = kBAtoms * kCols * kBPitch, kTurn = kY + kB;
+    static constexpr int kHAtoms = (TERMS * RP + 63) / 64, kHAtom = kRows * 128, kH = kHAtoms * kHAtom + (kManyRows - kRows) * 128;
     static constexpr int kRoom = (RP <= 64 ? 112 << 10 : 225 << 10) - kH - 2048;        // two blocks an SM where they fit
     static constexpr int kTurns = kRoom / kTurn < 5 ? kRoom / kTurn : 5;                // ring of turns
     static constexpr int kStages = kTurns * kTurn / kStage < 5 ? kTurns * kTurn / kStage : 5;
     // the first product's stages go to kSums accumulators in turn: the tensor cores cut sums off, and shorter chains lose less
-    static constexpr int kSums = RP <= 64 ? 128 / RP : 2, kD2 = kSums * RP, kTmem = RP <= 64 ? 256 : 512;
+    static constexpr int kSums = RP <= 64 ? 128 / RP : 256 / RP, kD2 = kSums * RP, kTmem = RP <= 64 ? 256 : 512;
     static constexpr int kPartPitch = RP + 4;                                          // floats: 16-byte writes of 8 rows meet no bank twice
     static constexpr int kRing = kTurns * kTurn;
     static constexpr size_t kSmem = 1024 + kRing + kH;
     static_assert(kTurns >= 3 && kStages >= 2 && kTurn % 1024 == 0 && kStage % 1024 == 0, "rings");
-    static_assert(kManyRows * kPartPitch * 4 <= (kTurns - 1) * kTurn, "the parts of H take the ring's place but for one turn's");
+    static_assert(kRows * kPartPitch * 4 <= (kTurns - 1) * kTurn, "the parts of H take the ring's place but for one turn's");
     static_assert(3 * kSmem > (228 << 10), "at most two blocks an SM, whose tensor memory is there");
 };
 
@@ -145,13 +149,13 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
     grid_wait();
     grid_release();
     int l = 0, from = 0, count = 0;
-    const bool any = find_tile(a, blockIdx.x >> shift, kManyRows, s_tile, l, from, count);
+    const bool any = find_tile(a, blockIdx.x >> shift, S::kRows, s_tile, l, from, count);
     // (the rows, the rank and the scale are asked for together)
     const int m_here = any && tid < count ? load(a.row + from + tid) : -1;
     const float scale = any && a.scale ? load(a.scale + l) : 1.f;
     const int rank = !any ? 0 : (a.rank ? min(max(load(a.rank + l), 0), a.R) : a.R);
     if (rank > 0) {             // (the same for the whole cluster)
-        if (tid < kManyRows) {
+        if (tid < S::kRows) {
             s_row[tid] = m_here < a.M ? m_here : -1;
             s_unit[tid] = 1.f;
         }
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
         const int steps = a.K / 64;
         const int s0 = steps * rank_in >> shift, n1 = (steps * (rank_in + 1) >> shift) - s0;        // (K <= 2^30)
         {
-            constexpr int kXC = kManyRows / 32, kAC = (RP + 31) / 32;
+            constexpr int kXC = S::kRows / 32, kAC = (RP + 31) / 32;
             const uint8_t* x[kXC];
             uint32_t live = 0;
 #pragma unroll
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
         const int turns = (a.N + kTurnCols - 1) / kTurnCols;
         const int t0 = turns * rank_in >> shift, n2 = (turns * (rank_in + 1) >> shift) - t0;        // (N <= 2^30)
         const bool wide = a.ldy % (16 / kYSize) == 0;
-        constexpr int kPer = 16 / kYSize, kYC = kManyRows / 32;        // values of a 16-byte piece; pieces of a thread
+        constexpr int kPer = 16 / kYSize, kYC = S::kRows / 32;        // values of a 16-byte piece; pieces of a thread
         const uint32_t y_to = swizzled<128>(r8, c8);
         // A turn is whole where all of its columns are there and rows of Y start 16-byte aligned. This thread's pieces of the
         // turn that is stored; those of the turn that is fetched lie kAhead turns further on. Rows that are not there
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
 #pragma unroll
         for (int c = 0; c < RP; c += 32) {
             float v[16];
-            if (copier && c + half * 16 < RP) {
+            if (copier && row < S::kRows && c + half * 16 < RP) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = 0.f;
                 for (int d = 0; d < min(n1, S::kSums); ++d) {
@@ -305,51 +309,60 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
 
         // ---- this block's share of the rows: summed, and their terms to every block
         {
-            constexpr int kLanes = RP / 4;      // of a row, 4 values each
-            const int rows = kManyRows / blocks;
+            constexpr int kLanes = RP < 128 ? RP / 4 : 32, kSets = RP / 4 / kLanes;      // of a row, sets of 4 values each
+            const int rows = S::kRows >> shift;
             for (int i = tid; i < rows * kLanes; i += S::kAll) {
-                const int r = rank_in * rows + i / kLanes, c = i % kLanes * 4;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int b0 = 0; b0 < blocks; b0 += 4) {
-                    float4 o[4];
+                const int r = rank_in * rows + i / kLanes;
+                float x[kSets][4], most = 0.f;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        if (b0 + b < blocks) o[b] = ld_cluster_f32x4(in_block(part + r * S::kPartPitch + c, b0 + b));
+                for (int e = 0; e < kSets; ++e) {
+                    const int c = (i % kLanes + e * kLanes) * 4;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int b0 = 0; b0 < blocks; b0 += 4) {
+                        float4 o[4];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        if (b0 + b < blocks) {
-                            v.x += o[b].x; v.y += o[b].y; v.z += o[b].z; v.w += o[b].w;
-                        }
+                        for (int b = 0; b < 4; ++b)
+                            if (b0 + b < blocks) o[b] = ld_cluster_f32x4(in_block(part + r * S::kPartPitch + c, b0 + b));
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b0 + b < blocks) {
+                                v.x += o[b].x; v.y += o[b].y; v.z += o[b].z; v.w += o[b].w;
+                            }
+                    }
+                    x[e][0] = v.x; x[e][1] = v.y; x[e][2] = v.z; x[e][3] = v.w;
+                    most = fmaxf(most, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
                 }
-                float x[4] = {v.x, v.y, v.z, v.w};
                 if constexpr (!BF) {
-                    float t = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-                    for (int o = 1; o < kLanes; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));      // (whole warps are in the loop)
-                    const uint32_t bits = __float_as_uint(t);
+                    for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));      // (whole warps are in the loop)
+                    const uint32_t bits = __float_as_uint(most);
                     const float by = row_unit_inverse(bits);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] *= by;
-                    if (c == 0)
+                    for (int e = 0; e < kSets; ++e)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[e][k] *= by;
+                    if (i % kLanes == 0)
                         for (int b = 0; b < blocks; ++b)
                             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(in_block(&s_unit[r], b)), "f"(row_unit(bits)) : "memory");
                 }
 #pragma unroll
-                for (int t = 0; t < kTerms; ++t) {
-                    uint32_t w[2];
+                for (int e = 0; e < kSets; ++e)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t lo = take_term<BF>(x[2 * k]), hi = take_term<BF>(x[2 * k + 1]);
-                        w[k] = lo | hi << 16;
+                    for (int t = 0; t < kTerms; ++t) {
+                        uint32_t w[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t lo = take_term<BF>(x[e][2 * k]), hi = take_term<BF>(x[e][2 * k + 1]);
+                            w[k] = lo | hi << 16;
+                        }
+                        const int col = t * RP + (i % kLanes + e * kLanes) * 4;
+                        const uint32_t at = H + (col >> 6) * S::kHAtom + swizzled<128>(r, (col & 63) >> 3) + (col & 7) * 2;
+                        for (int b = 0; b < blocks; ++b) {
+                            uint32_t to;
+                            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(b));
+                            asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(w[0]), "r"(w[1]) : "memory");
+                        }
                     }
-                    const int col = t * RP + c;
-                    const uint32_t at = H + (col >> 6) * (kManyRows * 128) + swizzled<128>(r, (col & 63) >> 3) + (col & 7) * 2;
-                    for (int b = 0; b < blocks; ++b) {
-                        uint32_t to;
-                        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(b));
-                        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(w[0]), "r"(w[1]) : "memory");
-                    }
-                }
             }
         }
         to_tensor_cores();
@@ -360,7 +373,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
         // ---- Y += scale H B^T, a turn's columns at a time
         const int chunks = (rank + 15) / 16;
         const float by = scale * s_unit[row];       // exact: a power of two
-        const int my_row = s_row[row];
+        const int my_row = row < S::kRows ? s_row[row] : -1;
         const uint32_t y_cell = swizzled<128>(row, 0);      // (a row's pieces differ in the same three bits)
 #pragma unroll
         for (int d = 1; d < S::kTurns - 2; ++d) fetch(d, d - 1, kAhead - d);
@@ -380,7 +393,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                 for (int t = 0; t < kTerms; ++t)
                     for (int k = 0; k < chunks; ++k) {
                         const int col = t * RP + k * 16;
-                        const uint32_t ha = gg::rows_lo(H + (col >> 6) * (kManyRows * 128)) + ((col & 63) >> 3);
+                        const uint32_t ha = gg::rows_lo(H + (col >> 6) * S::kHAtom) + ((col & 63) >> 3);
                         const uint32_t ba = gg::rows_lo(bt + (k >> 2) * (kTurnCols * 128)) + 2 * (k & 3);
                         mma_async<S::kBPitch>(d, ha, ba, idesc, t > 0 || k > 0);
                     }
@@ -397,21 +410,22 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                 const uint32_t tile = ring + before * S::kTurn;
                 fail = fail || !wait(S::kStages + (v & 1), (uint32_t)(v >> 1) & 1u);
                 gg::tc_fence_after();
+                const bool mine = row < S::kRows;        // (the same for the whole warp)
                 float acc[kHalf];
-                gg::tmem_ld(lanes + S::kD2 + (v & 1) * kTurnCols + half * kHalf, acc);
+                if (mine) gg::tmem_ld(lanes + S::kD2 + (v & 1) * kTurnCols + half * kHalf, acc);
                 constexpr int kV = Eight<YDT>::kVecs;
                 // (what rows that are not there hold in shared memory goes nowhere; all is read before the first is written,
                 // as the compiler keeps the order of these accesses)
                 Eight<YDT> y[kHalf / 8];
-                const bool fast = wide && whole(v);
+                const bool fast = mine && wide && whole(v);
 #pragma unroll
                 for (int j = 0; j < kHalf / 8; ++j)
-                    if (fast || (wide && n + 8 * j + 8 <= a.N))
+                    if (fast || (mine && wide && n + 8 * j + 8 <= a.N))
 #pragma unroll
                         for (int k = 0; k < kV; ++k) y[j].v[k] = read16(tile + (y_cell ^ ((half * 4 + j * kV + k) << 4)));
 #pragma unroll
                 for (int j = 0; j < kHalf / 8; ++j) {
-                    if (fast || (wide && n + 8 * j + 8 <= a.N)) {
+                    if (fast || (mine && wide && n + 8 * j + 8 <= a.N)) {
                         float x[8];
                         y[j].values(x);
 #pragma unroll
@@ -473,7 +487,7 @@ cudaError_t launch_many(const LoraArgs& a, int blocks, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
     if (e != cudaSuccess) return e;
     // at most one tile that is not full for each adapter that has rows
-    const long long tiles = (long long)a.M / kManyRows + (a.L < a.M ? a.L : a.M);
+    const long long tiles = (long long)a.M / S::kRows + (a.L < a.M ? a.L : a.M);
     return launch_behind(kern, dim3((unsigned)(tiles * blocks)), dim3(S::kAll), S::kSmem, (unsigned)blocks, s, p);
 }
 
@@ -492,16 +506,22 @@ cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
     // rank 128 512 rows 45 / 47, 900 rows 60 / 49, and 2560 x 2560 768 rows 20 / 19, 1024 rows 21 / 19). The cluster's size
     // fills the SMs once (two blocks an SM, one at rank 128), with the number of tiles guessed from M and L, since the host
     // does not see the offsets: of 8192 rows, 4 blocks take 102 us, 8 117 and 2 142 (before L2 fetched 256 bytes).
-    const int rank = a.R <= 16 ? 16 : (a.R <= 32 ? 32 : (a.R <= 64 ? 64 : 128));
-    const int from = rank == 16 ? 2304 : (rank == 32 ? 1536 : (rank == 64 ? 1280 : 768));
-    if (a.R <= 128 && a.M >= from) {
-        const int tiles = a.M / kManyRows;
-        const int blocks = blocks_of(tiles + (a.L < tiles ? a.L : tiles), rank == 128 ? kTargetSms : 2 * kTargetSms);
+    const int rank = a.R <= 16 ? 16 : (a.R <= 32 ? 32 : (a.R <= 64 ? 64 : (a.R <= 128 ? 128 : 256)));
+    const int from = rank == 16 ? 2304 : (rank == 32 ? 1536 : (rank == 64 ? 1280 : (rank == 128 ? 768 : 256)));
+    // Ranks above 128 (tiles of 64 rows, as H of more would not fit): from 256 rows on, where two terms stand for H
+    // (2560 x 2560 at rank 256, bf16: 256 rows 28 / 18, 512 rows 37 / 20, 4099 rows 101 / 53; f16 to float32 4099 rows 109 / 79).
+    // With three (bf16 to float32) what H leaves of shared memory is too little (6000 x 8192 x 8192 440 / 572).
+    constexpr bool kWide = terms_of(BF, YDT) == 2;
+    if ((a.R <= 128 || kWide) && a.M >= from) {
+        const int tiles = a.M / (rank > 128 ? 64 : kManyRows);
+        const int blocks = blocks_of(tiles + (a.L < tiles ? a.L : tiles), rank >= 128 ? kTargetSms : 2 * kTargetSms);
         switch (rank) {
             case 16: return launch_many<BF, YDT, 16>(a, blocks, s);
             case 32: return launch_many<BF, YDT, 32>(a, blocks, s);
             case 64: return launch_many<BF, YDT, 64>(a, blocks, s);
-            default: return launch_many<BF, YDT, 128>(a, blocks, s);
+            case 128: return launch_many<BF, YDT, 128>(a, blocks, s);
+            default:
+                if constexpr (kWide) return launch_many<BF, YDT, 256>(a, blocks, s);
         }
     }
     // 8 blocks for a few rows (16 rows of 16 adapters 4.6 us; 4 blocks 5.4), fewer where the tiles alone fill the GPU
