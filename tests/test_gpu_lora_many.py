@@ -18,7 +18,8 @@ def built():
 @pytest.mark.parametrize("dtype,y_dtype", [(qg.F16, qg.F32), (qg.BF16, qg.BF16), (qg.BF16, qg.F32), (qg.F16, qg.BF16)])
 @pytest.mark.parametrize("M,K,N,L,R", [
     (2304, 64, 1, 1, 8), (2500, 192, 129, 3, 16), (2305, 4096, 328, 2, 16), (1600, 448, 250, 40, 24), (1537, 1088, 64, 2, 32), (1300, 704, 191, 5, 40),
-    (2400, 320, 520, 700, 64), (800, 960, 96, 3, 72), (1025, 2560, 264, 1, 128), (9000, 128, 72, 9, 128)])
+    (2400, 320, 520, 700, 64), (800, 960, 96, 3, 72), (4300, 128, 40, 64, 16), (2800, 192, 72, 40, 96),
+    (20000, 64, 24, 300, 8), (1025, 2560, 264, 1, 128), (9000, 128, 72, 9, 128)])
 def test_many_rows(M, K, N, L, R, dtype, y_dtype):
     check(make(M, K, N, L, R, dtype, y_dtype, mixed(M, L, M), seed=M + R, ragged=M % 100 == 0))
 

@@ -511,8 +511,11 @@ cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
     // Ranks above 128 (tiles of 64 rows, as H of more would not fit): from 256 rows on, where two terms stand for H
     // (2560 x 2560 at rank 256, bf16: 256 rows 28 / 18, 512 rows 37 / 20, 4099 rows 101 / 53; f16 to float32 4099 rows 109 / 79).
     // With three (bf16 to float32) what H leaves of shared memory is too little (6000 x 8192 x 8192 440 / 572).
+    // An adapter's rows must fill tiles: 64 of them on average (4096 x 14336, rank 16, rows drawn at random, us: 2400 rows of 100
+    // adapters 75 / 129, of 1000 228 / 1073; 2560 x 2560, rank 128, 1000 rows of 30 23 / 35), 16 at ranks above 128 (300 rows
+    // of 30 33 / 39).
     constexpr bool kWide = terms_of(BF, YDT) == 2;
-    if ((a.R <= 128 || kWide) && a.M >= from) {
+    if ((a.R <= 128 || kWide) && a.M >= from && a.M / (rank > 128 ? 16 : 64) >= a.L) {
         const int tiles = a.M / (rank > 128 ? 64 : kManyRows);
         const int blocks = blocks_of(tiles + (a.L < tiles ? a.L : tiles), rank >= 128 ? kTargetSms : 2 * kTargetSms);
         switch (rank) {
