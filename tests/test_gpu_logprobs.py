@@ -122,6 +122,28 @@ def test_scales(scale):
     check(x, qg.F32, 3001, 5, scale, token)
 
 
+@pytest.mark.parametrize("T,V,ld,place,above", [(1, 5000, 5000, 17, 14.0), (3, 131072, 131072, 99999, 20.0), (300, 9001, 9003, 0, 16.0), (5, 40000, 40001, 39999, 25.0),
+                                                (2, 600, 601, 300, 9.0)])
+@pytest.mark.parametrize("dtype", [qg.F32, qg.BF16])
+def test_rows_that_one_logit_dominates(T, V, ld, place, above, dtype):
+    """-ln p of a token that is nearly certain: small, and good to a few units of its own size. Terms of t below 60 doublings: t is off by
+    3 u t, the powers and rescaled sums by 2^-22 each (4 of them), and n additions a thread and block."""
+    x, token = logits(T, ld, dtype, std=1.0)
+    x[:, place] = above
+    token[:] = place
+    got = run(x, dtype, V, 3, 1.25, token)
+    z = x[:, :V].double() * 1.25
+    rest = torch.exp(z - z[:, place:place + 1])
+    rest[:, place] = 0
+    want = torch.log1p(rest.sum(-1))
+    bound = 4 * 2.0 ** -22 + 3 * 60 * math.log(2) * ref.U + (V / 256 + 64) * ref.U
+    assert bool((want < 0.4).all())
+    assert bool(((got["logprob"].double() + want).abs() <= want * bound).all())
+    assert bool(((got["top_logprob"][:, 0].double() + want).abs() <= want * bound).all())
+    h = want - (torch.where(rest > 0, z - z[:, place:place + 1], 0) * rest).sum(-1) / (1 + rest.sum(-1))
+    assert bool(((got["entropy"].double() - h).abs() <= h * 2 * bound).all())
+
+
 def test_rising_logits_far_apart():
     """Each value far above the ones before: the sums' reference moves at every step."""
     x = (torch.arange(6000, device=DEV).float() * 8)[None].repeat(3, 1)

@@ -8,6 +8,9 @@
 // a float32 in units of t, and the fused product and difference round once, so its own rounding costs nothing. t is
 // held to -200 from below, which makes both terms 0 and takes in -inf and NaN, too: the larger of NaN and -200 is -200.
 // Rows whose largest value times c is 2^22 or more are summed a second time, from differences of values.
+// Where one logit has more than 2/3 of the probability (the usual row of a model that is sure), ln S is ln(1 + rest) with the rest
+// summed without it, so that a token's small -ln p keeps its digits (at 4e-4 an error of 1e-6 of it, and not of 1e-4):
+// 4 x 128000, k = 8 then takes 7.5 us; for the sums that are kept for it a row without such a logit takes 6.5, before 6.2.
 //
 // The k likeliest: each thread keeps its largest value and the pieces in which it found it first. The k best of those
 // (by value, then place) belong to k threads that must hold the row's k best values: any other thread has k
@@ -239,7 +242,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     __shared__ uint32_t s_least;
     __shared__ float s_top[kWarps];
     __shared__ float2 s_sums[kWarps];
-    __shared__ float4 s_again;          // the sums from differences
+    __shared__ float4 s_again;          // the sums a second time
+    __shared__ float2 s_mine[kThreads]; // each thread's sums
+    __shared__ int s_owner;             // a thread that holds the block's largest logit
     __shared__ float4 s_block;          // the block's largest logit, and its sums against that
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t blocks = cluster_size(), rank = blocks > 1 ? cluster_rank() : 0u;
@@ -367,6 +372,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_top[w]);
     Sums sums = sums_now();
     sums.against(in_units(top));
+    s_mine[tid] = make_float2(sums.s, sums.e);
+    if (most == top) s_owner = tid;         // (used where there is one only)
     block_sums(sums, s_sums, warp, lane);
     if (tid == 0) s_block = make_float4(top, sums.s, sums.e, 0.f);
 
@@ -499,17 +506,37 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
         __syncthreads();
         all = s_block;
     }
-    // A reference too far away (the same for all threads of the cluster): with logits of +inf their number is the sum;
-    // else both sums once more, from differences.
+    // Sums a second time (the same for all threads of the cluster). A reference too far away: with logits of +inf their
+    // number is the sum; else both from differences. A row that one logit dominates: without that one, whose rounding
+    // would cover the others (ln S = ln(1 + rest)); the thread that met it reads its pieces again, of the others' sums
+    // nothing was lost.
     const bool infinite = all.x == pos_inf();
-    if (infinite || (all.x > neg_inf() && fabsf(in_units(all.x)) >= kFar)) {
+    const bool far = infinite || (all.x > neg_inf() && fabsf(in_units(all.x)) >= kFar);
+    all.w = all.x > neg_inf() && !far ? fmaf(all.x, a.c, -in_units(all.x)) : 0.f;      // of the largest value, against the reference
+    const bool sharp = !far && all.x > neg_inf() && all.y < 1.5f;
+    if (far || sharp) {
         Sums again{0.f, 0.f, 0.f};
-        for (int v = v0 + tid; v < v1; v += kThreads) {
+        int v = v0 + tid, step = kThreads;
+        if (sharp) {
+            const bool here = s_block.x == all.x;
+            const float2 m = s_mine[tid];
+            if (!here || tid != s_owner) {
+                again = Sums{in_units(s_block.x), m.x, m.y};
+                again.against(in_units(all.x));
+                const float f = exp2_fast(-all.w);          // from the rounded reference to the largest value itself
+                again.e = f * fmaf(-all.w, again.s, again.e);
+                again.s *= f;
+            }
+            v = here ? v0 + s_owner + tid * kThreads : v1;
+            step = kThreads * kThreads;
+        }
+        for (; v < v1; v += step) {
             float x[P];
             R::values(row.piece(v), x);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const float t = infinite ? (x[j] == pos_inf() ? 0.f : -200.f) : fmaxf((x[j] - all.x) * a.c, -200.f);
+                float t = infinite ? (x[j] == pos_inf() ? 0.f : -200.f) : fmaxf((x[j] - all.x) * a.c, -200.f);
+                if (sharp && x[j] == all.x) t = -200.f;
                 const float p = exp2_fast(t);
                 again.s += p;
                 again.e = fmaf(p, t, again.e);
@@ -525,19 +552,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Args a) {
             all.y += p.y;
             all.z += p.z;
         }
-        all.w = 0.f;
-    } else {
-        all.w = all.x > neg_inf() ? fmaf(all.x, a.c, -in_units(all.x)) : 0.f;      // of the largest value, against the reference
     }
     if (rank == 0) {
-        const float over = logf(all.y) - kLn2 * all.w;      // ln S
+        const float over = sharp ? log1pf(all.y) : logf(all.y) - kLn2 * all.w;      // ln S
         auto log_p = [&](float x) {
             if (infinite) return x == pos_inf() ? -over : neg_inf();
             return x > neg_inf() ? fminf((x - all.x) * a.scale - over, 0.f) : neg_inf();
         };
         if (tid == 0) {
             if (a.logprob) a.logprob[t] = token >= 0 && token < a.V ? log_p(given) : 0.f;
-            if (a.entropy) a.entropy[t] = all.y > 0.f ? fmaxf(logf(all.y) - kLn2 * all.z / all.y, 0.f) : 0.f;
+            if (a.entropy) a.entropy[t] = sharp ? over - kLn2 * all.z / (1.f + all.y) : (all.y > 0.f ? fmaxf(logf(all.y) - kLn2 * all.z / all.y, 0.f) : 0.f);
         }
         if (a.k > 0) {
             if (blocks > 1) {
