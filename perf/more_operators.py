@@ -185,9 +185,12 @@ def run(s):
 
 
 def run_own(s):
+    c, op = s["case"], s["op"]
+    # the program that counted each adapter's rows has no call to make for a batch without any (neither has the plain form)
+    if op == "lora" and not s["most"]:
+        return s["y"]
     import weight_quantized_gemm_gb300 as qg
 
-    c, op = s["case"], s["op"]
     if op == "group":
         qg.qgemm_lora_group(c["m"], c["l"], s["adapter"], s["row"], s["offsets"])
         return dict(row=s["row"], offsets=s["offsets"])
