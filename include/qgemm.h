@@ -495,10 +495,11 @@ int qgemm_load(const char* path, void* Bp, size_t Bp_bytes, float* T, size_t T_b
 #define QGEMM_OPT_WAIT_LIMIT_US 4
 
 /* QGEMM_OPT_DEBUG_STALL (default 0). Diagnostic: when 1, every following launch of the TMA-fed
- * kernels, and of the adapters' kernel for many rows, has one role (the MMA issuer of the tensor-core
- * kernel, the first consumer warp of the decode kernel, all threads of the adapters' kernel) wait
- * first on a barrier that nothing arrives at, so that the wait runs out after
- * QGEMM_OPT_WAIT_LIMIT_US and the call ends with QGEMM_ERR_TIMEOUT as described above. It makes
+ * kernels has one role (the MMA issuer of the tensor-core kernel, the first consumer warp of the
+ * decode kernel) wait first on a barrier that nothing arrives at, so that the wait runs out after
+ * QGEMM_OPT_WAIT_LIMIT_US and the call ends with QGEMM_ERR_TIMEOUT as described above. In the
+ * adapters' kernel for many rows all threads of a block wait so, with products in flight (of its
+ * first stage, or in every other block of its first turn). It makes
  * the timeout path testable without a hang; production code keeps 0. Process-wide. */
 #define QGEMM_OPT_DEBUG_STALL 5
 

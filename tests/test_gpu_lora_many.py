@@ -147,3 +147,35 @@ def test_waits_that_run_out(M, R):
         c["Y"].copy_(before)
         qg.qgemm_lora_run(M, 512, 200, 3, R, qg.BF16, *plan, c["X"], 512, c["A"], c["B"], None, c["scale"], c["Y"], qg.BF16, 200)
         assert qg.qgemm_status() == 0 and torch.equal(c["Y"], want)
+
+
+@pytest.mark.parametrize("y_dtype", [qg.F32, qg.BF16])
+@pytest.mark.parametrize("M,R", [(2560, 16), (1300, 64), (900, 128), (300, 256)])
+@pytest.mark.parametrize("limit_us,stall", [(1, 0), (1, 1), (2000, 1)])
+def test_waits_that_run_out_with_products_in_flight(M, R, y_dtype, limit_us, stall):
+    """A bound so short that the waits run out while products are in flight, wherever that is; and the diagnostic wait behind
+    the first products. The block's own shared and tensor memory is all that those touch, and the next calls give their
+    bits."""
+    c = make(M, 1024, 520, 3, R, qg.F16, y_dtype, mixed(M, 3))
+    before = c["Y"].clone()
+    plan = run(c)
+    torch.cuda.synchronize()
+    want = c["Y"].clone()
+
+    def call():
+        c["Y"].copy_(before)
+        qg.qgemm_lora_run(M, 1024, 520, 3, R, qg.F16, *plan, c["X"], 1024, c["A"], c["B"], None, c["scale"], c["Y"], y_dtype, 520)
+
+    prev = qg.qgemm_set_option(qg.OPT_WAIT_LIMIT_US, limit_us), qg.qgemm_set_option(qg.OPT_DEBUG_STALL, stall)
+    try:
+        for _ in range(3):
+            call()
+        status = qg.qgemm_status()
+    finally:
+        qg.qgemm_set_option(qg.OPT_WAIT_LIMIT_US, prev[0])
+        qg.qgemm_set_option(qg.OPT_DEBUG_STALL, prev[1])
+    assert status == -6 or (stall == 0 and status == 0)
+    assert qg.qgemm_status() == 0
+    for _ in range(2):
+        call()
+        assert qg.qgemm_status() == 0 and torch.equal(c["Y"], want)

@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
         __syncthreads();
         bool fail = false;
         auto wait = [&](int i, uint32_t parity) { return ptx::mbar_wait(bar + 8 * i, parity, abort_flag, p.status, p.wait_ns); };
-        if (p.stall) fail = !wait(S::kStages + 2, 0);
+        // The diagnostic wait that runs out: behind the products of a first stage, or in every other block of a first turn.
+        const int stall = p.stall ? 1 + ((int)blockIdx.x & 1) : 0;
         const int c8 = tid & 7, r8 = tid >> 3;      // 8 threads copy a row's 128 bytes, 32 rows at a time
         const bool copier = RP <= 64 || warp != S::kIssuer;
 
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                         mma_async<128>(tmem + i % S::kSums * RP, xa + 2 * k, wa + 2 * k, idesc, i >= S::kSums || k > 0);
                     gg::mma_commit<gg::SOLO>(bar + 8 * slot);
                 }
+                if (stall == 1 && i == 0) fail = !wait(S::kStages + 2, 0);
                 if (i > 0) fail = fail || !wait(before, parity);       // the stage before has been read
                 fetch(i + S::kStages - 1, before);
                 before = slot;
@@ -399,6 +401,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                     }
                 gg::mma_commit<gg::SOLO>(bar + 8 * (S::kStages + (u & 1)));
             }
+            if (stall == 2 && u == 0) fail = !wait(S::kStages + 2, 0);
             fetch(u + S::kTurns - 2, next, u > 0 ? 0 : 1);
             if (u > 0 && !copier) {
                 if (__syncthreads_or(fail)) {
@@ -461,10 +464,11 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
         }
         copies_wait<0>();
         if (fail) {
-            // the MMAs issued end before the tensor memory is released: one that reports later than the ones before it
+            // The MMAs issued end before the tensor memory is released: a commit of the warp that issued them, as one
+            // tracks its own thread's alone.
             volatile int never = 0;
             __syncthreads();
-            if (warp == 0) {
+            if (warp == S::kIssuer) {
                 gg::mma_commit<gg::SOLO>(bar + 8 * (S::kStages + 2));
                 ptx::mbar_wait(bar + 8 * (S::kStages + 2), 0, &never, p.status);
             }
