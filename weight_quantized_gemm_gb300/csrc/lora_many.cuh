@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
             } else if (u > 0) {
                 const int v = u - 1, n = (t0 + v) * kTurnCols + half * kHalf;
                 const uint32_t tile = ring + before * S::kTurn;
-                fail = fail || !wait(S::kStages + (v & 1), (uint32_t)(v >> 1) & 1u);
+                fail = __any_sync(0xffffffffu, fail || !wait(S::kStages + (v & 1), (uint32_t)(v >> 1) & 1u));
                 gg::tc_fence_after();
                 const bool mine = row < S::kRows;        // (the same for the whole warp)
                 float acc[kHalf];
