@@ -1,0 +1,38 @@
+"""Adapters on values at the edges: infinities, the ranges of the middle values H = A x, and how many of their bits count. Each
+case runs on the kernel for few rows and on the one for many."""
+import math
+
+import pytest
+import torch
+
+import weight_quantized_gemm_gb300 as qg
+from tests._util import ensure_built
+from tests.test_gpu_lora import DEV, make, run
+
+pytestmark = pytest.mark.gpu
+INF = math.inf
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ensure_built()
+
+
+ROWS = [24, 2400]           # few rows, many rows (300 and more where the rank is above 128)
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("dtype,y_dtype", [(qg.F16, qg.F32), (qg.BF16, qg.F32), (qg.F16, qg.F16), (qg.BF16, qg.BF16)])
+@pytest.mark.parametrize("R,ranks", [(8, [1, 8]), (24, [3, 17]), (40, [9, 33]), (72, [16, 65]), (136, [7, 129])])
+def test_an_infinite_input_gives_infinity_at_every_rank(R, ranks, dtype, y_dtype, M):
+    """All values of A and B above 0: with an infinite x every H, and so every y, is that infinity. What pads a rank must not
+    make it a NaN (0 * inf)."""
+    c = make(M, 128, 70, 2, R, dtype, y_dtype, [i % 2 for i in range(M)])
+    c["rank"] = ranks
+    c["A"], c["B"] = c["A"].abs() + 0.125, c["B"].abs() + 0.125
+    before = c["Y"].clone()
+    c["X"][2, 5], c["X"][3, 5], c["X"][M - 1, 100] = INF, -INF, INF
+    run(c)
+    assert bool((c["Y"][2] == INF).all()) and bool((c["Y"][3] == -INF).all()) and bool((c["Y"][M - 1] == INF).all())
+    others = torch.tensor([m for m in range(M) if m not in (2, 3, M - 1)], device=DEV)
+    assert bool(torch.isfinite(c["Y"][others]).all()) and bool((c["Y"][others] != before[others]).any())

@@ -106,9 +106,10 @@ __device__ __forceinline__ float4 sum_of_blocks(const float* h, int blocks) {
     return v;
 }
 // H of all of K from the blocks' parts h: [rows][pitch], 16 * chunks columns, WIDTH pieces of 4 at a time; top: the bits
-// of each row's largest |H| (f16; cleared before). Every thread of the block calls it.
+// of each row's largest |H| (f16; cleared before). Columns past the rank become zeros: A's zeros there times an infinite X
+// were NaN. Every thread of the block calls it.
 template <bool BF, int WIDTH>
-__device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top, int pitch, int rows, int chunks, int blocks) {
+__device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top, int pitch, int rows, int rank, int chunks, int blocks) {
     for (int c0 = 0; c0 < chunks * 4; c0 += WIDTH)
         for (int i = threadIdx.x; i < rows * WIDTH; i += kThreads) {
             const int row = i / WIDTH, c = c0 + i % WIDTH, at = row * pitch + c * 4;
@@ -117,6 +118,8 @@ __device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top
             if (blocks == 1) v = *reinterpret_cast<const float4*>(h + at);
             else if (WIDTH <= 8 && blocks == 8) v = sum_of_blocks<8>(h + at, 8);
             else v = sum_of_blocks<4>(h + at, blocks);
+            const int left = rank - c * 4;
+            if (left < 4) v = make_float4(left > 0 ? v.x : 0.f, left > 1 ? v.y : 0.f, left > 2 ? v.z : 0.f, 0.f);
             *reinterpret_cast<float4*>(sum + at) = v;
             if constexpr (!BF) {
                 const float t = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     // ---- H of all of K, in the same order in every block, and its terms
     if (blocks > 1) cluster_sync();
     else __syncthreads();
-    join_h<BF, S::kRC / 4>(h, sum, top, pitch, S::kRows, chunks, blocks);
+    join_h<BF, S::kRC / 4>(h, sum, top, pitch, S::kRows, rank, chunks, blocks);
     if (blocks > 1) cluster_arrive();       // waited for at the end
     __syncthreads();
     make_terms<BF, kTerms>(sum, top, frag, pitch, chunks);
