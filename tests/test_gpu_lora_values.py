@@ -36,3 +36,19 @@ def test_an_infinite_input_gives_infinity_at_every_rank(R, ranks, dtype, y_dtype
     assert bool((c["Y"][2] == INF).all()) and bool((c["Y"][3] == -INF).all()) and bool((c["Y"][M - 1] == INF).all())
     others = torch.tensor([m for m in range(M) if m not in (2, 3, M - 1)], device=DEV)
     assert bool(torch.isfinite(c["Y"][others]).all()) and bool((c["Y"][others] != before[others]).any())
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("dtype", [qg.F16, qg.BF16])
+def test_an_infinite_middle_value_beside_a_large_one(M, dtype):
+    """H = (inf, 2^18), B = (1, -1): the sum is inf, though 2^18 is beyond f16."""
+    c = make(M, 128, 40, 1, 16, dtype, qg.F32, [0] * M, scaled=False)
+    c["X"].fill_(1.0)
+    c["A"].zero_()
+    c["A"][0, 0, 3] = INF
+    c["A"][0, 1].fill_(2048.0)
+    c["B"].zero_()
+    c["B"][0, :, 0], c["B"][0, :, 1] = 1.0, -1.0
+    c["rank"] = [2]
+    run(c)
+    assert bool((c["Y"] == INF).all())

@@ -77,14 +77,13 @@ __device__ __forceinline__ uint32_t take_term(float& x) {
     return bits;
 }
 
-// f16 terms are of H over the power of two of the row's largest |H| (its bits): this is that power.
-__device__ __forceinline__ float row_unit(uint32_t top) {
-    const uint32_t e = top >> 23;
-    return e == 255u ? 1.f : __uint_as_float(min(max(e, 1u), 253u) << 23);
-}
-__device__ __forceinline__ float row_unit_inverse(uint32_t top) {
-    const uint32_t e = top >> 23;
-    return e == 255u ? 1.f : __uint_as_float((254u - min(max(e, 1u), 253u)) << 23);
+// f16 terms are of H over the power of two of the row's largest finite |H| (its bits): this is that power.
+__device__ __forceinline__ float row_unit(uint32_t top) { return __uint_as_float(min(max(top >> 23, 1u), 253u) << 23); }
+__device__ __forceinline__ float row_unit_inverse(uint32_t top) { return __uint_as_float((254u - min(max(top >> 23, 1u), 253u)) << 23); }
+// |x|, and 0 where x is infinite or NaN: these need no unit, and must not set the others' (which were then beyond f16).
+__device__ __forceinline__ float finite_size(float x) {
+    x = fabsf(x);
+    return x < __uint_as_float(0x7F800000u) ? x : 0.f;
 }
 
 // 4 values at h of all blocks, added in rank order, AT_ONCE of them asked for together: a round trip to another block takes
@@ -106,7 +105,7 @@ __device__ __forceinline__ float4 sum_of_blocks(const float* h, int blocks) {
     return v;
 }
 // H of all of K from the blocks' parts h: [rows][pitch], 16 * chunks columns, WIDTH pieces of 4 at a time; top: the bits
-// of each row's largest |H| (f16; cleared before). Columns past the rank become zeros: A's zeros there times an infinite X
+// of each row's largest finite |H| (f16; cleared before). Columns past the rank become zeros: A's zeros there times an infinite X
 // were NaN. Every thread of the block calls it.
 template <bool BF, int WIDTH>
 __device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top, int pitch, int rows, int rank, int chunks, int blocks) {
@@ -122,7 +121,7 @@ __device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top
             if (left < 4) v = make_float4(left > 0 ? v.x : 0.f, left > 1 ? v.y : 0.f, left > 2 ? v.z : 0.f, 0.f);
             *reinterpret_cast<float4*>(sum + at) = v;
             if constexpr (!BF) {
-                const float t = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+                const float t = fmaxf(fmaxf(finite_size(v.x), finite_size(v.y)), fmaxf(finite_size(v.z), finite_size(v.w)));
                 atomicMax(top + row, __float_as_uint(t));
             }
         }

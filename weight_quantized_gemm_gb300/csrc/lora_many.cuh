@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                     x[e][0] = c < rank ? v.x : 0.f; x[e][1] = c + 1 < rank ? v.y : 0.f;
                     x[e][2] = c + 2 < rank ? v.z : 0.f; x[e][3] = c + 3 < rank ? v.w : 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) most = fmaxf(most, fabsf(x[e][k]));
+                    for (int k = 0; k < 4; ++k) most = fmaxf(most, finite_size(x[e][k]));
                 }
                 if constexpr (!BF) {
 #pragma unroll
