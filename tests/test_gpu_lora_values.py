@@ -52,3 +52,43 @@ def test_an_infinite_middle_value_beside_a_large_one(M, dtype):
     c["rank"] = [2]
     run(c)
     assert bool((c["Y"] == INF).all())
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("down", [4, 14, 20, 26, 30])
+@pytest.mark.parametrize("large", [2.0 ** -14, 1.0, 32768.0])
+def test_a_small_middle_value_beside_a_large_one(M, down, large):
+    """f16, H = (h, h 2^-down (1 + ...)) and B = (0, 1): y is the small one. It is off by 2^-23 of itself or 2^-39 of the large one at most
+    (half a step of the smallest f16, where the largest value is scaled to 2^14 at least), and by float32's two roundings."""
+    c = make(M, 128, 40, 1, 16, qg.F16, qg.F32, [0] * M, scaled=False)
+    c["Y"].zero_(), c["X"].zero_(), c["A"].zero_(), c["B"].zero_()
+    c["X"][:, 0], c["X"][:, 1] = large, 2.0 ** (-down // 2)
+    c["X"][:, 1] *= large
+    small = torch.linspace(1.0, 1.999, M, device=DEV).half()                        # 11 bits, times 11 bits: H has 22
+    c["X"][:, 1] *= small
+    c["A"][0, 0, 0], c["A"][0, 1, 1] = 1.0, 1.4990234375 * 2.0 ** (-down - (-down // 2))
+    c["B"][0, :, 1] = 1.0
+    c["rank"] = [2]
+    want = c["X"][:, 1].double() * float(c["A"][0, 1, 1])
+    run(c)
+    off = (c["Y"].double() - want[:, None]).abs()
+    allow = want * (2.0 ** -23 + 2.0 ** -23) + 2.0 ** -39 * large
+    assert bool((off <= allow[:, None]).all()), float((off / allow[:, None]).max())
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("dtype", [qg.F16, qg.BF16])
+def test_a_float32_result_has_float32_bits_of_the_middle_values(M, dtype):
+    """H = 1 + 2^-6 + 2^-12 + 2^-18 + 2^-21 exactly and B = 1: a float32 y has all of it but the last rounding (f16: within 2^-23 of
+    H), which two terms of bf16 miss by 2^-21."""
+    c = make(M, 128, 40, 1, 16, dtype, qg.F32, [0] * M, scaled=False)
+    c["Y"].zero_(), c["X"].zero_(), c["A"].zero_(), c["B"].zero_()
+    bits = [0, -6, -12, -18, -21]
+    for i, e in enumerate(bits):
+        c["X"][:, 16 * i] = 2.0 ** (e // 2)
+        c["A"][0, 0, 16 * i] = 2.0 ** (e - e // 2)
+    c["B"][0, :, 0] = 1.0
+    c["rank"] = [1]
+    want = sum(2.0 ** e for e in bits)
+    run(c)
+    assert float((c["Y"].double() - want).abs().max()) <= want * 2.0 ** -23

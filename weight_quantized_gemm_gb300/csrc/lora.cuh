@@ -16,10 +16,12 @@
 // values of two steps; and the order of the columns of the second product is chosen so that a lane ends with 8
 // neighbouring values of Y's row.
 //
-// H is exact to float32's rounding where it matters: it enters the second product as a sum of 16-bit terms (hi = its
-// nearest 16-bit value, then the nearest to what is left), 2 of them for 16-bit Y (17 bits of bf16, 22 of f16) and 3 of
-// bf16 for float32 Y. f16 terms are of H scaled by a power of two for each row, so that they neither overflow nor
-// lose their second term to f16's smallest exponent.
+// H is a float32 sum and enters the second product as a sum of 16-bit terms (hi = its nearest 16-bit value, then the
+// nearest to what is left): three of bf16 for float32 Y, which hold it whole; two of bf16 for 16-bit Y, off by up to 2^-17 of
+// it, where Y's own rounding is 2^-12 or 2^-9 (a third term is half as many products again, and its place in shared
+// memory); two of f16, off by up to 2^-23 of it, as float32's rounding is 2^-24, or by 2^-39 of the row's largest H if that
+// is more. f16 terms are of H scaled by a power of two for each row, so that they neither overflow nor lose their second
+// term to f16's smallest exponent.
 #pragma once
 
 #include "serve.cuh"
@@ -77,9 +79,11 @@ __device__ __forceinline__ uint32_t take_term(float& x) {
     return bits;
 }
 
-// f16 terms are of H over the power of two of the row's largest finite |H| (its bits): this is that power.
-__device__ __forceinline__ float row_unit(uint32_t top) { return __uint_as_float(min(max(top >> 23, 1u), 253u) << 23); }
-__device__ __forceinline__ float row_unit_inverse(uint32_t top) { return __uint_as_float((254u - min(max(top >> 23, 1u), 253u)) << 23); }
+// f16 terms are of H over a power of two that puts the row's largest finite |H| (its bits) between 2^14 and 2^15: half a step
+// of the smallest f16 is then 2^-39 of it at most (with the largest between 1 and 2, an H of 2^-30 of it became 0, which
+// counts where B's value for the largest is 0). This is that power.
+__device__ __forceinline__ float row_unit(uint32_t top) { return __uint_as_float((max(top >> 23, 15u) - 14u) << 23); }
+__device__ __forceinline__ float row_unit_inverse(uint32_t top) { return __uint_as_float((268u - max(top >> 23, 15u)) << 23); }
 // |x|, and 0 where x is infinite or NaN: these need no unit, and must not set the others' (which were then beyond f16).
 __device__ __forceinline__ float finite_size(float x) {
     x = fabsf(x);
