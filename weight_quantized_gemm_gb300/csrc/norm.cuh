@@ -88,7 +88,10 @@ __global__ void __launch_bounds__(MAXT, kBlocks<SDT, MAXT>) norm_kernel(const No
             for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum += f[c][j];
-            const float mean = total(sum, slot) * per;
+            // sum / K: the product with the rounded 1 / K, refined once by its residual. Without that it is off where the
+            // quotient is exact, and a row of 12345 is not 0 but -0.3 at K = 3584 and eps = 1e-5.
+            const float all = total(sum, slot), about = all * per;
+            const float mean = fmaf(fmaf(-about, (float)a.K, all), per, about);
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
