@@ -49,18 +49,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, 
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
-// 16 x 8 = 16 x 16 * 16 x 8
-template <bool BF>
-__device__ __forceinline__ void mma_first(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-    if constexpr (BF)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
-}
 // The 16-bit value nearest to x, as bits; x becomes what is left of it (0 where the value is infinite or NaN).
 template <bool BF>
 __device__ __forceinline__ uint32_t take_term(float& x) {

@@ -33,7 +33,6 @@ namespace qg {
 namespace lora {
 
 constexpr int kManyRows = 128;          // of a tile, and of the tensor cores' products
-constexpr int kMaxBlocks = 8;           // of a cluster
 
 template <int YDT, int RP, int TERMS>
 struct Many {
