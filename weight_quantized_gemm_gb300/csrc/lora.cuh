@@ -97,10 +97,9 @@ __device__ __forceinline__ float4 sum_of_blocks(const float* h, int blocks) {
     return v;
 }
 // H of all of K from the blocks' parts h: [rows][pitch], 16 * chunks columns, WIDTH pieces of 4 at a time; top: the bits
-// of each row's largest finite |H| (f16; cleared before). Columns past the rank become zeros: A's zeros there times an infinite X
-// were NaN. Every thread of the block calls it.
+// of each row's largest finite |H| (f16; cleared before). Every thread of the block calls it.
 template <bool BF, int WIDTH>
-__device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top, int pitch, int rows, int rank, int chunks, int blocks) {
+__device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top, int pitch, int rows, int chunks, int blocks) {
     for (int c0 = 0; c0 < chunks * 4; c0 += WIDTH)
         for (int i = threadIdx.x; i < rows * WIDTH; i += kThreads) {
             const int row = i / WIDTH, c = c0 + i % WIDTH, at = row * pitch + c * 4;
@@ -109,8 +108,6 @@ __device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top
             if (blocks == 1) v = *reinterpret_cast<const float4*>(h + at);
             else if (WIDTH <= 8 && blocks == 8) v = sum_of_blocks<8>(h + at, 8);
             else v = sum_of_blocks<4>(h + at, blocks);
-            const int left = rank - c * 4;
-            if (left < 4) v = make_float4(left > 0 ? v.x : 0.f, left > 1 ? v.y : 0.f, left > 2 ? v.z : 0.f, 0.f);
             *reinterpret_cast<float4*>(sum + at) = v;
             if constexpr (!BF) {
                 const float t = fmaxf(fmaxf(finite_size(v.x), finite_size(v.y)), fmaxf(finite_size(v.z), finite_size(v.w)));
@@ -118,9 +115,10 @@ __device__ __forceinline__ void join_h(const float* h, float* sum, uint32_t* top
             }
         }
 }
-// H's 16-bit terms, in the order in which the lanes take them: frag [chunks][terms][32].
+// H's 16-bit terms, in the order in which the lanes take them: frag [chunks][terms][32]. Columns past the rank become
+// zeros: A's zeros there times an infinite X were NaN.
 template <bool BF, int TERMS>
-__device__ __forceinline__ void make_terms(const float* sum, const uint32_t* top, uint4* frag, int pitch, int chunks) {
+__device__ __forceinline__ void make_terms(const float* sum, const uint32_t* top, uint4* frag, int pitch, int rank, int chunks) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     for (int f = warp; f < chunks; f += kWarps) {
         float v[2][4];
@@ -131,6 +129,10 @@ __device__ __forceinline__ void make_terms(const float* sum, const uint32_t* top
             const float by = BF ? 1.f : row_unit_inverse(top[row]);
             v[i][0] = o.x * by; v[i][1] = o.y * by; v[i][2] = o.z * by; v[i][3] = o.w * by;
         }
+        if (f * 16 + 16 > rank)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (f * 16 + q * 4 + k >= rank) v[0][k] = v[1][k] = 0.f;
 #pragma unroll
         for (int t = 0; t < TERMS; ++t) {
             uint32_t w[2][2];
@@ -458,10 +460,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     // ---- H of all of K, in the same order in every block, and its terms
     if (blocks > 1) cluster_sync();
     else __syncthreads();
-    join_h<BF, S::kRC / 4>(h, sum, top, pitch, S::kRows, rank, chunks, blocks);
+    join_h<BF, S::kRC / 4>(h, sum, top, pitch, S::kRows, chunks, blocks);
     if (blocks > 1) cluster_arrive();       // waited for at the end
     __syncthreads();
-    make_terms<BF, kTerms>(sum, top, frag, pitch, chunks);
+    make_terms<BF, kTerms>(sum, top, frag, pitch, rank, chunks);
     __syncthreads();
 
     // ---- Y += scale H B^T

@@ -330,11 +330,15 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                                 v.x += o[b].x; v.y += o[b].y; v.z += o[b].z; v.w += o[b].w;
                             }
                     }
-                    // (columns past the rank become zeros: A's zeros there times an infinite X were NaN)
-                    x[e][0] = c < rank ? v.x : 0.f; x[e][1] = c + 1 < rank ? v.y : 0.f;
-                    x[e][2] = c + 2 < rank ? v.z : 0.f; x[e][3] = c + 3 < rank ? v.w : 0.f;
+                    x[e][0] = v.x; x[e][1] = v.y; x[e][2] = v.z; x[e][3] = v.w;
+                    // columns past the rank become zeros: A's zeros there times an infinite X were NaN
+                    if (rank < RP)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) most = fmaxf(most, finite_size(x[e][k]));
+                        for (int k = 0; k < 4; ++k)
+                            if (c + k >= rank) x[e][k] = 0.f;
+                    if constexpr (!BF)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) most = fmaxf(most, finite_size(x[e][k]));
                 }
                 if constexpr (!BF) {
 #pragma unroll
