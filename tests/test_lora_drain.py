@@ -46,13 +46,13 @@ def test_the_last_commit_is_waited_for_with_the_full_bound_before_the_memory_is_
     assert re.match(r"ptx::mbar_wait\([^,]*, 0, &never, p\.status\)", after[wait:])
 
 
-def test_a_warp_agrees_on_a_wait_before_it_reads_tensor_memory():
-    """A read of tensor memory is of the whole warp, whose lanes may leave a bounded wait one by one and with different answers."""
+def test_a_warp_is_whole_again_behind_a_wait_before_it_reads_tensor_memory():
+    """A read of tensor memory is of the whole warp, whose lanes may leave a bounded wait one by one."""
     src = source()
     reads = [m.start() for m in re.finditer(r"gg::tmem_ld\(lanes", src)]
     assert len(reads) == 2
     for at in reads:
         before = src[:at]
-        wait = max(before.rfind("wait(before, parity)"), before.rfind("wait(S::kStages"))
+        wait = max(before.rfind("wait(before"), before.rfind("wait(S::kStages"))
         between = before[before.rfind("\n", 0, wait):]
-        assert "__any_sync(0xffffffffu, fail || !wait(" in between or "__syncthreads_or(fail)" in between
+        assert "__syncwarp()" in between or "__syncthreads_or(fail)" in between

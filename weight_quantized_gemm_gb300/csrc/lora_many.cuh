@@ -161,8 +161,10 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
         __syncthreads();
         bool fail = false;
         auto wait = [&](int i, uint32_t parity) { return ptx::mbar_wait(bar + 8 * i, parity, abort_flag, p.status, p.wait_ns); };
-        // The diagnostic wait that runs out: behind the products of a first stage, or in every other block of a first turn.
-        const int stall = p.stall ? 1 + ((int)blockIdx.x & 1) : 0;
+        // The diagnostic wait that runs out is the one for the products of a first stage (whose barrier is number 0), or in every
+        // other block for those of a first turn (number kStages), on the barrier that never completes (number kStages + 2).
+        const bool odd = blockIdx.x & 1u;
+        const int stuck1 = p.stall && !odd ? S::kStages + 2 : 0, stuck2 = p.stall && odd ? 2 : 0;
         const int c8 = tid & 7, r8 = tid >> 3;      // 8 threads copy a row's 128 bytes, 32 rows at a time
         const bool copier = RP <= 64 || warp != S::kIssuer;
 
@@ -216,8 +218,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                         mma_async<128>(tmem + i % S::kSums * RP, xa + 2 * k, wa + 2 * k, idesc, i >= S::kSums || k > 0);
                     gg::mma_commit<gg::SOLO>(bar + 8 * slot);
                 }
-                if (stall == 1 && i == 0) fail = !wait(S::kStages + 2, 0);
-                if (i > 0) fail = fail || !wait(before, parity);       // the stage before has been read
+                if (i > 0) fail = fail || !wait(before + stuck1, parity);       // the stage before has been read
                 fetch(i + S::kStages - 1, before);
                 before = slot;
                 if (++slot == S::kStages) slot = 0;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
             }
             // MMAs in flight end before anything else happens to what they read and write
             copies_wait<0>();
-            if (n1 > 0 && !fail) fail = !wait(before, parity);
+            if (n1 > 0 && !fail) fail = !wait(before + stuck1, parity);
             fail = __syncthreads_or(fail);
         }
 
@@ -407,7 +408,6 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                     }
                 gg::mma_commit<gg::SOLO>(bar + 8 * (S::kStages + (u & 1)));
             }
-            if (stall == 2 && u == 0) fail = !wait(S::kStages + 2, 0);
             fetch(u + S::kTurns - 2, next, u > 0 ? 0 : 1);
             if (u > 0 && !copier) {
                 if (__syncthreads_or(fail)) {
@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
             } else if (u > 0) {
                 const int v = u - 1, n = (t0 + v) * kTurnCols + half * kHalf;
                 const uint32_t tile = ring + before * S::kTurn;
-                fail = __any_sync(0xffffffffu, fail || !wait(S::kStages + (v & 1), (uint32_t)(v >> 1) & 1u));
+                fail = fail || !wait(S::kStages + stuck2 + (v & 1), (uint32_t)(v >> 1) & 1u);
+                __syncwarp();       // (the lanes may leave a wait one by one, and read tensor memory together)
                 gg::tc_fence_after();
                 const bool mine = row < S::kRows;        // (the same for the whole warp)
                 float acc[kHalf];
