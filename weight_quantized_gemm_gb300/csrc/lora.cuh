@@ -1,6 +1,7 @@
 // Low-rank adapters beside a shared projection: Y[m] += scale_l B_l (A_l X[m]) for the rows of every adapter, in one
-// launch. This file has the kernel for few rows, lora_many.cuh the one for many; instantiated for f16 (lora_f16.cu) and
-// bf16 (lora_bf16.cu).
+// launch. This file has the kernel for few rows, lora_many.cuh the one for many; instantiated for f16 and bf16 operands, each for
+// rows of Y that start 16-byte aligned (lora_f16.cu, lora_bf16.cu) and for rows that need not (lora_loose_f16.cu, lora_loose_bf16.cu).
+// In one kernel the second form's code made the first slower (8192 x 4096 x 14336 at rank 16 96 -> 98 us).
 //
 // A cluster of thread blocks takes up to 16 rows of one adapter. Its blocks share K in the first product (H = X A^T,
 // R values a row), join their parts of H in distributed shared memory, each in the same order, and share N in the
@@ -150,13 +151,76 @@ __device__ __forceinline__ void make_terms(const float* sum, const uint32_t* top
 // y[k] += scale * d[k] for the first `n` of 8 values, one at a time.
 template <int YDT>
 __device__ __forceinline__ void add_edge(void* y, const float (&d)[8], float scale, int n) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < n ? load_as_float<YDT>(y, k) : 0.f;      // (all asked for before the first is stored)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         if (k >= n) break;
-        const float v = fmaf(scale, d[k], load_as_float<YDT>(y, k));
-        if constexpr (YDT == DT_F32) static_cast<float*>(y)[k] = v;
-        else if constexpr (YDT == DT_F16) static_cast<__half*>(y)[k] = __float2half_rn(v);
-        else static_cast<__nv_bfloat16*>(y)[k] = __float2bfloat16_rn(v);
+        v[k] = fmaf(scale, d[k], v[k]);
+        if constexpr (YDT == DT_F32) static_cast<float*>(y)[k] = v[k];
+        else if constexpr (YDT == DT_F16) static_cast<__half*>(y)[k] = __float2half_rn(v[k]);
+        else static_cast<__nv_bfloat16*>(y)[k] = __float2bfloat16_rn(v[k]);
+    }
+}
+
+// Rows of Y that do not start 16-byte aligned: eight values of a row as the pairs n, n + 1, n + 8, n + 9, ... + 25, of which four
+// neighbouring lanes have 32 columns without a gap. 77 rows of 24 adapters, ranks up to 64, beside 4096 x 5760 in bf16 take 14
+// us aligned, 15 in rows of 5762 and 18 of 5761 values, 2000 rows of 100 adapters 28, 46 and 82 (with 8 neighbouring values a
+// lane, one after the other, 40 and 280). Values past N are neither read nor written.
+template <int YDT>
+__device__ __forceinline__ void fetch_pairs(Eight<YDT>& y, const void* row, int n, int N) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(y.v);
+    if constexpr (YDT == DT_F32) {
+        const uint32_t* p = static_cast<const uint32_t*>(row);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (n + 8 * t + i < N) w[2 * t + i] = load(p + n + 8 * t + i);
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(row);
+        const bool words = (reinterpret_cast<uintptr_t>(p) & 2u) == 0;      // (n is even)
+        uint16_t lo[4], hi[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int c = n + 8 * t;
+            lo[t] = hi[t] = 0;
+            if (words && c + 1 < N) {
+                w[t] = load(reinterpret_cast<const uint32_t*>(p + c));
+            } else {
+                if (c < N) lo[t] = load(p + c);
+                if (c + 1 < N) hi[t] = load(p + c + 1);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (!words || n + 8 * t + 1 >= N) w[t] = lo[t] | (uint32_t)hi[t] << 16;
+    }
+}
+template <int YDT>
+__device__ __forceinline__ void store_pairs(const Eight<YDT>& y, void* row, int n, int N) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(y.v);
+    if constexpr (YDT == DT_F32) {
+        uint32_t* p = static_cast<uint32_t*>(row);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (n + 8 * t + i < N) p[n + 8 * t + i] = w[2 * t + i];
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(row);
+        const bool words = (reinterpret_cast<uintptr_t>(p) & 2u) == 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int c = n + 8 * t;
+            if (words && c + 1 < N) {
+                *reinterpret_cast<uint32_t*>(p + c) = w[t];
+            } else {
+                if (c < N) p[c] = (uint16_t)w[t];
+                if (c + 1 < N) p[c + 1] = (uint16_t)(w[t] >> 16);
+            }
+        }
     }
 }
 
@@ -288,7 +352,7 @@ struct Shape {
     }
 };
 
-template <bool BF, int YDT, int JT>
+template <bool BF, int YDT, int JT, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     using S = Shape<JT>;
     constexpr int kNT = 2 * JT, kXV = S::kStep / 32, kTerms = terms_of(BF, YDT);
@@ -418,7 +482,6 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     const int u0 = units * rank_in >> shift, u1 = units * (rank_in + 1) >> shift;         // (N <= 2^30)
     const int chunks = (rank + 15) / 16;
     const uint16_t* B = static_cast<const uint16_t*>(a.B) + (size_t)l * a.N * a.R;
-    const bool wide = a.ldy % (YDT == DT_F32 ? 4 : 8) == 0;
     // Items of JT chunks of a unit of 32 columns, two in flight in registers of their own (Y's rows of the second where
     // registers allow it).
     constexpr int kYSets = JT == 4 && YDT == DT_F32 ? 1 : 2;
@@ -431,13 +494,20 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
             const int r = (c0 + j) * 16 + q * 4;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int n = u * 32 + (g >> 1) * 8 + t * 2 + (g & 1);
+                const int n = u * 32 + (WIDE ? (g >> 1) * 8 + t * 2 + (g & 1) : t * 8 + g);
                 load_if(b[j][t], B + (size_t)n * a.R + r, r < rank && n < a.N);
             }
         }
     };
+    auto y_row = [&](int i) { return static_cast<uint8_t*>(a.Y) + (long long)m[i] * a.ldy * (YDT == DT_F32 ? 4 : 2); };
     auto fetch_y = [&](int u, Eight<YDT> (&y)[2]) {
-        if (!wide || u * 32 + q * 8 + 8 > a.N) return;
+        if constexpr (!WIDE) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (m[i] >= 0) fetch_pairs<YDT>(y[i], y_row(i), u * 32 + q * 2, a.N);
+            return;
+        }
+        if (u * 32 + q * 8 + 8 > a.N) return;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (m[i] >= 0) y[i].fetch(a.Y, (size_t)((long long)m[i] * a.ldy) + u * 32 + q * 8);
@@ -509,16 +579,16 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
                 d[2 * t] = acc[t][2 * i] * mul[i];
                 d[2 * t + 1] = acc[t][2 * i + 1] * mul[i];
             }
-            uint8_t* out = static_cast<uint8_t*>(a.Y) + ((long long)m[i] * a.ldy + n) * (YDT == DT_F32 ? 4 : 2);
-            if (wide && n + 8 <= a.N) {
+            if (!WIDE || n + 8 <= a.N) {
                 float v[8];
                 y[i].values(v);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = fmaf(scale, d[k], v[k]);
                 y[i].round_from(v);
-                y[i].store(out, 0);
+                if constexpr (WIDE) y[i].store(y_row(i), n);
+                else store_pairs<YDT>(y[i], y_row(i), u * 32 + q * 2, a.N);
             } else {
-                add_edge<YDT>(out, d, scale, a.N - n);
+                add_edge<YDT>(y_row(i) + n * (size_t)(YDT == DT_F32 ? 4 : 2), d, scale, a.N - n);
             }
         }
         u += S::kWK;
@@ -534,11 +604,11 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     if (blocks > 1) cluster_wait();         // no block leaves while its H is read
 }
 
-template <bool BF, int YDT, int JT>
+template <bool BF, int YDT, int JT, bool WIDE>
 cudaError_t launch(const LoraArgs& a, int blocks, cudaStream_t s) {
     const Params p{a};
     const size_t smem = Shape<JT>::smem(a.R, terms_of(BF, YDT));
-    auto kern = lora_kernel<BF, YDT, JT>;
+    auto kern = lora_kernel<BF, YDT, JT, WIDE>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // at most one tile that is not full for each adapter that has rows

@@ -111,7 +111,7 @@ __device__ __forceinline__ void mma_async(uint32_t d, uint32_t a, uint32_t b, ui
         : "memory");
 }
 
-template <bool BF, int YDT, int RP>
+template <bool BF, int YDT, int RP, bool WIDE>
 __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ? 2 : 1) lora_many_kernel(const ManyParams p) {
     constexpr int kTerms = terms_of(BF, YDT);
     using S = Many<YDT, RP, kTerms>;
@@ -233,7 +233,6 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
         // ---- the second product's first turn comes while the blocks join their parts of H (behind which it has room)
         const int turns = (a.N + kTurnCols - 1) / kTurnCols;
         const int t0 = turns * rank_in >> shift, n2 = (turns * (rank_in + 1) >> shift) - t0;        // (N <= 2^30)
-        const bool wide = a.ldy % (16 / kYSize) == 0;
         constexpr int kPer = 16 / kYSize, kYC = S::kRows / 32;        // values of a 16-byte piece; pieces of a thread
         const uint32_t y_to = swizzled<128>(r8, c8);
         // A turn is whole where all of its columns are there and rows of Y start 16-byte aligned. This thread's pieces of the
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
             there |= (m >= 0 ? 1u : 0u) << i;
             y_at[i] = static_cast<uint8_t*>(a.Y) + ((long long)max(m, 0) * a.ldy + (size_t)t0 * kTurnCols + c8 * kPer) * kYSize;
         }
-        if (!wide) there = 0;
+        if (!WIDE) there = 0;
         const bool full = there == (1u << kYC) - 1;
         auto whole = [&](int u) { return (t0 + u + 1) * kTurnCols <= a.N; };
         // (8 columns belong together: they are copied, or at the row's end added one by one)
@@ -260,11 +259,36 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
         const uint32_t b_to = S::kY + (bc >> 3) * (kTurnCols * S::kBPitch) + swizzled<S::kBPitch>(bn, bc & 7);     // (kBApart is a multiple of 8)
         static_assert(kBApart % 8 == 0, "columns a thread copies have one order of pieces");
         const int b_bytes = min(max(rank - bc * 8, 0), 8) * 2;              // a piece's values past the adapter's rank become zeros
+        // Rows of Y that start anywhere: a warp copies a row at a time, a lane a 4-byte word of it. Of 16-bit rows that start
+        // between two words a lane reads and writes its two values one by one. 8192 rows at rank 16 beside 4096 x 5760, bf16:
+        // 55 us aligned, 99 in rows of 5762 and 258 of 5761 values, in float32 81, 142 and 144 (with a lane a row's 8 values
+        // one after the other 2500 to 2800).
+        constexpr int kLoose = S::kRows / kWarps, kWordValues = 4 / kYSize;
+        auto loose = [&](int u, auto each) {        // each(word's place in a tile, its address, its values that are there, whether it is a word in memory)
+            const int n = (t0 + u) * kTurnCols + lane * kWordValues, left = a.N - n;
+#pragma unroll 8
+            for (int i = 0; i < kLoose; ++i) {
+                const int r = warp + i * kWarps, m = s_row[r];
+                uint8_t* p = static_cast<uint8_t*>(a.Y) + ((long long)max(m, 0) * a.ldy + n) * kYSize;
+                if (m >= 0 && left > 0)
+                    each(swizzled<128>(r, lane >> 2) + (lane & 3) * 4, p, min(left, kWordValues), kYSize == 4 || (reinterpret_cast<uintptr_t>(p) & 2u) == 0);
+            }
+        };
         // fetches turn u; y_at is kAhead - `back` turns before it
         auto fetch = [&](int u, int slot, int back) {
             if (copier && u < n2) {
                 const uint32_t at = ring + slot * S::kTurn;
-                if (copied(u)) {
+                if constexpr (!WIDE) {
+                    loose(u, [&](uint32_t to, const uint8_t* p, int values, bool word) {
+                        if (word) {
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(at + to), "l"(p), "r"(values * kYSize) : "memory");
+                        } else {
+                            uint32_t v = load(reinterpret_cast<const uint16_t*>(p));
+                            if (values > 1) v |= (uint32_t)load(reinterpret_cast<const uint16_t*>(p) + 1) << 16;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + to), "r"(v) : "memory");
+                        }
+                    });
+                } else if (copied(u)) {
 #pragma unroll
                     for (int i = 0; i < kYC; ++i)
                         if (full || (there >> i & 1u)) copy16(at + y_to + i * 32 * 128, y_at[i] + (kAhead - back) * kTurnBytes, true);
@@ -427,15 +451,15 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                 // (what rows that are not there hold in shared memory goes nowhere; all is read before the first is written,
                 // as the compiler keeps the order of these accesses)
                 Eight<YDT> y[kHalf / 8];
-                const bool fast = mine && wide && whole(v);
+                const bool fast = mine && (!WIDE || whole(v));       // (values past N go nowhere either)
 #pragma unroll
                 for (int j = 0; j < kHalf / 8; ++j)
-                    if (fast || (mine && wide && n + 8 * j + 8 <= a.N))
+                    if (fast || (mine && n + 8 * j + 8 <= a.N))
 #pragma unroll
                         for (int k = 0; k < kV; ++k) y[j].v[k] = read16(tile + (y_cell ^ ((half * 4 + j * kV + k) << 4)));
 #pragma unroll
                 for (int j = 0; j < kHalf / 8; ++j) {
-                    if (fast || (mine && wide && n + 8 * j + 8 <= a.N)) {
+                    if (fast || (mine && n + 8 * j + 8 <= a.N)) {
                         float x[8];
                         y[j].values(x);
 #pragma unroll
@@ -454,7 +478,18 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                     fail = true;
                     break;
                 }
-                if (copied(v)) {
+                if constexpr (!WIDE) {
+                    loose(v, [&](uint32_t from, uint8_t* p, int values, bool word) {
+                        uint32_t w;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(tile + from) : "memory");
+                        if (word && values == kWordValues) {
+                            *reinterpret_cast<uint32_t*>(p) = w;
+                        } else {
+                            *reinterpret_cast<uint16_t*>(p) = (uint16_t)w;
+                            if (values > 1) *(reinterpret_cast<uint16_t*>(p) + 1) = (uint16_t)(w >> 16);
+                        }
+                    });
+                } else if (copied(v)) {
                     uint4 out[kYC];
 #pragma unroll
                     for (int i = 0; i < kYC; ++i) out[i] = read16(tile + y_to + i * 32 * 128);
@@ -489,12 +524,12 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
     }
 }
 
-template <bool BF, int YDT, int RP>
+template <bool BF, int YDT, int RP, bool WIDE>
 cudaError_t launch_many(const LoraArgs& a, int blocks, cudaStream_t s) {
     using S = Many<YDT, RP, terms_of(BF, YDT)>;
     const ManyParams p{a, status_word_address(), option_wait_ns(), option_stall()};
     if (!p.status) return cudaErrorUnknown;
-    auto kern = lora_many_kernel<BF, YDT, RP>;
+    auto kern = lora_many_kernel<BF, YDT, RP, WIDE>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
     if (e != cudaSuccess) return e;
     // at most one tile that is not full for each adapter that has rows
@@ -509,7 +544,7 @@ inline int blocks_of(long long tiles, int most) {
     return blocks;
 }
 
-template <bool BF, int YDT>
+template <bool BF, int YDT, bool WIDE>
 cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
     // Tiles of 128 rows where there are many rows; from how many on depends on the rank, as the few rows' kernel reads each
     // adapter once for every 16 rows, and from where on it needs a second round of blocks (4096 x 14336, us, few / many:
@@ -530,12 +565,12 @@ cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
         const int tiles = a.M / (rank > 128 ? 64 : kManyRows);
         const int blocks = blocks_of(tiles + (a.L < tiles ? a.L : tiles), rank >= 128 ? kTargetSms : 2 * kTargetSms);
         switch (rank) {
-            case 16: return launch_many<BF, YDT, 16>(a, blocks, s);
-            case 32: return launch_many<BF, YDT, 32>(a, blocks, s);
-            case 64: return launch_many<BF, YDT, 64>(a, blocks, s);
-            case 128: return launch_many<BF, YDT, 128>(a, blocks, s);
+            case 16: return launch_many<BF, YDT, 16, WIDE>(a, blocks, s);
+            case 32: return launch_many<BF, YDT, 32, WIDE>(a, blocks, s);
+            case 64: return launch_many<BF, YDT, 64, WIDE>(a, blocks, s);
+            case 128: return launch_many<BF, YDT, 128, WIDE>(a, blocks, s);
             default:
-                if constexpr (kWide) return launch_many<BF, YDT, 256>(a, blocks, s);
+                if constexpr (kWide) return launch_many<BF, YDT, 256, WIDE>(a, blocks, s);
         }
     }
     // 8 blocks for a few rows (16 rows of 16 adapters 4.6 us; 4 blocks 5.4), fewer where the tiles alone fill the GPU
@@ -544,18 +579,18 @@ cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
     // of each 12.8 / 9.2 / 11.7, 512 rows of 8 adapters 13.9 / 9.0 / 9.3).
     const int blocks = blocks_of(a.M / 16 + (long long)(a.L < a.M ? a.L : a.M) * 5 / 8, kTargetSms * 9 / 4);
     switch (rank) {
-        case 16: return launch<BF, YDT, 1>(a, blocks, s);
-        case 32: return launch<BF, YDT, 2>(a, blocks, s);
-        default: return launch<BF, YDT, 4>(a, blocks, s);
+        case 16: return launch<BF, YDT, 1, WIDE>(a, blocks, s);
+        case 32: return launch<BF, YDT, 2, WIDE>(a, blocks, s);
+        default: return launch<BF, YDT, 4, WIDE>(a, blocks, s);
     }
 }
 
-template <bool BF>
+template <bool BF, bool WIDE>
 cudaError_t launch_form(const LoraArgs& a, int y_dtype, cudaStream_t s) {
     switch (y_dtype) {
-        case DT_F32: return launch_y<BF, DT_F32>(a, s);
-        case DT_F16: return launch_y<BF, DT_F16>(a, s);
-        default: return launch_y<BF, DT_BF16>(a, s);
+        case DT_F32: return launch_y<BF, DT_F32, WIDE>(a, s);
+        case DT_F16: return launch_y<BF, DT_F16, WIDE>(a, s);
+        default: return launch_y<BF, DT_BF16, WIDE>(a, s);
     }
 }
 

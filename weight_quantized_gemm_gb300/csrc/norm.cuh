@@ -21,8 +21,9 @@ namespace qg {
 namespace norm {
 
 // Threads of a block at most, and blocks an SM at least (which bounds the registers): of rows above 5120 and up to 8192
-// values three blocks or more (16384 x 8192 in bf16, 80 registers a thread, 195 -> 170 us; x 6144 138 -> 126). Longer rows would lose
-// more to the stack than they gain (x 9728 222 us with two blocks, 241 with three), but with a residual in float32 that
+// values three blocks or more (16384 x 8192 in bf16, 80 registers a thread, 195 -> 170 us; x 6144 138 -> 126). Three blocks of the next longer
+// rows lose more to the stack than they gain (x 9728 222 us with two blocks, 241 with three); above 10240 values the bound of 1024 threads leaves
+// 64 registers, and 200 to 360 bytes a thread on the stack (instances for 384 or 512 threads were not tried). But with a residual in float32 that
 // is asked for only where it is added (kLate): 1023 x 9728 36.4 -> 34.4 us, x 8192 32.9 -> 26.6, x 6144 25.8 -> 21.1,
 // 2000 x 16384 119 -> 92; rows up to 5120 lose by that (20.8 -> 22.2).
 template <int SDT, int MAXT>

@@ -24,8 +24,16 @@ struct LoraArgs {
     long long ldy;
 };
 cudaError_t launch_lora_group(int M, int L, const int32_t* adapter, int32_t* row, int32_t* offsets, cudaStream_t s);
+// rows of Y that start 16-byte aligned, and rows that need not
 cudaError_t launch_lora_f16(const LoraArgs& a, int y_dtype, cudaStream_t s);
 cudaError_t launch_lora_bf16(const LoraArgs& a, int y_dtype, cudaStream_t s);
+cudaError_t launch_lora_loose_f16(const LoraArgs& a, int y_dtype, cudaStream_t s);
+cudaError_t launch_lora_loose_bf16(const LoraArgs& a, int y_dtype, cudaStream_t s);
+inline cudaError_t launch_lora(const LoraArgs& a, int dtype, int y_dtype, cudaStream_t s) {
+    if (a.ldy % (16 / (long long)dt_size(y_dtype)) == 0)
+        return dtype == DT_F16 ? launch_lora_f16(a, y_dtype, s) : launch_lora_bf16(a, y_dtype, s);
+    return dtype == DT_F16 ? launch_lora_loose_f16(a, y_dtype, s) : launch_lora_loose_bf16(a, y_dtype, s);
+}
 
 struct NormArgs {
     int M, K, kind;

@@ -70,8 +70,7 @@ int qgemm_lora_run(int M, int K, int N, int L, int R, int dtype, const int32_t* 
     if (!row_aligned(ldx, dtype)) return fail(QGEMM_ERR_ALIGN, "rows of X must start 16-byte aligned (ldx=%lld)", ldx);
     if (qg::api_inject_fault()) return injected();
     const qg::LoraArgs a{M, K, N, L, R, row, offsets, X, ldx, A, B, rank, scale, Y, ldy};
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return done(dtype == QGEMM_F16 ? qg::launch_lora_f16(a, y_dtype, s) : qg::launch_lora_bf16(a, y_dtype, s), "lora_run launch");
+    return done(qg::launch_lora(a, dtype, y_dtype, static_cast<cudaStream_t>(stream)), "lora_run launch");
 }
 
 int qgemm_norm_run(int M, int K, int kind, float eps, const void* X, int x_dtype, long long ldx, float x_scale, int post,
