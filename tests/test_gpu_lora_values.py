@@ -92,3 +92,32 @@ def test_a_float32_result_has_float32_bits_of_the_middle_values(M, dtype):
     want = sum(2.0 ** e for e in bits)
     run(c)
     assert float((c["Y"].double() - want).abs().max()) <= want * 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype", [qg.F16, qg.BF16])
+@pytest.mark.parametrize("M,K,R", [(19600, 16384, 64), (9800, 16384, 128), (9800, 8192, 256), (1000, 65536, 128), (2400, 131072, 16)])
+def test_long_sums_are_float32_sums(M, K, R, dtype):
+    """Values above 0, so that nothing cancels and every cut-off adds up. The tensor cores cut a running sum off by 2 u of it at most; the
+    first product's chains are 16 steps long (32 u of the whole), added up in float32 (a rounding for each chain of an
+    accumulator, each accumulator, and each of 8 blocks), the second one's have a step for 16 ranks; the terms of H
+    hold 2^-23 = 2 u of it, the smaller ones' products are 2^-8 of the whole or less and add 1 u, and the last sum rounds once."""
+    if dtype == qg.BF16 and R > 128:
+        pytest.skip("takes the kernel for few rows")
+    N = 40
+    g = torch.Generator(device=DEV).manual_seed(M + R)
+    dt = torch.float16 if dtype == qg.F16 else torch.bfloat16
+    X = torch.rand(M, K, generator=g, device=DEV, dtype=torch.float32).to(dt)
+    A = (torch.rand(1, R, K, generator=g, device=DEV) * 0.01).to(dt)
+    B = torch.rand(1, N, R, generator=g, device=DEV).to(dt)
+    Y = torch.zeros(M, N, device=DEV)
+    row = torch.arange(M, dtype=torch.int32, device=DEV)
+    offsets = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    qg.qgemm_lora_run(M, K, N, 1, R, dtype, row, offsets, X, K, A, B, None, None, Y, qg.F32, N)
+    u = 2.0 ** -24
+    rp = max(16, 1 << (R - 1).bit_length())
+    sums = (256 if rp <= 64 else 512) // rp
+    bound = u * (32 + -(-K // 64 // (4 * sums)) + sums + 8 + 2 * R / 16 + 2 + 1 + 2)
+    for rows in torch.arange(M, device=DEV).split(1024):
+        want = (X[rows].double() @ A[0].double().T) @ B[0].double().T
+        off = float(((Y[rows].double() - want).abs() / want).max())
+        assert off <= bound, (off / u, bound / u)

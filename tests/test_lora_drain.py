@@ -50,9 +50,9 @@ def test_a_warp_is_whole_again_behind_a_wait_before_it_reads_tensor_memory():
     """A read of tensor memory is of the whole warp, whose lanes may leave a bounded wait one by one."""
     src = source()
     reads = [m.start() for m in re.finditer(r"gg::tmem_ld\(lanes", src)]
-    assert len(reads) == 2
+    assert len(reads) == 3
     for at in reads:
         before = src[:at]
-        wait = max(before.rfind("wait(before"), before.rfind("wait(S::kStages"))
+        wait = max(before.rfind("wait(before"), before.rfind("wait(S::kStages"), before.rfind("auto empty"))
         between = before[before.rfind("\n", 0, wait):]
         assert "__syncwarp()" in between or "__syncthreads_or(fail)" in between

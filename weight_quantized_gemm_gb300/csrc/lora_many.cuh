@@ -51,8 +51,15 @@ struct Many {
     static constexpr int kRoom = (RP <= 64 ? 112 << 10 : 225 << 10) - kH - 2048;        // two blocks an SM where they fit
     static constexpr int kTurns = kRoom / kTurn < 5 ? kRoom / kTurn : 5;                // ring of turns
     static constexpr int kStages = kTurns * kTurn / kStage < 5 ? kTurns * kTurn / kStage : 5;
-    // the first product's stages go to kSums accumulators in turn: the tensor cores cut sums off, and shorter chains lose less
-    static constexpr int kSums = RP <= 64 ? 128 / RP : 256 / RP, kD2 = kSums * RP, kTmem = RP <= 64 ? 256 : 512;
+    // The first product's stages go to kSums accumulators in turn, each of which is emptied after kChain stages if there are
+    // more: the tensor cores cut sums off instead of rounding them, and shorter chains lose less (f16 to float32, 6000 rows,
+    // K = 8192: off by 5.0e-7 at rank 128 and 6.4e-7 at 256, a float32 product by 6.0e-7 and 1.6e-6; never emptied, with half as
+    // many accumulators, by 2.8e-6 and 1.0e-5, in the same time). They are emptied into registers, at ranks above 128, where these
+    // do not hold them (48 -> 53 us at 4099 x 2560 x 2560), into H's place. The second product's two accumulators take the place of these.
+    static constexpr int kTmem = RP <= 64 ? 256 : 512, kSums = kTmem / RP, kChain = 4;
+    static constexpr bool kHeld = RP <= 128;        // in registers
+    static_assert(kHeld || kRows * RP * 4 <= kH, "H's place");
+    static_assert(kSums >= 2 && 2 * kCols <= kTmem, "accumulators");
     static constexpr int kPartPitch = RP + 4;                                          // floats: 16-byte writes of 8 rows meet no bank twice
     static constexpr int kRing = kTurns * kTurn;
     static constexpr size_t kSmem = 1024 + kRing + kH;
@@ -168,6 +175,13 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
         const int c8 = tid & 7, r8 = tid >> 3;      // 8 threads copy a row's 128 bytes, 32 rows at a time
         const bool copier = RP <= 64 || warp != S::kIssuer;
 
+        // a warp reads its quarter's lanes of tensor memory, and half of the columns (the issuer of its own none)
+        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)quarter * 32 << 16);
+        const bool reads = copier && row < S::kRows;
+        float held[S::kHeld ? (RP + 31) / 32 : 1][16] = {};
+        float* spare = reinterpret_cast<float*>(smem_raw + (H - ptx::smem_u32(smem_raw))) + row;        // [RP][kRows], this thread's row
+
         // ---- D1 = X A^T over this block's part of K
         const int steps = a.K / 64;
         const int s0 = steps * rank_in >> shift, n1 = (steps * (rank_in + 1) >> shift) - s0;        // (K <= 2^30)
@@ -198,6 +212,29 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                 copies_end();
             };
             const uint32_t idesc = gg::inst_desc<gg::HALF>(kManyRows, RP, BF);
+            // Empties the accumulator of stage j (whose products have ended) if it is full and used again. The stage after j, whose
+            // products are in flight, has another; the next one that has the same is issued behind a barrier.
+            auto empty = [&](int j) {
+                if (j / S::kSums % S::kChain != S::kChain - 1 || j + S::kSums >= n1 || !reads) return;
+                __syncwarp();       // (the lanes may leave a wait one by one)
+                gg::tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < RP; c += 32)
+                    if (c + half * 16 < RP) {
+                        float w[16];
+                        gg::tmem_ld(lanes + j % S::kSums * RP + c + half * 16, w);
+                        if constexpr (S::kHeld) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) held[c / 32][k] += w[k];
+                        } else {
+                            float* to = spare + (c + half * 16) * S::kRows;
+                            const bool first = j == S::kSums * (S::kChain - 1);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) to[k * S::kRows] = first ? w[k] : to[k * S::kRows] + w[k];
+                        }
+                    }
+                gg::tc_fence_before();
+            };
 #pragma unroll
             for (int d = 0; d < S::kStages - 1; ++d) fetch(d, d);
             int slot = 0, before = S::kStages - 1;
@@ -215,10 +252,13 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                     uint32_t xa = gg::rows_lo(at), wa = gg::rows_lo(at + S::kX);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_async<128>(tmem + i % S::kSums * RP, xa + 2 * k, wa + 2 * k, idesc, i >= S::kSums || k > 0);
+                        mma_async<128>(tmem + i % S::kSums * RP, xa + 2 * k, wa + 2 * k, idesc, i / S::kSums % S::kChain != 0 || k > 0);
                     gg::mma_commit<gg::SOLO>(bar + 8 * slot);
                 }
-                if (i > 0) fail = fail || !wait(before + stuck1, parity);       // the stage before has been read
+                if (i > 0) {
+                    fail = fail || !wait(before + stuck1, parity);       // the stage before has been read
+                    empty(i - 1);
+                }
                 fetch(i + S::kStages - 1, before);
                 before = slot;
                 if (++slot == S::kStages) slot = 0;
@@ -309,15 +349,14 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
 
         // ---- the block's part of H, where the stages were
         float* part = reinterpret_cast<float*>(smem_raw + (ring - ptx::smem_u32(smem_raw)));      // [128][kPartPitch]
-        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;      // a warp reads its quarter's lanes (the issuer none)
-        const uint32_t lanes = tmem + ((uint32_t)quarter * 32 << 16);
         gg::tc_fence_after();
 #pragma unroll
         for (int c = 0; c < RP; c += 32) {
-            float v[16];
-            if (copier && row < S::kRows && c + half * 16 < RP) {
+            float (&v)[16] = held[S::kHeld ? c / 32 : 0];
+            if (reads && c + half * 16 < RP) {
+                if (!S::kHeld)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                    for (int j = 0; j < 16; ++j) v[j] = n1 > S::kSums * S::kChain ? spare[(c + half * 16 + j) * S::kRows] : 0.f;
                 for (int d = 0; d < min(n1, S::kSums); ++d) {
                     float w[16];
                     gg::tmem_ld(lanes + d * RP + c + half * 16, w);
@@ -422,13 +461,14 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
             }
             if (warp == S::kIssuer && u < n2) {
                 gg::tc_fence_after();
-                const uint32_t d = tmem + S::kD2 + (u & 1) * kTurnCols, bt = ring + slot * S::kTurn + S::kY;
-                for (int t = 0; t < kTerms; ++t)
+                const uint32_t d = tmem + (u & 1) * kTurnCols, bt = ring + slot * S::kTurn + S::kY;
+                // (the small terms first: a sum is cut off by what its size is)
+                for (int t = kTerms - 1; t >= 0; --t)
                     for (int k = 0; k < chunks; ++k) {
                         const int col = t * RP + k * 16;
                         const uint32_t ha = gg::rows_lo(H + (col >> 6) * S::kHAtom) + ((col & 63) >> 3);
                         const uint32_t ba = gg::rows_lo(bt + (k >> 2) * (kTurnCols * 128)) + 2 * (k & 3);
-                        mma_async<S::kBPitch>(d, ha, ba, idesc, t > 0 || k > 0);
+                        mma_async<S::kBPitch>(d, ha, ba, idesc, t < kTerms - 1 || k > 0);
                     }
                 gg::mma_commit<gg::SOLO>(bar + 8 * (S::kStages + (u & 1)));
             }
@@ -446,7 +486,7 @@ __global__ void __launch_bounds__(RP > 64 ? kThreads + 32 : kThreads, RP <= 64 ?
                 gg::tc_fence_after();
                 const bool mine = row < S::kRows;        // (the same for the whole warp)
                 float acc[kHalf];
-                if (mine) gg::tmem_ld(lanes + S::kD2 + (v & 1) * kTurnCols + half * kHalf, acc);
+                if (mine) gg::tmem_ld(lanes + (v & 1) * kTurnCols + half * kHalf, acc);
                 constexpr int kV = Eight<YDT>::kVecs;
                 // (what rows that are not there hold in shared memory goes nowhere; all is read before the first is written,
                 // as the compiler keeps the order of these accesses)
