@@ -121,3 +121,27 @@ def test_long_sums_are_float32_sums(M, K, R, dtype):
         want = (X[rows].double() @ A[0].double().T) @ B[0].double().T
         off = float(((Y[rows].double() - want).abs() / want).max())
         assert off <= bound, (off / u, bound / u)
+
+
+@pytest.mark.parametrize("dtype", [qg.F16, qg.BF16])
+@pytest.mark.parametrize("M,K,R,L", [(2000, 65536, 16, 1), (2000, 32768, 32, 100), (1200, 65536, 64, 1), (700, 65536, 128, 40), (240, 65536, 256, 40), (9, 131072, 16, 1)])
+def test_long_sums_of_few_rows_are_float32_sums(M, K, R, L, dtype):
+    """The same for the kernel for few rows: chains of 16 or 32 steps in the first product, a rounding for each of them and each of 8
+    warps and 8 blocks; 3 steps for 16 ranks in the second, 128 ranks at a time."""
+    N = 40
+    g = torch.Generator(device=DEV).manual_seed(M + R)
+    dt = torch.float16 if dtype == qg.F16 else torch.bfloat16
+    X = torch.rand(M, K, generator=g, device=DEV).to(dt)
+    A = (torch.rand(L, R, K, generator=g, device=DEV) * 0.01).to(dt)
+    B = torch.rand(L, N, R, generator=g, device=DEV).to(dt)
+    Y = torch.zeros(M, N, device=DEV)
+    row = torch.arange(M, dtype=torch.int32, device=DEV)
+    at = [M * l // L for l in range(L + 1)]
+    qg.qgemm_lora_run(M, K, N, L, R, dtype, row, torch.tensor(at, dtype=torch.int32, device=DEV), X, K, A, B, None, None, Y, qg.F32, N)
+    u, chain = 2.0 ** -24, 16 if R <= 32 else 32
+    bound = u * (2 * chain + -(-K // 8 // 16 // chain) + 16 + 2 * 3 * min(R / 16, 8) + 2 + 2 + 1)
+    for l in range(L):
+        x = X[at[l]: at[l + 1]].double()
+        want = (x @ A[l].double().T) @ B[l].double().T
+        off = float(((Y[at[l]: at[l + 1]].double() - want).abs() / want).max())
+        assert off <= bound, (off / u, bound / u)

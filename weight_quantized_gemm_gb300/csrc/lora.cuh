@@ -341,6 +341,12 @@ struct Shape {
     static constexpr int kRC = 16 * JT;               // ranks of a pass over K
     static constexpr int kPartPitch = kRC + 8;        // floats; 8 mod 32 spreads 4 rows' pairs over all banks
     static constexpr int kStep = JT <= 2 ? 64 : 32;   // of K at a time
+    // Two steps are a turn; after kChain of them (16 products into an accumulator, 32 where there are many) a warp adds its sums
+    // to those in shared memory, as the tensor cores cut sums off instead of rounding them (float32 Y, 2000 rows of 100
+    // adapters, K = 8192: off by 3.8e-7 in f16 and 2.7e-7 in bf16 at rank 16, a float32 product by 4.5e-7 and 2.1e-7; without
+    // it by 1.3e-6 and 1.1e-6). So are the second product's at ranks above 128, two items at a time. What it costs: nothing at ranks up to 32, 2 % at
+    // 64 and 128 (6000 x 8192 x 8192 of 200 adapters 342 -> 347 us), 7 % above (4099 x 2560 x 2560, bf16 to float32, 111 -> 118).
+    static constexpr int kChain = (JT <= 2 ? 16 : 32) / (2 * kStep / 16);
     __host__ __device__ static int ranks(int R) { return (R + 15) / 16 * 16; }
     static size_t smem(int R, int terms) {
         return shared_floats(R) * 4 + (size_t)kRows * (ranks(R) + 8) * 4 + (size_t)(ranks(R) / 16) * terms * 512 + kRows * 4;
@@ -431,10 +437,26 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
         fetch(0, s0 + wk + S::kWK, x[1], w[1]);
         for (int r0 = 0; r0 < rank; r0 += S::kRC) {
             float acc[kNT][4];
+            float* const mine = part + (wk * S::kRows + g) * S::kPartPitch + 2 * q;
+            auto clear = [&]() {
 #pragma unroll
-            for (int n = 0; n < kNT; ++n)
+                for (int n = 0; n < kNT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+                    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+            };
+            // to this lane's place in the warp's part of H, or what is there already
+            auto put = [&](bool add) {
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float2* to = reinterpret_cast<float2*>(mine + i * 8 * S::kPartPitch + n * 8);
+                        const float2 v = add ? *to : make_float2(0.f, 0.f);
+                        *to = make_float2(v.x + acc[n][2 * i], v.y + acc[n][2 * i + 1]);
+                    }
+            };
+            clear();
+            if (r0 > 0) __syncthreads();        // the pass before has been read
             auto step = [&](const uint4 (&x)[2][kXV], const uint4 (&w)[kNT][kXV]) {
 #pragma unroll
                 for (int v = 0; v < kXV; ++v)
@@ -444,22 +466,22 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
                         mma<BF>(acc[n], make_uint4(x[0][v].z, x[1][v].z, x[0][v].w, x[1][v].w), w[n][v].z, w[n][v].w);
                     }
             };
-            for (int s = s0 + wk; s < s1; s += 2 * S::kWK) {
+            int s = s0 + wk;
+            auto turns = [&]() { return (s - s0 - wk) / (2 * S::kWK); };
+            for (; s < s1; s += 2 * S::kWK) {
                 step(x[0], w[0]);
                 fetch(r0, s + 2 * S::kWK, x[0], w[0]);
                 if (s + S::kWK >= s1) break;
                 step(x[1], w[1]);
                 fetch(r0, s + 3 * S::kWK, x[1], w[1]);
+                if (turns() % S::kChain == S::kChain - 1) {
+                    put(turns() >= S::kChain);
+                    clear();
+                }
             }
             fetch(r0 + S::kRC, s0 + wk, x[0], w[0]);
             fetch(r0 + S::kRC, s0 + wk + S::kWK, x[1], w[1]);
-            if (r0 > 0) __syncthreads();        // the pass before has been read
-            float* mine = part + (wk * S::kRows + g) * S::kPartPitch + 2 * q;
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-                *reinterpret_cast<float2*>(mine + n * 8) = make_float2(acc[n][0], acc[n][1]);
-                *reinterpret_cast<float2*>(mine + 8 * S::kPartPitch + n * 8) = make_float2(acc[n][2], acc[n][3]);
-            }
+            put(turns() >= S::kChain);
             __syncthreads();
             constexpr int kWidth = S::kRC / 4;
             for (int i = tid; i < S::kRows * kWidth; i += kThreads) {
@@ -540,10 +562,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
     float mul[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) mul[i] = BF ? 1.f : row_unit(top[g + 8 * i]);
+    // Two items' products (each item's small terms first) are added up by themselves, and then to the unit's, which wait in H's
+    // place (see kChain).
     float acc[4][4];
+    float4* const total = reinterpret_cast<float4*>(part) + warp * 4 * 32 + lane;
     int u = u0 + wk, c0 = 0;
     auto item = [&](uint2 (&b)[JT][4], Eight<YDT> (&y)[2]) {
-        if (c0 == 0)
+        if (c0 % (2 * JT) == 0)
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -551,22 +576,30 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const Params p) {
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
             if (c0 + j >= chunks) break;
-            const int left = rank - (c0 + j) * 16 - q * 4;
-            if (left < 4)                   // values past the adapter's rank are cleared
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    b[j][t].x &= left >= 2 ? ~0u : (left == 1 ? 0xFFFFu : 0u);
-                    b[j][t].y &= left == 3 ? 0xFFFFu : 0u;
-                }
-            const uint4* f = frag + (c0 + j) * kTerms * 32 + lane;
+            for (int k = kTerms - 1; k >= 0; --k) {
+                const int left = rank - (c0 + j) * 16 - q * 4;
+                if (k == kTerms - 1 && left < 4)        // values past the adapter's rank are cleared
 #pragma unroll
-            for (int k = 0; k < kTerms; ++k) {
-                const uint4 h = f[k * 32];
+                    for (int t = 0; t < 4; ++t) {
+                        b[j][t].x &= left >= 2 ? ~0u : (left == 1 ? 0xFFFFu : 0u);
+                        b[j][t].y &= left == 3 ? 0xFFFFu : 0u;
+                    }
+                const uint4 h = frag[((c0 + j) * kTerms + k) * 32 + lane];
 #pragma unroll
                 for (int t = 0; t < 4; ++t) mma<BF>(acc[t], h, b[j][t].x, b[j][t].y);
             }
         }
         c0 += JT;
+        if (JT == 4 && chunks > 2 * JT && (c0 % (2 * JT) == 0 || c0 >= chunks))
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (c0 > 2 * JT) {
+                    const float4 v = total[t * 32];
+                    acc[t][0] += v.x; acc[t][1] += v.y; acc[t][2] += v.z; acc[t][3] += v.w;
+                }
+                if (c0 < chunks) total[t * 32] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+            }
         if (c0 < chunks) return;
         c0 = 0;
         const int n = u * 32 + q * 8;
