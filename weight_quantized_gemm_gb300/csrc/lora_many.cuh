@@ -589,13 +589,15 @@ cudaError_t launch_y(const LoraArgs& a, cudaStream_t s) {
     // Tiles of 128 rows where there are many rows; from how many on depends on the rank, as the few rows' kernel reads each
     // adapter once for every 16 rows, and from where on it needs a second round of blocks (4096 x 14336, us, few / many:
     // rank 16 2048 rows 42 / 51, 2900 rows 74 / 53; rank 32 1500 rows 46 / 45; rank 64 1024 rows 37 / 48, 1300 rows 65 / 49;
-    // rank 128 512 rows 45 / 47, 900 rows 60 / 49, and 2560 x 2560 768 rows 20 / 19, 1024 rows 21 / 19). The cluster's size
+    // rank 128 512 rows 45 / 47, 900 rows 60 / 49, and 2560 x 2560 768 rows 20 / 19, 1024 rows 21 / 19). These two widths are all
+    // that was measured, and just above the border the other kernel may be the quicker one (rank 16, 2400 rows 44 / 49: its
+    // second round of blocks begins between 2400 and 2900). The cluster's size
     // fills the SMs once (two blocks an SM, one at rank 128), with the number of tiles guessed from M and L, since the host
     // does not see the offsets: of 8192 rows, 4 blocks take 102 us, 8 117 and 2 142 (before L2 fetched 256 bytes).
     const int rank = a.R <= 16 ? 16 : (a.R <= 32 ? 32 : (a.R <= 64 ? 64 : (a.R <= 128 ? 128 : 256)));
     const int from = rank == 16 ? 2304 : (rank == 32 ? 1536 : (rank == 64 ? 1280 : (rank == 128 ? 768 : 256)));
     // Ranks above 128 (tiles of 64 rows, as H of more would not fit): from 256 rows on, where two terms stand for H
-    // (2560 x 2560 at rank 256, bf16: 256 rows 28 / 18, 512 rows 37 / 20, 4099 rows 101 / 53; f16 to float32 4099 rows 109 / 79).
+    // (2560 x 2560 at rank 256, bf16: 256 rows 28 / 18, 512 rows 37 / 20, 4099 rows 101 / 57; f16 to float32 4099 rows 109 / 79).
     // With three (bf16 to float32) what H leaves of shared memory is too little (6000 x 8192 x 8192 440 / 572).
     // An adapter's rows must fill tiles: 64 of them on average (4096 x 14336, rank 16, rows drawn at random, us: 2400 rows of 100
     // adapters 75 / 129, of 1000 228 / 1073; 2560 x 2560, rank 128, 1000 rows of 30 23 / 35), 16 at ranks above 128 (300 rows
