@@ -179,3 +179,12 @@ def test_waits_that_run_out_with_products_in_flight(M, R, y_dtype, limit_us, sta
     for _ in range(2):
         call()
         assert qg.qgemm_status() == 0 and torch.equal(c["Y"], want)
+
+
+# stages of 64 of K in each of 8 blocks: as many as the accumulators take without being emptied, one and some more, and several rounds
+@pytest.mark.parametrize("M,R,stages", [(300, 256, (8, 9, 10, 16, 17, 25)), (900, 128, (16, 17, 20, 33)), (1300, 64, (16, 17, 33)), (1600, 32, (32, 33, 66)),
+                                        (2304, 16, (64, 65, 130))])
+@pytest.mark.parametrize("dtype,y_dtype", [(qg.F16, qg.F32), (qg.BF16, qg.BF16), (qg.BF16, qg.F32)])
+def test_accumulators_that_are_emptied(M, R, stages, dtype, y_dtype):
+    for n in stages:
+        check(make(M, 64 * 8 * n, 40, 1, R, dtype, y_dtype, mixed(M, 1, n, none=0.02), seed=n, ragged=False))

@@ -13,8 +13,8 @@
 // RP: the ranks rounded up to a power of two; what lies past an adapter's rank is filled with zeros.
 //
 // There are few operations to a byte, so HBM's bytes are the floor: X, Y and Y again. 8192 x 4096 x 14336 at rank 16 in
-// bf16 takes 98 us (5.5 TB/s; a kernel that does nothing but add 1 to that Y in 128-byte runs takes 80 for its 470 MB,
-// and 67 MB of X come on top), at rank 64 125; 4099 x 2560 x 2560 at rank 128 28 us, with one block an SM, in which the first
+// bf16 takes 97 us (5.5 TB/s; a kernel that does nothing but add 1 to that Y in 128-byte runs takes 80 for its 470 MB,
+// and 67 MB of X come on top), at rank 64 120; 4099 x 2560 x 2560 at rank 128 28 us, with one block an SM, in which the first
 // product takes 6.6 (1260 cycles a stage of 32 KB), the join 4 and a turn 1.1. With 16x8x16 steps from registers, as in
 // lora.cuh, these took 109, 189 and 61 us: 12 instructions a value of Y, and the loads that feed
 // such steps. Waiting for all memory before each turn's products, and not for shared memory alone, made 102 us 151.
@@ -54,8 +54,9 @@ struct Many {
     // The first product's stages go to kSums accumulators in turn, each of which is emptied after kChain stages if there are
     // more: the tensor cores cut sums off instead of rounding them, and shorter chains lose less (f16 to float32, 6000 rows,
     // K = 8192: off by 5.0e-7 at rank 128 and 6.4e-7 at 256, a float32 product by 6.0e-7 and 1.6e-6; never emptied, with half as
-    // many accumulators, by 2.8e-6 and 1.0e-5, in the same time). They are emptied into registers, at ranks above 128, where these
-    // do not hold them (48 -> 53 us at 4099 x 2560 x 2560), into H's place. The second product's two accumulators take the place of these.
+    // many accumulators, by 2.8e-6 and 1.0e-5). They are emptied into registers, in which this costs no time, and at ranks above
+    // 128, for which there are too few of those, into H's place (4099 x 2560 x 2560 48 -> 52 us, with registers on the stack 53).
+    // The second product's two accumulators take the place of these.
     static constexpr int kTmem = RP <= 64 ? 256 : 512, kSums = kTmem / RP, kChain = 4;
     static constexpr bool kHeld = RP <= 128;        // in registers
     static_assert(kHeld || kRows * RP * 4 <= kH, "H's place");
